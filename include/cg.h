@@ -437,6 +437,141 @@ typedef struct {
  * slot length) zero. */
 cg_status cg_plan_levels(const cg_level_plan *p, uint32_t *level, cg_chunk_time *time, double *finish_s);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Sequences in a paged pool.  A context decoded into a paged pool
+ * (cg_decode_paged) is continued by many requests: each is a sequence with a
+ * row of blocks of its own, whose leading blocks it may share with others.
+ * The calls below keep those rows and attend over them.  They are this
+ * library's (the CacheGen pages stop at handing the decoded KV to the serving
+ * LLM: gptget.net page, method details).
+ *
+ * State, all caller-owned device memory:
+ *   tables u32 [n_slots][n_blocks]  block of tokens [i * block_tokens, ...) of
+ *                                   the sequence in a slot, or CG_NO_BLOCK; a
+ *                                   slot holds every block of its row, those
+ *                                   reserved past its length included
+ *   lens   u32 [n_slots]            tokens of the sequence (0: empty)
+ *   refs   u32 [n_pool_blocks]      how many table entries hold the block;
+ *                                   0: the block is free
+ * An empty slot has length 0 and CG_NO_BLOCK in its whole row.  The calls
+ * read the state as it is when the kernel runs, so they can be captured into
+ * a CUDA graph; every result is the same from run to run.
+ * Pool elements are 16-bit (fp16, or bf16 for cg_attend with CG_BF16):
+ * element (layer l, K/V kv, block b, row t, channel c) is
+ *     pool[l * layer_stride + kv * kv_stride + b * block_stride + t * token_stride + c]
+ * with a token's C channels contiguous; no two elements may share an address.
+ */
+#define CG_NO_BLOCK 0xFFFFFFFFu
+#define CG_NO_SLOT 0xFFFFFFFFu
+typedef struct {
+    uint16_t *pool;                                               /* device */
+    uint32_t L, C;                                                /* layers; channels of a token row */
+    uint32_t n_pool_blocks, block_tokens;                         /* block_tokens: a power of two */
+    uint64_t layer_stride, kv_stride, block_stride, token_stride; /* in 16-bit elements; token_stride >= C */
+    uint32_t *tables, *lens, *refs;                               /* device */
+    uint32_t n_slots, n_blocks;
+} cg_pages;
+
+/* Workspace bytes of the page calls on `p` (cg_pages_fork, cg_pages_compact).
+ * Host only.  CG_ERR_INVALID_ARG for zero sizes, block_tokens not a power of
+ * two, token_stride < C, or n_blocks * block_tokens above 2^31 (token
+ * positions are 32-bit). */
+cg_status cg_pages_ws_bytes(const cg_pages *p, size_t *ws_bytes);
+
+/* Copy n whole blocks, every layer, K and V: block dst_ids[i] of `to` gets
+ * block src_ids[i] of `from` (the same pool or another one with the same L, C
+ * and block_tokens; strides may differ).  src_ids / dst_ids: device [n].
+ * Tables, lengths and references are not touched.  An id outside its pool
+ * sets CG_ERR_RANGE in *dev_status and that pair is skipped.  A block that is
+ * a destination twice, or both a source and a destination, is left with
+ * unspecified values. */
+cg_status cg_pages_copy(const cg_pages *to, const cg_pages *from, const uint32_t *src_ids, const uint32_t *dst_ids,
+                        uint32_t n, uint32_t *dev_status, void *stream);
+
+/* Start n sequences.  Sequence i takes the empty slot child[i] and continues
+ * slot parent[i]: it shares the parent's full blocks (their references go up),
+ * gets a copy of the rows of the parent's last, partly filled block, and
+ * blocks for reserve[i] further tokens.  Its length is the parent's.  With
+ * parent[i] == CG_NO_SLOT it starts empty, with blocks for reserve[i] tokens.
+ * Fresh blocks are the lowest-numbered free ones, handed out in the order of
+ * i.  parent / child / reserve: device [n] (reserve may be null: 0).
+ * All or nothing: CG_ERR_RANGE in *dev_status and no change when a slot is
+ * out of range, a child is not empty or named twice, a row would need more
+ * than n_blocks entries, or too few blocks are free.  A parent's block
+ * outside the pool sets CG_ERR_CORRUPT; the child gets CG_NO_BLOCK there.
+ * ws: device, cg_pages_ws_bytes bytes, 256-byte aligned. */
+cg_status cg_pages_fork(const cg_pages *p, const uint32_t *parent, const uint32_t *child, const uint32_t *reserve,
+                        uint32_t n, void *ws, size_t ws_bytes, uint32_t *dev_status, void *stream);
+
+/* End the sequences in slots[n] (device): every block of the row loses one
+ * reference, the row becomes CG_NO_BLOCK and the length 0.  An empty slot, or
+ * one named twice, is ended once.  A slot out of range sets CG_ERR_RANGE and
+ * is skipped; a block outside the pool, or one that has no reference left,
+ * sets CG_ERR_CORRUPT and its count stays as it is. */
+cg_status cg_pages_free(const cg_pages *p, const uint32_t *slots, uint32_t n, uint32_t *dev_status, void *stream);
+
+/* Move the blocks in use to the front of the pool: with n_live blocks in use,
+ * the i-th block in use numbered n_live or above moves (every layer, K and V)
+ * to the i-th free block below n_live.  tables and refs are rewritten, and
+ * remap (device u32 [n_pool_blocks]) gets each block's new number, or
+ * CG_NO_BLOCK for a free one.  A table entry that names a free block or one
+ * outside the pool becomes CG_NO_BLOCK and sets CG_ERR_CORRUPT.
+ * ws: as for cg_pages_fork. */
+cg_status cg_pages_compact(const cg_pages *p, uint32_t *remap, void *ws, size_t ws_bytes, uint32_t *dev_status,
+                           void *stream);
+
+/*
+ * Attention of a batch of sequences over their own blocks and the blocks they
+ * share, whose keys and values are read once for the whole batch.
+ * Request r is the sequence in slot s = slots[r]; its last n_queries tokens
+ * are the query tokens (their K and V are already in the pool), so query
+ * token i of length-n sequence s sees tokens t < lim = max(0, n - n_queries +
+ * 1 + i).  Query head h reads KV head k = h / (n_q_heads / n_kv_heads),
+ * channels [k * head_dim, (k + 1) * head_dim) of a token row:
+ *     s_t = scale * <q, K_t>,  lse = ln sum_{t < lim} e^{s_t},
+ *     out = sum_{t < lim} e^{s_t - lse} V_t
+ * A query that sees nothing (an empty slot of a padded batch, n < n_queries)
+ * gets out = 0 and lse = -inf.  The first shared_blocks entries of every
+ * request's row are taken to equal those of slot shared_slot (as
+ * cg_pages_fork leaves them) and are read through that slot's row.  Rows of
+ * the pool at or past a sequence's length are never used, whatever they hold.
+ * Scores, softmax sums and outputs are accumulated in fp32; the weights
+ * e^{s_t - max} are rounded to the 16-bit type for the product with V.
+ * Device-side errors: CG_ERR_RANGE for a slot out of range, a length above
+ * n_blocks * block_tokens, a non-empty sequence whose first query token lies
+ * in the shared blocks (those requests are answered as empty), or a block
+ * outside the pool among a sequence's tokens; CG_ERR_TIMEOUT if a wait for a
+ * copy gave up.
+ */
+#define CG_FP16 0u
+#define CG_BF16 1u
+typedef struct {
+    const uint16_t *q;     /* device; element (r, i, h, d) at r * q_stride[0] + i * q_stride[1] + h * q_stride[2] + d */
+    uint16_t *out;         /* device; the same with out_stride */
+    float *lse;            /* device [n_requests][n_queries][n_q_heads], or NULL */
+    const uint32_t *slots; /* device [n_requests], or NULL: request r is slot r */
+    uint32_t dtype;        /* CG_FP16 or CG_BF16: q, out and the pool */
+    uint32_t n_requests, n_queries, n_q_heads, n_kv_heads, head_dim;
+    uint32_t layer, shared_slot, shared_blocks;
+    uint64_t q_stride[3], out_stride[3]; /* elements */
+    float scale;
+} cg_attention;
+
+/* Workspace bytes of cg_attend for `a` on `p` (host only; lengths do not
+ * enter).  CG_ERR_INVALID_ARG as for cg_attend. */
+cg_status cg_attend_ws_bytes(const cg_pages *p, const cg_attention *a, size_t *ws_bytes);
+
+/* Host checks (CG_ERR_INVALID_ARG): null pointers (lens and tables included),
+ * head_dim other than 64 or 128, n_kv_heads * head_dim != C, n_q_heads not a
+ * multiple of n_kv_heads, zero counts, layer >= L, shared_slot >= n_slots or
+ * shared_blocks > n_blocks (where shared_blocks > 0), a non-finite scale,
+ * block_tokens < 8, and a pool, q, out or stride that is not a multiple of 16
+ * bytes (blocks are fetched by TMA).  ws: device, 256-byte aligned;
+ * CG_ERR_RANGE if smaller than cg_attend_ws_bytes. */
+cg_status cg_attend(const cg_pages *p, const cg_attention *a, void *ws, size_t ws_bytes, uint32_t *dev_status,
+                    void *stream);
+
 #ifdef __cplusplus
 }
 #endif

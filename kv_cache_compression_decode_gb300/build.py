@@ -10,7 +10,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libcg.so")
-SOURCES = ["cg_encode.cu", "cg_decode.cu", "cg_host.cu"]
+SOURCES = ["cg_encode.cu", "cg_decode.cu", "cg_host.cu", "cg_pages.cu", "cg_attend.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 

@@ -78,6 +78,25 @@ class cg_paged_kv(ct.Structure):
                 ("kv_stride", ct.c_uint64), ("block_stride", ct.c_uint64), ("token_stride", ct.c_uint64)]
 
 
+CG_NO_BLOCK = CG_NO_SLOT = 0xFFFFFFFF
+CG_FP16, CG_BF16 = 0, 1
+
+
+class cg_pages(ct.Structure):
+    _fields_ = [("pool", ct.c_void_p), ("L", ct.c_uint32), ("C", ct.c_uint32), ("n_pool_blocks", ct.c_uint32),
+                ("block_tokens", ct.c_uint32), ("layer_stride", ct.c_uint64), ("kv_stride", ct.c_uint64),
+                ("block_stride", ct.c_uint64), ("token_stride", ct.c_uint64), ("tables", ct.c_void_p),
+                ("lens", ct.c_void_p), ("refs", ct.c_void_p), ("n_slots", ct.c_uint32), ("n_blocks", ct.c_uint32)]
+
+
+class cg_attention(ct.Structure):
+    _fields_ = [("q", ct.c_void_p), ("out", ct.c_void_p), ("lse", ct.c_void_p), ("slots", ct.c_void_p),
+                ("dtype", ct.c_uint32), ("n_requests", ct.c_uint32), ("n_queries", ct.c_uint32),
+                ("n_q_heads", ct.c_uint32), ("n_kv_heads", ct.c_uint32), ("head_dim", ct.c_uint32),
+                ("layer", ct.c_uint32), ("shared_slot", ct.c_uint32), ("shared_blocks", ct.c_uint32),
+                ("q_stride", ct.c_uint64 * 3), ("out_stride", ct.c_uint64 * 3), ("scale", ct.c_float)]
+
+
 ABLATION_FIELDS = ("values", "delta_bits_channel", "delta_bits_slice", "delta_bits_global", "escape_bits",
                    "anchor_bits_raw", "anchor_bits_channel")
 
@@ -98,7 +117,8 @@ EXPORTS = ("cg_status_string", "cg_status_from_flags", "cg_encode_bounds", "cg_e
            "cg_serialize",
            "cg_deserialize_header", "cg_deserialize", "cg_plan_levels", "cg_decode_paged",
            "cg_encode_levels_ws_bytes", "cg_encode_levels", "cg_ablation_ws_bytes", "cg_ablation",
-           "cg_cache_source", "cg_test_decode_timeout")
+           "cg_cache_source", "cg_test_decode_timeout", "cg_pages_ws_bytes", "cg_pages_copy", "cg_pages_fork",
+           "cg_pages_free", "cg_pages_compact", "cg_attend_ws_bytes", "cg_attend")
 
 _lib = None
 
@@ -131,6 +151,14 @@ def lib() -> ct.CDLL:
         L.cg_ablation.argtypes = [ct.POINTER(cg_config), P, P, ct.c_size_t, P, P, P]
         L.cg_encode_levels.argtypes = [ct.POINTER(cg_config), U32, P, P, P, ct.c_size_t, P, P, P, P]
         L.cg_decode_paged.argtypes = [ct.POINTER(cg_config), ct.POINTER(cg_encoded), ct.POINTER(cg_paged_kv), P, P]
+        PG, SZ = ct.POINTER(cg_pages), ct.POINTER(ct.c_size_t)
+        L.cg_pages_ws_bytes.argtypes = [PG, SZ]
+        L.cg_pages_copy.argtypes = [PG, PG, P, P, U32, P, P]
+        L.cg_pages_fork.argtypes = [PG, P, P, P, U32, P, ct.c_size_t, P, P]
+        L.cg_pages_free.argtypes = [PG, P, U32, P, P]
+        L.cg_pages_compact.argtypes = [PG, P, P, ct.c_size_t, P, P]
+        L.cg_attend_ws_bytes.argtypes = [PG, ct.POINTER(cg_attention), SZ]
+        L.cg_attend.argtypes = [PG, ct.POINTER(cg_attention), P, ct.c_size_t, P, P]
         L.cg_cache_source.argtypes = [P, ct.POINTER(ct.c_int), ct.POINTER(ct.c_void_p)]
         for name in EXPORTS:
             if name not in ("cg_status_string",):

@@ -1,0 +1,652 @@
+// cg_attend.cu -- attention of a batch of sequences in a paged pool whose
+// leading blocks are shared (sm_103a).
+//
+// The softmax over a sequence splits at the end of the shared blocks: with
+// m the largest score of a part, l = sum e^{s - m} and O = sum e^{s - m} V,
+// parts join as m = max m_j, l = sum l_j e^{m_j - m}, O likewise, out = O / l.
+// The shared part has the same keys for every request, so the query rows of
+// all requests that use one KV head form one matrix against it, and its K
+// and V are read once for the batch.  Every part may be split along its
+// tokens again; the pieces go to the workspace and k_merge joins them in a
+// fixed order.  Scores are kept in log2 units (scale * log2 e folded in).
+#include <cuda.h>
+#include <math.h>
+
+#include "cg_async.cuh"
+
+namespace cg {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr uint32_t kTok = 64;       // tokens of a tile
+constexpr uint32_t kRows = 16;      // query rows of a row tile
+constexpr uint32_t kStages = 3;     // tiles in flight
+constexpr uint32_t kConsumers = 4;  // warps that compute; one more fetches
+constexpr uint32_t kThreads = (kConsumers + 1) * 32;
+
+struct Args {
+    const uint16_t *q;
+    uint16_t *out;
+    float *lse;
+    const uint32_t *slots, *tables, *lens;
+    uint32_t n_slots, n_blocks, n_pool, bshift;
+    uint32_t R, nq, g, Hkv;  // requests, query tokens, query heads per KV head, KV heads
+    uint32_t P, shared_slot; // shared tokens
+    uint32_t rt;             // row tiles of a request
+    uint32_t npt;            // row tiles of the whole batch over the shared tokens
+    uint32_t n_cta;          // blocks of k_rows
+    uint64_t qs[3], os[3];
+    float scale2;            // |scale| * log2 e
+    uint32_t flip;           // sign bits to flip in q (scale < 0)
+    uint32_t *status;
+    // workspace
+    uint64_t *cum;           // [R + 1] first tile of request r; [R]: tiles of all requests
+    float *part_o;           // [piece][piece_rows][D]
+    float2 *part_ml;         // [piece][piece_rows] (m, l)
+    uint32_t piece_rows;
+};
+
+// Tokens of request r's sequence; 0 for an empty slot and for a request that
+// is refused (*bad).
+__device__ __forceinline__ uint32_t tokens_of(const Args &a, uint32_t r, bool *bad) {
+    const uint32_t s = a.slots ? a.slots[r] : r;
+    if (s >= a.n_slots) {
+        *bad = true;
+        return 0;
+    }
+    const uint32_t n = a.lens[s];
+    // the first query token, n - nq, has to lie past the shared tokens
+    if (n != 0 && (n > ((uint64_t)a.n_blocks << a.bshift) || (a.P && (uint64_t)n + 1 < (uint64_t)a.P + a.nq))) {
+        *bad = true;
+        return 0;
+    }
+    return n;
+}
+
+__device__ __forceinline__ uint32_t tiles_of(uint32_t tokens) { return (tokens + kTok - 1) / kTok; }
+
+// Work list: for each request its row tiles x KV heads ("items"), each
+// ceil(own tokens / 64) tiles long, then the items of the shared part.  Block
+// c of n takes tiles [c T / n, (c + 1) T / n) of the whole list, so every
+// block has the same share whatever the lengths are (n is cut to T, so that
+// no block between two others is left without a tile).  A block's run of tiles
+// of one item is a piece; its slot c + item is unique, since along the list
+// each new piece has a larger block or a larger item.
+struct Piece {
+    uint32_t r;        // request; R: the shared part
+    uint32_t item;     // number of the item
+    uint32_t rtile, head;
+    uint32_t tile0, n; // tiles of the item
+    uint32_t of;       // tiles the item has
+    uint32_t len;      // tokens in the sequence (request) or P
+};
+
+struct Walk {
+    uint64_t t, end, base;  // position, end of this block's share, first tile of request r
+    uint32_t r;
+};
+
+__device__ __forceinline__ bool next_piece(const Args &a, Walk &w, Piece &p) {
+    if (w.t >= w.end) return false;
+    bool bad = false;
+    uint32_t nt = 0, len = 0;
+    while (w.r < a.R) {
+        len = tokens_of(a, w.r, &bad);
+        nt = len > a.P ? tiles_of(len - a.P) : 0;
+        const uint64_t all = (uint64_t)nt * a.rt * a.Hkv;
+        if (w.t < w.base + all) break;
+        w.base += all;
+        w.r++;
+    }
+    p.r = w.r;
+    if (w.r == a.R) {
+        len = a.P;
+        nt = tiles_of(a.P);
+    }
+    const uint64_t at = w.t - w.base;
+    const uint32_t local = (uint32_t)(at / nt);
+    p.item = (uint32_t)min(w.r, a.R) * a.rt * a.Hkv + local;
+    p.rtile = local / a.Hkv;
+    p.head = local - p.rtile * a.Hkv;
+    p.tile0 = (uint32_t)(at - (uint64_t)local * nt);
+    p.n = (uint32_t)min((uint64_t)(nt - p.tile0), w.end - w.t);
+    p.of = nt;
+    p.len = len;
+    w.t += p.n;
+    return true;
+}
+
+// Query row `row` of an item: request, query token, query head.
+struct Row {
+    uint32_t r, i, h;
+    bool valid;
+};
+__device__ __forceinline__ Row row_of(const Args &a, const Piece &p, uint32_t row) {
+    Row o;
+    const uint32_t per = a.nq * a.g;
+    uint32_t x = p.rtile * kRows + row;
+    if (p.r == a.R) {
+        o.r = x / per;
+        x -= o.r * per;
+        o.valid = o.r < a.R;
+    } else {
+        o.r = p.r;
+        o.valid = x < per;
+    }
+    o.i = x / a.g;
+    o.h = p.head * a.g + (x - o.i * a.g);
+    return o;
+}
+
+template <uint32_t D> struct Smem {
+    static constexpr uint32_t kHalf = kTok * 128;           // 64 channels of a tile, 128-byte swizzled rows
+    static constexpr uint32_t kTile = kTok * D * 2;         // K or V of a tile
+    static constexpr uint32_t kStage = 2 * kTile;
+    static constexpr uint32_t kBufStride = D + 4;
+    static constexpr uint32_t oBuf = kStages * kStage;      // [16][D + 4] fp32
+    static constexpr uint32_t oMl = oBuf + kRows * kBufStride * 4;
+    static constexpr uint32_t oBar = oMl + kConsumers * kRows * 8;
+    static constexpr uint32_t oMisc = oBar + 2 * kStages * 8;
+    static constexpr uint32_t kBytes = oMisc + 64 + 1024;   // and slack to align the tiles to 1 KiB
+};
+
+// Query rows in tiles of 16 against their tokens, 64 at a time: four warps
+// take 16 tokens each with a softmax state of their own and join at the end
+// of the piece; a fifth warp fetches the tiles, three in flight.
+template <class T, uint32_t D>
+__global__ void __launch_bounds__(kThreads, 2) k_rows(const __grid_constant__ CUtensorMap map, const Args a) {
+    using S = Smem<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (s_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sm = s_addr(smem);
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+    const uint32_t full = sm + S::oBar, empty = full + kStages * 8;
+    uint64_t *misc = reinterpret_cast<uint64_t *>(smem + S::oMisc);
+
+    if (tid == 0) {
+        for (uint32_t k = 0; k < kStages; k++) {
+            bar_init(full + 8 * k, 1);
+            bar_init(empty + 8 * k, kConsumers);
+        }
+        fence_bar_init();
+    }
+    // This block's share of the work list: every thread sums its own run of requests.
+    const uint32_t per = (a.R + kThreads - 1) / kThreads;
+    const uint32_t r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
+    uint64_t mine = 0;
+    bool bad = false;
+    for (uint32_t r = r0; r < r1; r++) {
+        const uint32_t n = tokens_of(a, r, &bad);
+        mine += (uint64_t)(n > a.P ? tiles_of(n - a.P) : 0) * a.rt * a.Hkv;
+    }
+    if (bad && blockIdx.x == 0) flag(a.status, CG_ERR_RANGE);
+    uint64_t inc = mine;
+    for (uint32_t d = 1; d < 32; d <<= 1) {
+        const uint64_t y = __shfl_up_sync(kFull, inc, d);
+        if (lane >= d) inc += y;
+    }
+    if (lane == 31) misc[warp] = inc;
+    __syncthreads();
+    uint64_t before = inc - mine, own = 0;
+    for (uint32_t k = 0; k <= kConsumers; k++) {
+        if (k < warp) before += misc[k];
+        own += misc[k];
+    }
+    const uint64_t total = own + (uint64_t)a.npt * a.Hkv * tiles_of(a.P);
+    if (blockIdx.x == 0) {
+        uint64_t at = before;
+        bool b = false;
+        for (uint32_t r = r0; r < r1; r++) {
+            a.cum[r] = at;
+            const uint32_t n = tokens_of(a, r, &b);
+            at += (uint64_t)(n > a.P ? tiles_of(n - a.P) : 0) * a.rt * a.Hkv;
+        }
+        if (tid == 0) a.cum[a.R] = own;
+    }
+    Walk w;
+    const uint64_t n_cta = min((uint64_t)a.n_cta, total);  // at least a tile each
+    w.t = blockIdx.x < n_cta ? blockIdx.x * total / n_cta : total;
+    w.end = blockIdx.x < n_cta ? (blockIdx.x + 1ull) * total / n_cta : total;
+    if (tid == 0) {
+        misc[5] = own;
+        misc[6] = a.R;
+    }
+    __syncthreads();
+    if (mine && w.t >= before && w.t < before + mine) {  // one thread at most
+        misc[5] = before;
+        misc[6] = r0;
+    }
+    __syncthreads();
+    w.base = misc[5];
+    w.r = (uint32_t)misc[6];
+
+    Piece p;
+    uint32_t it = 0;  // tiles so far: stage it % kStages, parity it / kStages
+    if (warp == kConsumers) {
+        const uint32_t rows_log = min(a.bshift, 6u), rows = 1u << rows_log, boxes = kTok >> rows_log;
+        bool ok = true;
+        while (ok && next_piece(a, w, p)) {
+            const bool shared = p.r == a.R;
+            const uint32_t slot = shared ? a.shared_slot : a.slots ? a.slots[p.r] : p.r;
+            const uint32_t *row = a.tables + (uint64_t)slot * a.n_blocks;
+            const uint32_t first = shared ? 0u : a.P;
+            for (uint32_t k = 0; k < p.n; k++, it++) {
+                const uint32_t st = it % kStages;
+                // the block of this lane's box; a box past the sequence lies outside the map and reads zeros
+                const uint32_t pos = first + (p.tile0 + k) * kTok + lane * rows;
+                uint32_t id = a.n_pool;
+                if (lane < boxes && pos < p.len) {
+                    id = row[pos >> a.bshift];
+                    if (id >= a.n_pool) {
+                        id = a.n_pool;
+                        flag(a.status, CG_ERR_RANGE);
+                    }
+                }
+                if (it >= kStages) ok = bar_wait(empty + 8 * st, (it / kStages - 1) & 1u);
+                ok = __all_sync(kFull, ok);
+                if (!ok) break;
+                if (lane == 0) bar_expect(full + 8 * st, S::kStage);
+                __syncwarp();
+                if (lane < boxes) {
+                    const uint32_t dst = sm + st * S::kStage + lane * rows * 128;
+                    const int c = (int)(p.head * D), in = (int)(pos & ((1u << a.bshift) - 1u));
+#pragma unroll
+                    for (uint32_t kv = 0; kv < 2; kv++)
+#pragma unroll
+                        for (uint32_t h = 0; h < D / 64; h++)
+                            tma_box(dst + kv * S::kTile + h * S::kHalf, &map, c + 64 * (int)h, in, (int)id, (int)kv,
+                                    full + 8 * st);
+                }
+            }
+        }
+        if (!ok) {  // wait for the copies in flight before leaving
+            for (uint32_t k = it > kStages ? it - kStages : 0; k < it; k++)
+                bar_wait(full + 8 * (k % kStages), (k / kStages) & 1u);
+            if (lane == 0) flag_why(a.status, CG_ERR_TIMEOUT, kWhyWait);
+        }
+        return;
+    }
+
+    float *buf = reinterpret_cast<float *>(smem + S::oBuf);
+    float2 *ml = reinterpret_cast<float2 *>(smem + S::oMl);
+    const uint32_t qd = lane & 3u, rw = lane >> 2;
+    bool ok = true;
+    while (next_piece(a, w, p)) {
+        const bool shared = p.r == a.R;
+        const uint32_t own_tokens = shared ? a.P : p.len - a.P;
+        // query fragments, and how many of the item's tokens each of this lane's two rows sees
+        uint32_t q[D / 16][4];
+        uint32_t lim[2], least = own_tokens;
+        for (uint32_t e = 0; e < 2; e++) {
+            const Row o = row_of(a, p, rw + 8 * e);
+            const uint16_t *src = a.q + o.r * a.qs[0] + o.i * a.qs[1] + o.h * a.qs[2] + 2 * qd;
+            for (uint32_t k = 0; k < D / 16; k++) {
+                q[k][e] = o.valid ? *reinterpret_cast<const uint32_t *>(src + 16 * k) ^ a.flip : 0u;
+                q[k][e + 2] = o.valid ? *reinterpret_cast<const uint32_t *>(src + 16 * k + 8) ^ a.flip : 0u;
+            }
+            lim[e] = own_tokens;
+            if (!shared) {
+                const uint32_t sees = p.len + 1 + o.i;  // + 1 - nq below
+                lim[e] = sees > a.nq + a.P ? min(sees - a.nq - a.P, own_tokens) : 0u;
+                least = min(least, p.len + 1 > a.nq + a.P ? p.len + 1 - a.nq - a.P : 0u);
+            }
+        }
+        float o[D / 8][4];
+#pragma unroll
+        for (uint32_t d = 0; d < D / 8; d++)
+#pragma unroll
+            for (uint32_t k = 0; k < 4; k++) o[d][k] = 0.f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+        for (uint32_t k = 0; k < p.n; k++, it++) {
+            const uint32_t st = it % kStages;
+            if (ok) ok = bar_wait(full + 8 * st, (it / kStages) & 1u);
+            if (!__all_sync(kFull, ok)) {
+                ok = false;
+                continue;
+            }
+            const uint32_t tok = (p.tile0 + k) * kTok + 16 * warp;  // this warp's 16 tokens of the item
+            if (tok < own_tokens) {
+                const uint32_t kb = sm + st * S::kStage, vb = kb + S::kTile;
+                const bool tail = tok + 16 > own_tokens;
+                if (tail) {  // rows past the sequence hold anything: V's must not meet the weight 0
+                    const uint32_t r = 16 * warp + (lane >> 1);
+                    if (tok + (lane >> 1) >= own_tokens)
+                        for (uint32_t b = 0; b < D * 2; b += 32) {
+                            const uint32_t x = b + 16 * (lane & 1u);
+                            *reinterpret_cast<uint4 *>(smem + st * S::kStage + S::kTile + (x >> 7) * S::kHalf + r * 128 +
+                                                       (x & 127u)) = make_uint4(0, 0, 0, 0);
+                        }
+                    __syncwarp();
+                }
+                float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                {
+                    const uint32_t r = 16 * warp + (lane >> 4) * 8 + (lane & 7u);
+                    const uint32_t rb = kb + r * 128, x = r & 7u, hi = (lane >> 3) & 1u;
+#pragma unroll
+                    for (uint32_t c = 0; c < D / 16; c++) {
+                        uint32_t b[4];
+                        ldsm4(b, rb + (c >> 2) * S::kHalf + ((((c & 3u) * 2 + hi) ^ x) << 4));
+                        Half<T>::mma(s[0], q[c], b[0], b[1]);
+                        Half<T>::mma(s[1], q[c], b[2], b[3]);
+                    }
+                }
+                const bool mask = tok + 16 > least;
+                float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (uint32_t n = 0; n < 2; n++)
+#pragma unroll
+                    for (uint32_t j = 0; j < 4; j++) {
+                        const uint32_t e = j >> 1, t = tok + n * 8 + 2 * qd + (j & 1u);
+                        s[n][j] *= a.scale2;
+                        if (mask && t >= lim[e]) s[n][j] = -INFINITY;
+                        mx[e] = fmaxf(mx[e], s[n][j]);
+                    }
+                float c[2];
+                bool moved = false;
+#pragma unroll
+                for (uint32_t e = 0; e < 2; e++) {
+                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(kFull, mx[e], 1));
+                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(kFull, mx[e], 2));
+                    const float nm = fmaxf(m[e], mx[e]);
+                    c[e] = m[e] == nm ? 1.f : ex2(m[e] - nm);
+                    moved |= m[e] != nm;
+                    m[e] = nm;
+                }
+                if (__any_sync(kFull, moved)) {
+#pragma unroll
+                    for (uint32_t d = 0; d < D / 8; d++) {
+                        o[d][0] *= c[0];
+                        o[d][1] *= c[0];
+                        o[d][2] *= c[1];
+                        o[d][3] *= c[1];
+                    }
+                    l[0] *= c[0];
+                    l[1] *= c[1];
+                }
+                const float z[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+                for (uint32_t n = 0; n < 2; n++)
+#pragma unroll
+                    for (uint32_t j = 0; j < 4; j++) {
+                        s[n][j] = ex2(s[n][j] - z[j >> 1]);
+                        l[j >> 1] += s[n][j];
+                    }
+                const uint32_t pa[4] = {Half<T>::pack(s[0][0], s[0][1]), Half<T>::pack(s[0][2], s[0][3]),
+                                        Half<T>::pack(s[1][0], s[1][1]), Half<T>::pack(s[1][2], s[1][3])};
+                const uint32_t r = 16 * warp + ((lane >> 3) & 1u) * 8 + (lane & 7u);
+                const uint32_t rb = vb + r * 128, x = r & 7u, hi = lane >> 4;
+#pragma unroll
+                for (uint32_t d = 0; d < D / 16; d++) {
+                    uint32_t b[4];
+                    ldsm4_t(b, rb + (d >> 2) * S::kHalf + ((((d & 3u) * 2 + hi) ^ x) << 4));
+                    Half<T>::mma(o[2 * d], pa, b[0], b[1]);
+                    Half<T>::mma(o[2 * d + 1], pa, b[2], b[3]);
+                }
+                if (tail) fence_async();  // the zeros are ordered before the copy that reuses the stage
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(empty + 8 * st);
+        }
+
+        // join the four warps: states, then the outputs one warp after another
+#pragma unroll
+        for (uint32_t e = 0; e < 2; e++) {
+            l[e] += __shfl_xor_sync(kFull, l[e], 1);
+            l[e] += __shfl_xor_sync(kFull, l[e], 2);
+            if (qd == 0) ml[warp * kRows + rw + 8 * e] = make_float2(m[e], l[e]);
+        }
+        group_sync(1, kConsumers * 32);
+        float f[2];
+#pragma unroll
+        for (uint32_t e = 0; e < 2; e++) {
+            float mm = -INFINITY;
+            for (uint32_t k = 0; k < kConsumers; k++) mm = fmaxf(mm, ml[k * kRows + rw + 8 * e].x);
+            f[e] = m[e] == mm ? 1.f : ex2(m[e] - mm);
+        }
+        for (uint32_t k = 0; k < kConsumers; k++) {
+            if (warp == k) {
+#pragma unroll
+                for (uint32_t d = 0; d < D / 8; d++)
+#pragma unroll
+                    for (uint32_t e = 0; e < 2; e++) {
+                        float2 *at = reinterpret_cast<float2 *>(buf + (rw + 8 * e) * S::kBufStride + d * 8 + 2 * qd);
+                        float2 v = k ? *at : make_float2(0.f, 0.f);
+                        v.x += o[d][2 * e] * f[e];
+                        v.y += o[d][2 * e + 1] * f[e];
+                        *at = v;
+                    }
+            }
+            group_sync(1, kConsumers * 32);
+        }
+        // eight threads a row
+        const uint32_t row = tid >> 3, part = tid & 7u;
+        const Row ro = row_of(a, p, row);
+        if (ro.valid) {
+            float mm = -INFINITY, ll = 0.f;
+            for (uint32_t k = 0; k < kConsumers; k++) mm = fmaxf(mm, ml[k * kRows + row].x);
+            for (uint32_t k = 0; k < kConsumers; k++) {
+                const float2 v = ml[k * kRows + row];
+                ll += v.y * (v.x == mm ? 1.f : ex2(v.x - mm));
+            }
+            const float *src = buf + row * S::kBufStride + part * (D / 8);
+            if (a.P == 0 && p.n == p.of) {  // the whole sequence: the answer
+                const float inv = ll == 0.f ? 0.f : 1.f / ll;
+                uint16_t *dst = a.out + ro.r * a.os[0] + ro.i * a.os[1] + ro.h * a.os[2] + part * (D / 8);
+                for (uint32_t d = 0; d < D / 8; d += 2)
+                    *reinterpret_cast<uint32_t *>(dst + d) = Half<T>::pack(src[d] * inv, src[d + 1] * inv);
+                if (a.lse && part == 0)
+                    a.lse[((uint64_t)ro.r * a.nq + ro.i) * (a.g * a.Hkv) + ro.h] =
+                        ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+            } else {
+                const uint64_t at = ((uint64_t)blockIdx.x + p.item) * a.piece_rows + row;
+                float4 *dst = reinterpret_cast<float4 *>(a.part_o + at * D + part * (D / 8));
+                for (uint32_t d = 0; d < D / 32; d++) dst[d] = *reinterpret_cast<const float4 *>(src + 4 * d);
+                if (part == 0) a.part_ml[at] = make_float2(mm, ll);
+            }
+        }
+        group_sync(1, kConsumers * 32);
+    }
+    if (!ok && lane == 0) flag_why(a.status, CG_ERR_TIMEOUT, kWhyWait);
+}
+
+// Joins the pieces of each query row, a warp per row.
+template <class T, uint32_t D>
+__global__ void __launch_bounds__(256) k_merge(const Args a) {
+    const uint32_t lane = threadIdx.x & 31u;
+    const uint32_t Hq = a.g * a.Hkv;
+    const uint64_t row = ((uint64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
+    if (row >= (uint64_t)a.R * a.nq * Hq) return;
+    const uint32_t h = (uint32_t)(row % Hq), ri = (uint32_t)(row / Hq), i = ri % a.nq, r = ri / a.nq;
+    const uint32_t head = h / a.g, x = i * a.g + h % a.g;
+    constexpr uint32_t kPer = D / 32;
+    bool bad = false;
+    const uint32_t len = tokens_of(a, r, &bad);
+    const uint64_t total = a.cum[a.R] + (uint64_t)a.npt * a.Hkv * tiles_of(a.P);
+    const uint64_t n_cta = min((uint64_t)a.n_cta, total);
+    float m = -INFINITY, l = 0.f, o[kPer];
+    for (uint32_t k = 0; k < kPer; k++) o[k] = 0.f;
+    // the pieces of one item: its tiles [t0, t0 + nt) are spread over blocks c0..c1
+    auto join = [&](uint64_t t0, uint32_t nt, uint32_t item, uint32_t local) {
+        const uint64_t c0 = ((t0 + 1) * n_cta - 1) / total, c1 = ((t0 + nt) * n_cta - 1) / total;
+        for (uint64_t c = c0; c <= c1; c++) {
+            const uint64_t at = (c + item) * a.piece_rows + local;
+            const float2 v = a.part_ml[at];
+            const float *src = a.part_o + at * D + lane * kPer;
+            float y[kPer];
+            for (uint32_t k = 0; k < kPer; k++) y[k] = src[k];
+            if (v.x == -INFINITY && v.y == 0.f) continue;  // a piece the row sees nothing of
+            const float nm = fmaxf(m, v.x);
+            const float f = m == nm ? 1.f : ex2(m - nm), e = v.x == nm ? 1.f : ex2(v.x - nm);
+            m = nm;
+            l = l * f + v.y * e;
+            for (uint32_t k = 0; k < kPer; k++) o[k] = o[k] * f + y[k] * e;
+        }
+        return c0 == c1;
+    };
+    if (len) {
+        const uint32_t nt = len > a.P ? tiles_of(len - a.P) : 0;
+        if (a.npt) {
+            const uint32_t xp = r * a.nq * a.g + x, item = (xp / kRows) * a.Hkv + head;
+            const uint32_t ntp = tiles_of(a.P);
+            join(a.cum[a.R] + (uint64_t)item * ntp, ntp, a.R * a.rt * a.Hkv + item, xp % kRows);
+        }
+        if (nt) {
+            const uint32_t item = (x / kRows) * a.Hkv + head;
+            const bool one = join(a.cum[r] + (uint64_t)item * nt, nt, r * a.rt * a.Hkv + item, x % kRows);
+            if (one && a.P == 0) return;  // k_rows has written the answer
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint16_t *dst = a.out + r * a.os[0] + i * a.os[1] + h * a.os[2] + lane * kPer;
+    for (uint32_t k = 0; k < kPer; k += 2)
+        *reinterpret_cast<uint32_t *>(dst + k) = Half<T>::pack(o[k] * inv, o[k + 1] * inv);
+    if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+bool misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1u)) != 0; }
+
+struct Plan {
+    uint32_t g, rt, npt, piece_rows;
+    uint64_t items, pieces, cum_bytes, o_bytes, bytes;
+};
+
+constexpr uint32_t kMaxCtas = 512;  // bound of the grid that the workspace is sized for
+
+bool make_plan(const cg_pages *p, const cg_attention *a, Plan *o) {
+    if (!p || !a || !p->pool || !p->tables || !p->lens || !a->q || !a->out) return false;
+    if (!p->L || !p->C || !p->n_pool_blocks || p->n_pool_blocks > (1u << 31) - 1u || !p->n_slots || !p->n_blocks)
+        return false;
+    const uint32_t bt = p->block_tokens;
+    if (bt < 8 || (bt & (bt - 1u)) || (uint64_t)p->n_blocks * bt > (1ull << 31) - 64u || p->token_stride < p->C)
+        return false;
+    if (a->dtype > CG_BF16 || !a->n_requests || !a->n_queries || !a->n_q_heads || !a->n_kv_heads) return false;
+    if (a->head_dim != 64 && a->head_dim != 128) return false;
+    if ((uint64_t)a->n_kv_heads * a->head_dim != p->C || a->n_q_heads % a->n_kv_heads) return false;
+    if (a->layer >= p->L || a->shared_blocks > p->n_blocks) return false;
+    if (a->shared_blocks && a->shared_slot >= p->n_slots) return false;
+    if (!isfinite(a->scale)) return false;
+    const uint64_t strides = p->layer_stride | p->kv_stride | p->block_stride | p->token_stride | a->q_stride[0] |
+                             a->q_stride[1] | a->q_stride[2] | a->out_stride[0] | a->out_stride[1] | a->out_stride[2];
+    if (strides % 8 || misaligned(p->pool, 16) || misaligned(a->q, 16) || misaligned(a->out, 16)) return false;
+    if (misaligned(p->tables, 4) || misaligned(p->lens, 4) || misaligned(a->lse, 4) || misaligned(a->slots, 4))
+        return false;
+    // a tensor map's strides have 40 bits, and its rows and blocks may not be empty strides
+    if ((p->kv_stride | p->block_stride | p->token_stride) >> 39 || !p->kv_stride || !p->block_stride) return false;
+    o->g = a->n_q_heads / a->n_kv_heads;
+    const uint64_t per = (uint64_t)a->n_queries * o->g, all = per * a->n_requests;
+    if (all * a->n_kv_heads > (1ull << 31)) return false;
+    o->rt = (uint32_t)((per + kRows - 1) / kRows);
+    o->npt = a->shared_blocks ? (uint32_t)((all + kRows - 1) / kRows) : 0;
+    o->piece_rows = o->npt ? (uint32_t)(all < kRows ? all : kRows) : (uint32_t)(per < kRows ? per : kRows);
+    o->items = ((uint64_t)a->n_requests * o->rt + o->npt) * a->n_kv_heads;
+    if (o->items > (1ull << 31)) return false;
+    o->pieces = o->items + kMaxCtas;
+    o->cum_bytes = round_up((a->n_requests + 1ull) * 8, 256);
+    o->o_bytes = round_up(o->pieces * o->piece_rows * a->head_dim * 4, 256);
+    o->bytes = o->cum_bytes + o->o_bytes + round_up(o->pieces * o->piece_rows * 8, 256);
+    return true;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+    static const EncodeTiled fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeTiled>(f);
+    }();
+    return fn;
+}
+
+// The layer's K and V as (channel, row, block, K/V), in boxes of 64 channels x `rows` rows.
+bool make_map(const cg_pages *p, const cg_attention *a, uint32_t rows, CUtensorMap *map) {
+    const EncodeTiled enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {p->C, p->block_tokens, p->n_pool_blocks, 2};
+    const cuuint64_t strides[3] = {2 * p->token_stride, 2 * p->block_stride, 2 * p->kv_stride};
+    const cuuint32_t box[4] = {64, rows, 1, 1}, step[4] = {1, 1, 1, 1};
+    return enc(map, a->dtype == CG_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+               p->pool + a->layer * p->layer_stride, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class T, uint32_t D>
+cudaError_t launch(const CUtensorMap &map, Args &a, int sms, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(k_rows<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    a.n_cta = (uint32_t)sms * 2u < kMaxCtas ? (uint32_t)sms * 2u : kMaxCtas;
+    k_rows<T, D><<<a.n_cta, kThreads, Smem<D>::kBytes, s>>>(map, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const uint64_t rows = (uint64_t)a.R * a.nq * a.g * a.Hkv;
+    k_merge<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace cg
+
+using namespace cg;
+
+extern "C" cg_status cg_attend_ws_bytes(const cg_pages *p, const cg_attention *a, size_t *ws_bytes) {
+    Plan pl;
+    if (!ws_bytes || !make_plan(p, a, &pl)) return CG_ERR_INVALID_ARG;
+    *ws_bytes = pl.bytes;
+    return CG_OK;
+}
+
+extern "C" cg_status cg_attend(const cg_pages *p, const cg_attention *at, void *ws, size_t ws_bytes,
+                               uint32_t *dev_status, void *stream) {
+    Plan pl;
+    if (!make_plan(p, at, &pl) || !ws || misaligned(ws, 256)) return CG_ERR_INVALID_ARG;
+    if (ws_bytes < pl.bytes) return CG_ERR_RANGE;
+    int dev = 0, sms = 0;
+    CG_CUDA_TRY(cudaGetDevice(&dev));
+    CG_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    const uint32_t bshift = (uint32_t)__builtin_ctz(p->block_tokens);
+    CUtensorMap map;
+    if (!make_map(p, at, p->block_tokens < kTok ? p->block_tokens : kTok, &map)) return CG_ERR_CUDA;
+    Args a{};
+    a.q = at->q;
+    a.out = at->out;
+    a.lse = at->lse;
+    a.slots = at->slots;
+    a.tables = p->tables;
+    a.lens = p->lens;
+    a.n_slots = p->n_slots;
+    a.n_blocks = p->n_blocks;
+    a.n_pool = p->n_pool_blocks;
+    a.bshift = bshift;
+    a.R = at->n_requests;
+    a.nq = at->n_queries;
+    a.g = pl.g;
+    a.Hkv = at->n_kv_heads;
+    a.P = at->shared_blocks << bshift;
+    a.shared_slot = at->shared_slot;
+    a.rt = pl.rt;
+    a.npt = pl.npt;
+    for (int k = 0; k < 3; k++) {
+        a.qs[k] = at->q_stride[k];
+        a.os[k] = at->out_stride[k];
+    }
+    a.scale2 = fabsf(at->scale) * kLog2e;
+    a.flip = at->scale < 0.f ? 0x80008000u : 0u;
+    a.status = dev_status;
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    a.cum = reinterpret_cast<uint64_t *>(w);
+    a.part_o = reinterpret_cast<float *>(w + pl.cum_bytes);
+    a.part_ml = reinterpret_cast<float2 *>(w + pl.cum_bytes + pl.o_bytes);
+    a.piece_rows = pl.piece_rows;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool fp16 = at->dtype == CG_FP16;
+    if (at->head_dim == 128) CG_CUDA_TRY((fp16 ? launch<__half, 128>(map, a, sms, s) : launch<__nv_bfloat16, 128>(map, a, sms, s)));
+    else CG_CUDA_TRY((fp16 ? launch<__half, 64>(map, a, sms, s) : launch<__nv_bfloat16, 64>(map, a, sms, s)));
+    return CG_OK;
+}
