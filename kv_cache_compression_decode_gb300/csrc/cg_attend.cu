@@ -33,7 +33,10 @@ struct Args {
     uint32_t R, nq, g, Hkv;  // requests, query tokens, query heads per KV head, KV heads
     uint32_t P, shared_slot; // shared tokens
     uint32_t rt;             // row tiles of a request
-    uint32_t npt;            // row tiles of the whole batch over the shared tokens
+    uint32_t npt;            // row tiles of the whole batch over the shared tokens in k_rows (0: k_shared has them)
+    uint32_t pairs;          // k_shared: pairs of 128-row tiles of the whole batch (0: k_rows has the shared part)
+    uint32_t one;            // k_shared: the batch fits one 128-row tile
+    uint32_t n_tc;           // blocks of k_shared
     uint32_t n_cta;          // blocks of k_rows
     uint64_t qs[3], os[3];
     float scale2;            // |scale| * log2 e
@@ -44,6 +47,8 @@ struct Args {
     float *part_o;           // [piece][piece_rows][D]
     float2 *part_ml;         // [piece][piece_rows] (m, l)
     uint32_t piece_rows;
+    float *tc_o;             // k_shared: [piece][2][128][D]
+    float2 *tc_ml;           // [piece][2][128]
 };
 
 // Tokens of request r's sequence; 0 for an empty slot and for a request that
@@ -450,6 +455,345 @@ __global__ void __launch_bounds__(kThreads, 2) k_rows(const __grid_constant__ CU
     if (!ok && lane == 0) flag_why(a.status, CG_ERR_TIMEOUT, kWhyWait);
 }
 
+// ---------------------------------------------------------------------------
+// The shared part for many query rows, on tcgen05.
+//
+// Rows: a KV head's query rows of all requests, 128 to a tile (the M of the
+// matrix instructions, a row per TMEM lane).  A block works on two softmax
+// streams, each with a score tile S and an output O in TMEM: with more than
+// 128 rows the streams are two row tiles that read the same K and V; with up
+// to 128 rows they are the even and the odd token tiles of one row tile.
+// While one stream's warps turn S into weights, the tensor cores work on the
+// other's.  Token tiles are 128 long: S = Q K^T (both from shared memory),
+// P = e^{S - m} goes back into TMEM as the A operand of O += P V, whose V is
+// read as it lies in the pool (rows = tokens, the contraction dimension).
+// The running maximum m is only raised, and O rescaled, when a tile's maximum
+// lies more than 8 (a factor of 2^8) above it; P is kept kShift octaves high,
+// so that fp16 weights neither overflow (2^(8 + 6)) nor lose their small end.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kTcTok = 128, kTcSlots = 5;
+// Three warpgroups: two of softmax, one whose first warps fetch tiles and
+// issue MMAs.  The launch gives 168 registers a thread; the last group keeps
+// 72, so that a softmax thread can hold its row of scores: 2 x 216 + 72 = 3 x 168.
+constexpr uint32_t kTcThreads = 384;
+constexpr float kGrow = 8.f, kShift = 6.f;
+
+template <uint32_t D> struct TcSmem {
+    static constexpr uint32_t kHalf = kTcTok * 128;     // 64 channels x 128 rows
+    static constexpr uint32_t kTile = kTcTok * D * 2;   // K, V or Q
+    static constexpr uint32_t oQ = kTcSlots * kTile;
+    static constexpr uint32_t oBar = oQ + 2 * kTile;
+    static constexpr uint32_t kBytes = oBar + 256 + 1024;
+};
+// TMEM columns.  With D = 64 there is room for P beside S; with D = 128 it
+// lies on S, which the MMAs of one shape leave in order.
+template <uint32_t D> struct Tmem {
+    static constexpr __host__ __device__ uint32_t S(uint32_t s) { return s * 128; }
+    static constexpr __host__ __device__ uint32_t O(uint32_t s) { return 256 + s * D; }
+    static constexpr __host__ __device__ uint32_t P(uint32_t s) { return D == 64 ? 384 + s * 64 : s * 128; }
+};
+
+struct TcPiece {
+    uint32_t item, pair, head, tile0, n;
+};
+__device__ __forceinline__ bool next_tc_piece(const Args &a, uint64_t &t, uint64_t end, uint32_t of, TcPiece &p) {
+    if (t >= end) return false;
+    p.item = (uint32_t)(t / of);
+    p.head = p.item / a.pairs;
+    p.pair = p.item - p.head * a.pairs;
+    p.tile0 = (uint32_t)(t - (uint64_t)p.item * of);
+    p.n = (uint32_t)min((uint64_t)(of - p.tile0), end - t);
+    t += p.n;
+    return true;
+}
+
+template <class T, uint32_t D>
+__global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant__ CUtensorMap map, const Args a) {
+    using M = TcSmem<D>;
+    constexpr bool kBf16 = sizeof(T) == 2 && !__is_same(T, __half);
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (s_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sm = s_addr(smem), tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+    // barriers: slot full / empty, then per stream: scores ready, weights ready, output ready; queries ready; drain
+    const uint32_t full = sm + M::oBar, empty = full + 8 * kTcSlots, s_rdy = empty + 8 * kTcSlots, p_rdy = s_rdy + 16,
+                   o_rdy = p_rdy + 16, q_rdy = o_rdy + 16, drain = q_rdy + 8;
+    uint32_t *tm_at = reinterpret_cast<uint32_t *>(smem + M::oBar + 8 * (2 * kTcSlots + 8));
+    if (tid == 0) {
+        for (uint32_t k = 0; k < 2 * kTcSlots; k++) bar_init(full + 8 * k, 1);
+        for (uint32_t s = 0; s < 2; s++) {
+            bar_init(s_rdy + 8 * s, 1);
+            bar_init(p_rdy + 8 * s, 128);
+            bar_init(o_rdy + 8 * s, 1);
+        }
+        bar_init(q_rdy, 256);
+        bar_init(drain, 1);
+        fence_bar_init();
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(s_addr(tm_at)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = *tm_at;
+
+    const uint32_t of = (a.P + kTcTok - 1) / kTcTok;  // tiles of an item
+    const uint64_t total = (uint64_t)a.pairs * a.Hkv * of;
+    const uint64_t n_cta = min((uint64_t)a.n_tc, total);
+    uint64_t t = blockIdx.x < n_cta ? blockIdx.x * total / n_cta : total;
+    const uint64_t end = blockIdx.x < n_cta ? (blockIdx.x + 1ull) * total / n_cta : total;
+    TcPiece p;
+    bool ok = true;
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 8) {  // fetch: tiles in the order in which the MMA warp uses them
+            const uint32_t rows_log = min(a.bshift, 6u), rows = 1u << rows_log, boxes = kTcTok >> rows_log;
+            const uint32_t *row = a.tables + (uint64_t)a.shared_slot * a.n_blocks;
+            uint32_t cnt = 0;
+            auto fetch = [&](uint32_t tile, uint32_t kv, uint32_t head) {
+                if (!ok) return;
+                const uint32_t st = cnt % kTcSlots;
+                const uint32_t pos = tile * kTcTok + lane * rows;
+                uint32_t id = a.n_pool;  // outside the map: reads zeros
+                if (lane < boxes && pos < a.P) {
+                    id = row[pos >> a.bshift];
+                    if (id >= a.n_pool) {
+                        id = a.n_pool;
+                        flag(a.status, CG_ERR_RANGE);
+                    }
+                }
+                if (cnt >= kTcSlots) ok = bar_wait(empty + 8 * st, (cnt / kTcSlots - 1) & 1u);
+                ok = __all_sync(kFull, ok);
+                if (!ok) return;
+                if (lane == 0) bar_expect(full + 8 * st, M::kTile);
+                __syncwarp();
+                if (lane < boxes)
+    #pragma unroll
+                    for (uint32_t h = 0; h < D / 64; h++)
+                        tma_box(sm + st * M::kTile + h * M::kHalf + lane * rows * 128, &map, (int)(head * D + 64 * h),
+                                (int)(pos & ((1u << a.bshift) - 1u)), (int)id, (int)kv, full + 8 * st);
+                cnt++;
+            };
+            while (next_tc_piece(a, t, end, of, p)) {
+                const uint32_t ahead = a.one ? 2 : 1;  // score tiles fetched before the first V
+                for (uint32_t k = 0; k < ahead && k < p.n; k++) fetch(p.tile0 + k, 0, p.head);
+                for (uint32_t k = 0; k < p.n; k++) {
+                    fetch(p.tile0 + k, 1, p.head);
+                    if (k + ahead < p.n) fetch(p.tile0 + k + ahead, 0, p.head);
+                }
+            }
+            if (!ok) {
+                for (uint32_t k = cnt > kTcSlots ? cnt - kTcSlots : 0; k < cnt; k++)
+                    bar_wait(full + 8 * (k % kTcSlots), (k / kTcSlots) & 1u);
+                if (lane == 0) flag_why(a.status, CG_ERR_TIMEOUT, kWhyWait);
+            }
+        } else if (warp == 9) {
+            if (lane == 0) {
+                constexpr uint32_t kQk = mma_shape(kBf16, kTcTok, true), kPv = mma_shape(kBf16, D, false);
+                uint32_t cnt = 0, piece = 0, np[2] = {0, 0};
+                auto slot_ready = [&](uint32_t c) {
+                    if (ok) ok = bar_wait(full + 8 * (c % kTcSlots), (c / kTcSlots) & 1u);
+                    tc_fence_after();
+                };
+                auto qk = [&](uint32_t s, uint32_t c) {
+                    if (!ok) return;
+                    const uint32_t q = mma_desc(sm + M::oQ + (a.one ? 0 : s) * M::kTile, true, 0),
+                                   k = mma_desc(sm + (c % kTcSlots) * M::kTile, true, 0);
+    #pragma unroll
+                    for (uint32_t x = 0; x < D / 16; x++) {
+                        const uint32_t o = ((x >> 2) * M::kHalf + (x & 3u) * 32) >> 4;
+                        tc_mma_ss(tm + Tmem<D>::S(s), q + o, k + o, kQk, x != 0);
+                    }
+                    tc_commit(s_rdy + 8 * s);
+                };
+                auto pv = [&](uint32_t s, uint32_t c, bool first) {
+                    if (ok) ok = bar_wait(p_rdy + 8 * s, np[s]++ & 1u);
+                    tc_fence_after();
+                    if (!ok) return;
+                    const uint32_t v = mma_desc(sm + (c % kTcSlots) * M::kTile, false, M::kHalf);
+    #pragma unroll
+                    for (uint32_t x = 0; x < kTcTok / 16; x++)
+                        tc_mma_ts(tm + Tmem<D>::O(s), tm + Tmem<D>::P(s) + 8 * x, v + x * 128, kPv, !first || x != 0);
+                };
+                auto free_slot = [&](uint32_t c) {
+                    if (ok) tc_commit(empty + 8 * (c % kTcSlots));
+                };
+                auto done = [&](uint32_t s) {
+                    if (ok) tc_commit(o_rdy + 8 * s);
+                };
+                while (next_tc_piece(a, t, end, of, p)) {
+                    if (ok) ok = bar_wait(q_rdy, piece++ & 1u);
+                    tc_fence_after();
+                    if (a.one) {  // even token tiles: stream 0, odd ones: stream 1
+                        for (uint32_t k = 0; k < 2 && k < p.n; k++) {
+                            slot_ready(cnt);
+                            qk(k, cnt);
+                            free_slot(cnt++);
+                        }
+                        for (uint32_t k = 0; k < p.n; k++) {
+                            const uint32_t s = k & 1u;
+                            slot_ready(cnt);
+                            pv(s, cnt, k < 2);
+                            free_slot(cnt++);
+                            if (k + 2 < p.n) {
+                                slot_ready(cnt);
+                                qk(s, cnt);
+                                free_slot(cnt++);
+                            } else {
+                                done(s);
+                            }
+                        }
+                    } else {
+                        slot_ready(cnt);
+                        qk(0, cnt);
+                        qk(1, cnt);
+                        free_slot(cnt++);
+                        for (uint32_t k = 0; k < p.n; k++) {
+                            const uint32_t v = cnt++;
+                            const bool more = k + 1 < p.n;
+                            slot_ready(v);
+                            if (more) slot_ready(cnt);
+                            for (uint32_t s = 0; s < 2; s++) {
+                                pv(s, v, k == 0);
+                                if (s) free_slot(v);
+                                if (more) qk(s, cnt);
+                                else done(s);
+                            }
+                            if (more) free_slot(cnt++);
+                        }
+                    }
+                }
+                if (!ok) {
+                    tc_commit(drain);
+                    bar_wait(drain, 0);
+                    flag_why(a.status, CG_ERR_TIMEOUT, kWhyWait);
+                }
+            }
+            __syncwarp();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const uint32_t s = warp >> 2, rl = tid & 127u;            // stream, row (TMEM lane)
+        const uint32_t tml = tm + ((warp & 3u) << 21);            // this warp's lanes
+        uint32_t ns = 0, piece = 0;
+        const uint32_t rows_all = a.R * a.nq * a.g, per = a.nq * a.g;
+        while (next_tc_piece(a, t, end, of, p)) {
+            // the queries: a row per thread; with one row tile the first group brings it
+            if (!(a.one && s)) {
+                const uint32_t x = p.pair * 256 + s * 128 + rl;
+                const bool valid = x < rows_all;
+                const uint32_t r = x / per, y = x - r * per, i = y / a.g, h = p.head * a.g + (y - i * a.g);
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + r * a.qs[0] + i * a.qs[1] + h * a.qs[2]);
+                uint8_t *dst = smem + M::oQ + s * M::kTile + rl * 128;
+#pragma unroll
+                for (uint32_t c = 0; c < D / 8; c++) {
+                    uint4 v = valid ? src[c] : make_uint4(0, 0, 0, 0);
+                    v.x ^= a.flip;
+                    v.y ^= a.flip;
+                    v.z ^= a.flip;
+                    v.w ^= a.flip;
+                    *reinterpret_cast<uint4 *>(dst + (c >> 3) * M::kHalf + (((c & 7u) ^ (rl & 7u)) << 4)) = v;
+                }
+            }
+            fence_async();
+            bar_arrive(q_rdy);
+
+            const uint32_t mine = a.one ? (p.n + 1 - s) / 2 : p.n;
+            float m = -INFINITY, l = 0.f;
+            for (uint32_t k = 0; k < mine; k++) {
+                if (ok) ok = bar_wait(s_rdy + 8 * s, ns++ & 1u);
+                ok = __all_sync(kFull, ok);
+                if (!ok) continue;
+                tc_fence_after();
+                uint32_t x[4][32];
+#pragma unroll
+                for (uint32_t c = 0; c < 4; c++) tc_ld32(x[c], tml + Tmem<D>::S(s) + 32 * c);
+                tc_wait_ld();
+                const uint32_t tile = p.tile0 + (a.one ? 2 * k + s : k), left = a.P - tile * kTcTok;
+                if (left < kTcTok) {
+#pragma unroll
+                    for (uint32_t c = 0; c < 4; c++)
+#pragma unroll
+                        for (uint32_t j = 0; j < 32; j++)
+                            if (32 * c + j >= left) x[c][j] = 0xFF800000u;
+                }
+                float mx = -INFINITY;
+#pragma unroll
+                for (uint32_t c = 0; c < 4; c++)
+#pragma unroll
+                    for (uint32_t j = 0; j < 32; j++) mx = fmaxf(mx, __uint_as_float(x[c][j]));
+                mx = mx == -INFINITY ? mx : mx * a.scale2;
+                const bool grow = k == 0 || mx - m > kGrow;
+                if (__any_sync(kFull, grow)) {
+                    const float nm = grow ? fmaxf(m, mx) : m, f = nm == m ? 1.f : ex2(m - nm);
+                    m = nm;
+                    l *= f;
+                    if (k) {  // the MMAs before this tile's scores, and so O, are done
+#pragma unroll
+                        for (uint32_t c = 0; c < D / 32; c++) {
+                            uint32_t o[32];
+                            tc_ld32(o, tml + Tmem<D>::O(s) + 32 * c);
+                            tc_wait_ld();
+#pragma unroll
+                            for (uint32_t j = 0; j < 32; j++) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tc_st32(tml + Tmem<D>::O(s) + 32 * c, o);
+                        }
+                    }
+                }
+                const float z = m == -INFINITY ? 0.f : kShift - m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (uint32_t c = 0; c < 2; c++) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (uint32_t j = 0; j < 32; j++) {
+                        const uint32_t e = 2 * j;
+                        const float u = ex2(fmaf(__uint_as_float(x[2 * c + (e >> 5)][e & 31u]), a.scale2, z));
+                        const float v = ex2(fmaf(__uint_as_float(x[2 * c + (e >> 5)][(e & 31u) + 1]), a.scale2, z));
+                        sum[j & 3u] += u + v;
+                        w[j] = Half<T>::pack(u, v);
+                    }
+                    tc_st32(tml + Tmem<D>::P(s) + 32 * c, w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tc_wait_st();
+                tc_fence_before();
+                bar_arrive(p_rdy + 8 * s);
+            }
+            // the piece's result
+            const uint64_t at = (((uint64_t)blockIdx.x + p.item) * 2 + s) * 128 + rl;
+            a.tc_ml[at] = make_float2(m == -INFINITY ? m : m - kShift, l);
+            if (mine) {
+                if (ok) ok = bar_wait(o_rdy + 8 * s, piece & 1u);
+                ok = __all_sync(kFull, ok);
+                if (ok) {
+                    tc_fence_after();
+#pragma unroll
+                    for (uint32_t c = 0; c < D / 32; c++) {
+                        uint32_t o[32];
+                        tc_ld32(o, tml + Tmem<D>::O(s) + 32 * c);
+                        tc_wait_ld();
+                        uint4 *dst = reinterpret_cast<uint4 *>(a.tc_o + at * D + 32 * c);
+#pragma unroll
+                        for (uint32_t j = 0; j < 8; j++)
+                            dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    }
+                    tc_fence_before();
+                }
+                piece++;
+            }
+            group_sync(1, 256);  // both streams are done with the queries and with TMEM
+        }
+        if (!ok && lane == 0) flag_why(a.status, CG_ERR_TIMEOUT, kWhyWait);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm));
+}
+
 // Joins the pieces of each query row, a warp per row.
 template <class T, uint32_t D>
 __global__ void __launch_bounds__(256) k_merge(const Args a) {
@@ -467,24 +811,32 @@ __global__ void __launch_bounds__(256) k_merge(const Args a) {
     float m = -INFINITY, l = 0.f, o[kPer];
     for (uint32_t k = 0; k < kPer; k++) o[k] = 0.f;
     // the pieces of one item: its tiles [t0, t0 + nt) are spread over blocks c0..c1
+    auto add = [&](const float2 *ml, const float *po, uint64_t at) {
+        const float2 v = ml[at];
+        if (v.y == 0.f) return;  // a piece the row sees nothing of
+        const float *src = po + at * D + lane * kPer;
+        const float nm = fmaxf(m, v.x);
+        const float f = m == nm ? 1.f : ex2(m - nm), e = v.x == nm ? 1.f : ex2(v.x - nm);
+        m = nm;
+        l = l * f + v.y * e;
+        for (uint32_t k = 0; k < kPer; k++) o[k] = o[k] * f + src[k] * e;
+    };
     auto join = [&](uint64_t t0, uint32_t nt, uint32_t item, uint32_t local) {
         const uint64_t c0 = ((t0 + 1) * n_cta - 1) / total, c1 = ((t0 + nt) * n_cta - 1) / total;
-        for (uint64_t c = c0; c <= c1; c++) {
-            const uint64_t at = (c + item) * a.piece_rows + local;
-            const float2 v = a.part_ml[at];
-            const float *src = a.part_o + at * D + lane * kPer;
-            float y[kPer];
-            for (uint32_t k = 0; k < kPer; k++) y[k] = src[k];
-            if (v.x == -INFINITY && v.y == 0.f) continue;  // a piece the row sees nothing of
-            const float nm = fmaxf(m, v.x);
-            const float f = m == nm ? 1.f : ex2(m - nm), e = v.x == nm ? 1.f : ex2(v.x - nm);
-            m = nm;
-            l = l * f + v.y * e;
-            for (uint32_t k = 0; k < kPer; k++) o[k] = o[k] * f + y[k] * e;
-        }
+        for (uint64_t c = c0; c <= c1; c++) add(a.part_ml, a.part_o, (c + item) * a.piece_rows + local);
         return c0 == c1;
     };
     if (len) {
+        if (a.pairs) {
+            const uint32_t of = (a.P + kTcTok - 1) / kTcTok, xp = r * a.nq * a.g + x;
+            const uint32_t item = head * a.pairs + (xp >> 8);
+            const uint64_t tt = (uint64_t)a.pairs * a.Hkv * of, n = min((uint64_t)a.n_tc, tt), t0 = (uint64_t)item * of;
+            const uint64_t c0 = ((t0 + 1) * n - 1) / tt, c1 = ((t0 + of) * n - 1) / tt;
+            for (uint64_t c = c0; c <= c1; c++) {
+                add(a.tc_ml, a.tc_o, (c + item) * 256 + (xp & 255u));
+                if (a.one) add(a.tc_ml, a.tc_o, (c + item) * 256 + 128 + xp);
+            }
+        }
         const uint32_t nt = len > a.P ? tiles_of(len - a.P) : 0;
         if (a.npt) {
             const uint32_t xp = r * a.nq * a.g + x, item = (xp / kRows) * a.Hkv + head;
@@ -507,10 +859,11 @@ __global__ void __launch_bounds__(256) k_merge(const Args a) {
 bool misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1u)) != 0; }
 
 struct Plan {
-    uint32_t g, rt, npt, piece_rows;
-    uint64_t items, pieces, cum_bytes, o_bytes, bytes;
+    uint32_t g, rt, npt, pairs, one, piece_rows;
+    uint64_t items, pieces, cum_bytes, o_bytes, ml_bytes, tc_o_bytes, bytes;
 };
 
+constexpr uint32_t kTcRows = 32;    // k_shared takes the shared part from more query rows than this per KV head
 constexpr uint32_t kMaxCtas = 512;  // bound of the grid that the workspace is sized for
 
 bool make_plan(const cg_pages *p, const cg_attention *a, Plan *o) {
@@ -537,14 +890,20 @@ bool make_plan(const cg_pages *p, const cg_attention *a, Plan *o) {
     const uint64_t per = (uint64_t)a->n_queries * o->g, all = per * a->n_requests;
     if (all * a->n_kv_heads > (1ull << 31)) return false;
     o->rt = (uint32_t)((per + kRows - 1) / kRows);
-    o->npt = a->shared_blocks ? (uint32_t)((all + kRows - 1) / kRows) : 0;
+    const bool tc = a->shared_blocks && all > kTcRows;
+    o->pairs = tc ? (uint32_t)((all + 255) / 256) : 0;
+    o->one = all <= 128;
+    o->npt = a->shared_blocks && !tc ? (uint32_t)((all + kRows - 1) / kRows) : 0;
     o->piece_rows = o->npt ? (uint32_t)(all < kRows ? all : kRows) : (uint32_t)(per < kRows ? per : kRows);
     o->items = ((uint64_t)a->n_requests * o->rt + o->npt) * a->n_kv_heads;
     if (o->items > (1ull << 31)) return false;
     o->pieces = o->items + kMaxCtas;
     o->cum_bytes = round_up((a->n_requests + 1ull) * 8, 256);
     o->o_bytes = round_up(o->pieces * o->piece_rows * a->head_dim * 4, 256);
-    o->bytes = o->cum_bytes + o->o_bytes + round_up(o->pieces * o->piece_rows * 8, 256);
+    o->ml_bytes = round_up(o->pieces * o->piece_rows * 8, 256);
+    const uint64_t tc_rows = tc ? ((uint64_t)o->pairs * a->n_kv_heads + kMaxCtas) * 256 : 0;
+    o->tc_o_bytes = tc_rows * a->head_dim * 4;
+    o->bytes = o->cum_bytes + o->o_bytes + o->ml_bytes + o->tc_o_bytes + tc_rows * 8;
     return true;
 }
 
@@ -581,6 +940,14 @@ template <class T, uint32_t D>
 cudaError_t launch(const CUtensorMap &map, Args &a, int sms, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(k_rows<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
     if (e != cudaSuccess) return e;
+    if (a.pairs) {
+        e = cudaFuncSetAttribute(k_shared<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<D>::kBytes);
+        if (e != cudaSuccess) return e;
+        a.n_tc = (uint32_t)sms < kMaxCtas ? (uint32_t)sms : kMaxCtas;
+        k_shared<T, D><<<a.n_tc, kTcThreads, TcSmem<D>::kBytes, s>>>(map, a);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
     a.n_cta = (uint32_t)sms * 2u < kMaxCtas ? (uint32_t)sms * 2u : kMaxCtas;
     k_rows<T, D><<<a.n_cta, kThreads, Smem<D>::kBytes, s>>>(map, a);
     e = cudaGetLastError();
@@ -636,7 +1003,7 @@ extern "C" cg_status cg_attend(const cg_pages *p, const cg_attention *at, void *
         a.qs[k] = at->q_stride[k];
         a.os[k] = at->out_stride[k];
     }
-    a.scale2 = fabsf(at->scale) * kLog2e;
+    a.scale2 = fmaxf(fabsf(at->scale) * kLog2e, 1e-35f);  // not 0: masked scores are -inf before the product
     a.flip = at->scale < 0.f ? 0x80008000u : 0u;
     a.status = dev_status;
     uint8_t *w = static_cast<uint8_t *>(ws);
@@ -644,6 +1011,10 @@ extern "C" cg_status cg_attend(const cg_pages *p, const cg_attention *at, void *
     a.part_o = reinterpret_cast<float *>(w + pl.cum_bytes);
     a.part_ml = reinterpret_cast<float2 *>(w + pl.cum_bytes + pl.o_bytes);
     a.piece_rows = pl.piece_rows;
+    a.pairs = pl.pairs;
+    a.one = pl.one;
+    a.tc_o = reinterpret_cast<float *>(w + pl.cum_bytes + pl.o_bytes + pl.ml_bytes);
+    a.tc_ml = reinterpret_cast<float2 *>(w + pl.cum_bytes + pl.o_bytes + pl.ml_bytes + pl.tc_o_bytes);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool fp16 = at->dtype == CG_FP16;
     if (at->head_dim == 128) CG_CUDA_TRY((fp16 ? launch<__half, 128>(map, a, sms, s) : launch<__nv_bfloat16, 128>(map, a, sms, s)));
