@@ -18,11 +18,8 @@ namespace cg {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr uint32_t kTok = 64;       // tokens of a tile
-constexpr uint32_t kRows = 16;      // query rows of a row tile
-constexpr uint32_t kStages = 3;     // tiles in flight
-constexpr uint32_t kConsumers = 4;  // warps that compute; one more fetches
-constexpr uint32_t kThreads = (kConsumers + 1) * 32;
+constexpr uint32_t kRows = 16;  // query rows of a row tile
+constexpr uint32_t kTileRows = 64;  // K rows of a tile of k_rows: 64 / nh tokens of nh neighbouring heads
 
 struct Args {
     const uint16_t *q;
@@ -32,8 +29,10 @@ struct Args {
     uint32_t n_slots, n_blocks, n_pool, bshift;
     uint32_t R, nq, g, Hkv;  // requests, query tokens, query heads per KV head, KV heads
     uint32_t P, shared_slot; // shared tokens
-    uint32_t rt;             // row tiles of a request
-    uint32_t npt;            // row tiles of the whole batch over the shared tokens in k_rows (0: k_shared has them)
+    uint32_t nh, ng;         // k_rows: heads that one block takes together (1, 2 or 4), groups of them
+    uint32_t tlog;           // log2 of the tokens of a tile, 64 / nh
+    uint32_t rt;             // items' row ranges of a request
+    uint32_t npt;            // row ranges of the whole batch over the shared tokens in k_rows (0: k_shared has them)
     uint32_t pairs;          // k_shared: pairs of 128-row tiles of the whole batch (0: k_rows has the shared part)
     uint32_t one;            // k_shared: the batch fits one 128-row tile
     uint32_t n_tc;           // blocks of k_shared
@@ -44,9 +43,9 @@ struct Args {
     uint32_t *status;
     // workspace
     uint64_t *cum;           // [R + 1] first tile of request r; [R]: tiles of all requests
-    float *part_o;           // [piece][piece_rows][D]
-    float2 *part_ml;         // [piece][piece_rows] (m, l)
-    uint32_t piece_rows;
+    float *part_o;           // [piece][4][piece_rows][D], a quarter per warp column of k_rows
+    float2 *part_ml;         // [piece][4][piece_rows] (m, l)
+    uint32_t piece_rows, range_rows; // rows of a piece that are stored; rows of an item's range
     float *tc_o;             // k_shared: [piece][2][128][D]
     float2 *tc_ml;           // [piece][2][128]
 };
@@ -68,19 +67,25 @@ __device__ __forceinline__ uint32_t tokens_of(const Args &a, uint32_t r, bool *b
     return n;
 }
 
-__device__ __forceinline__ uint32_t tiles_of(uint32_t tokens) { return (tokens + kTok - 1) / kTok; }
+__device__ __forceinline__ uint32_t tiles_of(const Args &a, uint32_t tokens) {
+    return (tokens + (1u << a.tlog) - 1u) >> a.tlog;
+}
+// Blocks that a list of `total` tiles is dealt to: two tiles each at least.
+__device__ __forceinline__ uint64_t shares(const Args &a, uint64_t total) {
+    return min((uint64_t)a.n_cta, (total + 1) / 2);
+}
 
-// Work list: for each request its row tiles x KV heads ("items"), each
-// ceil(own tokens / 64) tiles long, then the items of the shared part.  Block
+// Work list: for each request its row ranges x head groups ("items"), each as
+// long as the request's own tokens, then the items of the shared part.  Block
 // c of n takes tiles [c T / n, (c + 1) T / n) of the whole list, so every
-// block has the same share whatever the lengths are (n is cut to T, so that
-// no block between two others is left without a tile).  A block's run of tiles
-// of one item is a piece; its slot c + item is unique, since along the list
-// each new piece has a larger block or a larger item.
+// block has the same share whatever the lengths are (n <= T: no block between
+// two others is left without a tile).  A block's run of tiles of one item is a
+// piece; its slot c + item is unique, since along the list each new piece has
+// a larger block or a larger item.
 struct Piece {
     uint32_t r;        // request; R: the shared part
     uint32_t item;     // number of the item
-    uint32_t rtile, head;
+    uint32_t range, group;
     uint32_t tile0, n; // tiles of the item
     uint32_t of;       // tiles the item has
     uint32_t len;      // tokens in the sequence (request) or P
@@ -97,8 +102,8 @@ __device__ __forceinline__ bool next_piece(const Args &a, Walk &w, Piece &p) {
     uint32_t nt = 0, len = 0;
     while (w.r < a.R) {
         len = tokens_of(a, w.r, &bad);
-        nt = len > a.P ? tiles_of(len - a.P) : 0;
-        const uint64_t all = (uint64_t)nt * a.rt * a.Hkv;
+        nt = len > a.P ? tiles_of(a, len - a.P) : 0;
+        const uint64_t all = (uint64_t)nt * a.rt * a.ng;
         if (w.t < w.base + all) break;
         w.base += all;
         w.r++;
@@ -106,13 +111,13 @@ __device__ __forceinline__ bool next_piece(const Args &a, Walk &w, Piece &p) {
     p.r = w.r;
     if (w.r == a.R) {
         len = a.P;
-        nt = tiles_of(a.P);
+        nt = tiles_of(a, a.P);
     }
     const uint64_t at = w.t - w.base;
     const uint32_t local = (uint32_t)(at / nt);
-    p.item = (uint32_t)min(w.r, a.R) * a.rt * a.Hkv + local;
-    p.rtile = local / a.Hkv;
-    p.head = local - p.rtile * a.Hkv;
+    p.item = w.r * a.rt * a.ng + local;
+    p.range = local / a.ng;
+    p.group = local - p.range * a.ng;
     p.tile0 = (uint32_t)(at - (uint64_t)local * nt);
     p.n = (uint32_t)min((uint64_t)(nt - p.tile0), w.end - w.t);
     p.of = nt;
@@ -121,15 +126,15 @@ __device__ __forceinline__ bool next_piece(const Args &a, Walk &w, Piece &p) {
     return true;
 }
 
-// Query row `row` of an item: request, query token, query head.
+// Query row x of an item (of the request, or of the batch in the shared
+// part): request, query token, query head.
 struct Row {
     uint32_t r, i, h;
     bool valid;
 };
-__device__ __forceinline__ Row row_of(const Args &a, const Piece &p, uint32_t row) {
+__device__ __forceinline__ Row row_of(const Args &a, const Piece &p, uint32_t x, uint32_t head) {
     Row o;
     const uint32_t per = a.nq * a.g;
-    uint32_t x = p.rtile * kRows + row;
     if (p.r == a.R) {
         o.r = x / per;
         x -= o.r * per;
@@ -139,28 +144,33 @@ __device__ __forceinline__ Row row_of(const Args &a, const Piece &p, uint32_t ro
         o.valid = x < per;
     }
     o.i = x / a.g;
-    o.h = p.head * a.g + (x - o.i * a.g);
+    o.h = head * a.g + (x - o.i * a.g);
     return o;
 }
 
-template <uint32_t D> struct Smem {
-    static constexpr uint32_t kHalf = kTok * 128;           // 64 channels of a tile, 128-byte swizzled rows
-    static constexpr uint32_t kTile = kTok * D * 2;         // K or V of a tile
+// kR row tiles of 16 query rows a block.
+template <uint32_t D, uint32_t kR> struct Smem {
+    static constexpr uint32_t kStages = 3 * kR;             // tiles in flight: 96 KB, or 192 KB where one block has an SM
+    static constexpr uint32_t kThreads = (4 * kR + 1) * 32; // kR x 4 warps compute, one fetches
+    static constexpr uint32_t kTile = kTileRows * D * 2;    // K or V of a tile
     static constexpr uint32_t kStage = 2 * kTile;
-    static constexpr uint32_t kBufStride = D + 4;
-    static constexpr uint32_t oBuf = kStages * kStage;      // [16][D + 4] fp32
-    static constexpr uint32_t oMl = oBuf + kRows * kBufStride * 4;
-    static constexpr uint32_t oBar = oMl + kConsumers * kRows * 8;
+    static constexpr uint32_t oBar = kStages * kStage;
     static constexpr uint32_t oMisc = oBar + 2 * kStages * 8;
-    static constexpr uint32_t kBytes = oMisc + 64 + 1024;   // and slack to align the tiles to 1 KiB
+    static constexpr uint32_t kBytes = oMisc + 128 + 1024;  // and slack to align the tiles to 1 KiB
 };
 
-// Query rows in tiles of 16 against their tokens, 64 at a time: four warps
-// take 16 tokens each with a softmax state of their own and join at the end
-// of the piece; a fifth warp fetches the tiles, three in flight.
-template <class T, uint32_t D>
-__global__ void __launch_bounds__(kThreads, 2) k_rows(const __grid_constant__ CUtensorMap map, const Args a) {
-    using S = Smem<D>;
+// Query rows in tiles of 16 against their tokens.  A block takes nh = 4
+// neighbouring KV heads, 16 tokens at a time: a token's rows of four heads are
+// one run of memory (1 KiB with 128 channels), and each warp has a head of its
+// own, so that its softmax needs no other warp.  With fewer heads (nh = 2, 1)
+// tiles are 32 or 64 tokens long and the warps of a head take every second or
+// fourth 16 of them; their results go out as separate parts.  With kR = 2, two
+// sets of warps take two row tiles against the same K and V.  One more warp
+// fetches the tiles by TMA.
+template <class T, uint32_t D, uint32_t kR>
+__global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __grid_constant__ CUtensorMap map, const Args a) {
+    using S = Smem<D, kR>;
+    constexpr uint32_t kStages = S::kStages, kWarps = 4 * kR;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (s_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t sm = s_addr(smem);
@@ -171,18 +181,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_rows(const __grid_constant__ CU
     if (tid == 0) {
         for (uint32_t k = 0; k < kStages; k++) {
             bar_init(full + 8 * k, 1);
-            bar_init(empty + 8 * k, kConsumers);
+            bar_init(empty + 8 * k, kWarps);
         }
         fence_bar_init();
     }
     // This block's share of the work list: every thread sums its own run of requests.
-    const uint32_t per = (a.R + kThreads - 1) / kThreads;
+    const uint32_t per = (a.R + S::kThreads - 1) / S::kThreads;
     const uint32_t r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
     uint64_t mine = 0;
     bool bad = false;
     for (uint32_t r = r0; r < r1; r++) {
         const uint32_t n = tokens_of(a, r, &bad);
-        mine += (uint64_t)(n > a.P ? tiles_of(n - a.P) : 0) * a.rt * a.Hkv;
+        mine += (uint64_t)(n > a.P ? tiles_of(a, n - a.P) : 0) * a.rt * a.ng;
     }
     if (bad && blockIdx.x == 0) flag(a.status, CG_ERR_RANGE);
     uint64_t inc = mine;
@@ -193,74 +203,73 @@ __global__ void __launch_bounds__(kThreads, 2) k_rows(const __grid_constant__ CU
     if (lane == 31) misc[warp] = inc;
     __syncthreads();
     uint64_t before = inc - mine, own = 0;
-    for (uint32_t k = 0; k <= kConsumers; k++) {
+    for (uint32_t k = 0; k <= kWarps; k++) {
         if (k < warp) before += misc[k];
         own += misc[k];
     }
-    const uint64_t total = own + (uint64_t)a.npt * a.Hkv * tiles_of(a.P);
+    const uint64_t total = own + (uint64_t)a.npt * a.ng * tiles_of(a, a.P);
     if (blockIdx.x == 0) {
         uint64_t at = before;
         bool b = false;
         for (uint32_t r = r0; r < r1; r++) {
             a.cum[r] = at;
             const uint32_t n = tokens_of(a, r, &b);
-            at += (uint64_t)(n > a.P ? tiles_of(n - a.P) : 0) * a.rt * a.Hkv;
+            at += (uint64_t)(n > a.P ? tiles_of(a, n - a.P) : 0) * a.rt * a.ng;
         }
         if (tid == 0) a.cum[a.R] = own;
     }
+    const uint64_t n_cta = shares(a, total);
     Walk w;
-    const uint64_t n_cta = min((uint64_t)a.n_cta, total);  // at least a tile each
     w.t = blockIdx.x < n_cta ? blockIdx.x * total / n_cta : total;
     w.end = blockIdx.x < n_cta ? (blockIdx.x + 1ull) * total / n_cta : total;
     if (tid == 0) {
-        misc[5] = own;
-        misc[6] = a.R;
+        misc[kWarps + 1] = own;
+        misc[kWarps + 2] = a.R;
     }
     __syncthreads();
     if (mine && w.t >= before && w.t < before + mine) {  // one thread at most
-        misc[5] = before;
-        misc[6] = r0;
+        misc[kWarps + 1] = before;
+        misc[kWarps + 2] = r0;
     }
     __syncthreads();
-    w.base = misc[5];
-    w.r = (uint32_t)misc[6];
+    w.base = misc[kWarps + 1];
+    w.r = (uint32_t)misc[kWarps + 2];
 
+    const uint32_t tt = 1u << a.tlog;                 // tokens of a tile
+    const uint32_t head_bytes = tt * D * 2, half_bytes = tt * 128;
     Piece p;
     uint32_t it = 0;  // tiles so far: stage it % kStages, parity it / kStages
-    if (warp == kConsumers) {
-        const uint32_t rows_log = min(a.bshift, 6u), rows = 1u << rows_log, boxes = kTok >> rows_log;
+    if (warp == kWarps) {
+        // a box (64 channels x up to tt rows of one block) per lane, at most 32 of them
+        const uint32_t rlog = min(a.bshift, a.tlog), subs = tt >> rlog;
+        const uint32_t sub = lane % subs, x = lane / subs, half = x % (D / 64), y = x / (D / 64);
+        const uint32_t head = y % a.nh, kv = y / a.nh;
+        const bool mine_box = kv < 2;
+        const uint32_t dst0 = sm + kv * S::kTile + head * head_bytes + half * half_bytes + (sub << rlog) * 128;
         bool ok = true;
         while (ok && next_piece(a, w, p)) {
             const bool shared = p.r == a.R;
             const uint32_t slot = shared ? a.shared_slot : a.slots ? a.slots[p.r] : p.r;
             const uint32_t *row = a.tables + (uint64_t)slot * a.n_blocks;
-            const uint32_t first = shared ? 0u : a.P;
-            for (uint32_t k = 0; k < p.n; k++, it++) {
-                const uint32_t st = it % kStages;
-                // the block of this lane's box; a box past the sequence lies outside the map and reads zeros
-                const uint32_t pos = first + (p.tile0 + k) * kTok + lane * rows;
-                uint32_t id = a.n_pool;
-                if (lane < boxes && pos < p.len) {
-                    id = row[pos >> a.bshift];
-                    if (id >= a.n_pool) {
-                        id = a.n_pool;
-                        flag(a.status, CG_ERR_RANGE);
-                    }
-                }
+            const int c = (int)((p.group * a.nh + head) * D + half * 64);
+            uint32_t pos = (shared ? 0u : a.P) + (p.tile0 << a.tlog) + (sub << rlog);
+            // the block of this lane's box; a box past the sequence lies outside the map and reads zeros
+            uint32_t next = mine_box && pos < p.len ? row[pos >> a.bshift] : a.n_pool;
+            for (uint32_t k = 0; k < p.n; k++, it++, pos += tt) {
+                const uint32_t st = it % kStages, in = pos & ((1u << a.bshift) - 1u);
+                uint32_t id = next;
+                next = mine_box && pos + tt < p.len && k + 1 < p.n ? row[(pos + tt) >> a.bshift] : a.n_pool;
                 if (it >= kStages) ok = bar_wait(empty + 8 * st, (it / kStages - 1) & 1u);
                 ok = __all_sync(kFull, ok);
                 if (!ok) break;
                 if (lane == 0) bar_expect(full + 8 * st, S::kStage);
                 __syncwarp();
-                if (lane < boxes) {
-                    const uint32_t dst = sm + st * S::kStage + lane * rows * 128;
-                    const int c = (int)(p.head * D), in = (int)(pos & ((1u << a.bshift) - 1u));
-#pragma unroll
-                    for (uint32_t kv = 0; kv < 2; kv++)
-#pragma unroll
-                        for (uint32_t h = 0; h < D / 64; h++)
-                            tma_box(dst + kv * S::kTile + h * S::kHalf, &map, c + 64 * (int)h, in, (int)id, (int)kv,
-                                    full + 8 * st);
+                if (mine_box) {
+                    if (id > a.n_pool || (id == a.n_pool && pos < p.len)) {
+                        id = a.n_pool;
+                        flag(a.status, CG_ERR_RANGE);
+                    }
+                    tma_box(dst0 + st * S::kStage, &map, c, (int)in, (int)id, (int)kv, full + 8 * st);
                 }
             }
         }
@@ -272,18 +281,20 @@ __global__ void __launch_bounds__(kThreads, 2) k_rows(const __grid_constant__ CU
         return;
     }
 
-    float *buf = reinterpret_cast<float *>(smem + S::oBuf);
-    float2 *ml = reinterpret_cast<float2 *>(smem + S::oMl);
     const uint32_t qd = lane & 3u, rw = lane >> 2;
+    const uint32_t col = warp & 3u, hd = col % a.nh, part = col / a.nh;  // head of the group, 16 tokens of the tile
+    const uint32_t kbase = hd * head_bytes + part * 16 * 128, vbase = S::kTile + kbase;
     bool ok = true;
     while (next_piece(a, w, p)) {
         const bool shared = p.r == a.R;
         const uint32_t own_tokens = shared ? a.P : p.len - a.P;
+        const uint32_t head = p.group * a.nh + hd, x0 = p.range * (kR * kRows) + (warp >> 2) * kRows;
         // query fragments, and how many of the item's tokens each of this lane's two rows sees
         uint32_t q[D / 16][4];
         uint32_t lim[2], least = own_tokens;
+        Row ro[2];
         for (uint32_t e = 0; e < 2; e++) {
-            const Row o = row_of(a, p, rw + 8 * e);
+            const Row o = ro[e] = row_of(a, p, x0 + rw + 8 * e, head);
             const uint16_t *src = a.q + o.r * a.qs[0] + o.i * a.qs[1] + o.h * a.qs[2] + 2 * qd;
             for (uint32_t k = 0; k < D / 16; k++) {
                 q[k][e] = o.valid ? *reinterpret_cast<const uint32_t *>(src + 16 * k) ^ a.flip : 0u;
@@ -310,28 +321,25 @@ __global__ void __launch_bounds__(kThreads, 2) k_rows(const __grid_constant__ CU
                 ok = false;
                 continue;
             }
-            const uint32_t tok = (p.tile0 + k) * kTok + 16 * warp;  // this warp's 16 tokens of the item
+            const uint32_t tok = ((p.tile0 + k) << a.tlog) + 16 * part;  // this warp's 16 tokens of the item
             if (tok < own_tokens) {
-                const uint32_t kb = sm + st * S::kStage, vb = kb + S::kTile;
+                const uint32_t kb = sm + st * S::kStage + kbase, vb = sm + st * S::kStage + vbase;
                 const bool tail = tok + 16 > own_tokens;
                 if (tail) {  // rows past the sequence hold anything: V's must not meet the weight 0
-                    const uint32_t r = 16 * warp + (lane >> 1);
                     if (tok + (lane >> 1) >= own_tokens)
-                        for (uint32_t b = 0; b < D * 2; b += 32) {
-                            const uint32_t x = b + 16 * (lane & 1u);
-                            *reinterpret_cast<uint4 *>(smem + st * S::kStage + S::kTile + (x >> 7) * S::kHalf + r * 128 +
-                                                       (x & 127u)) = make_uint4(0, 0, 0, 0);
-                        }
+                        for (uint32_t b = 16 * (lane & 1u); b < D * 2; b += 32)
+                            *reinterpret_cast<uint4 *>(smem + st * S::kStage + vbase + (b >> 7) * half_bytes +
+                                                       (lane >> 1) * 128 + (b & 127u)) = make_uint4(0, 0, 0, 0);
                     __syncwarp();
                 }
                 float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
                 {
-                    const uint32_t r = 16 * warp + (lane >> 4) * 8 + (lane & 7u);
+                    const uint32_t r = (lane >> 4) * 8 + (lane & 7u);
                     const uint32_t rb = kb + r * 128, x = r & 7u, hi = (lane >> 3) & 1u;
 #pragma unroll
                     for (uint32_t c = 0; c < D / 16; c++) {
                         uint32_t b[4];
-                        ldsm4(b, rb + (c >> 2) * S::kHalf + ((((c & 3u) * 2 + hi) ^ x) << 4));
+                        ldsm4(b, rb + (c >> 2) * half_bytes + ((((c & 3u) * 2 + hi) ^ x) << 4));
                         Half<T>::mma(s[0], q[c], b[0], b[1]);
                         Half<T>::mma(s[1], q[c], b[2], b[3]);
                     }
@@ -379,12 +387,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_rows(const __grid_constant__ CU
                     }
                 const uint32_t pa[4] = {Half<T>::pack(s[0][0], s[0][1]), Half<T>::pack(s[0][2], s[0][3]),
                                         Half<T>::pack(s[1][0], s[1][1]), Half<T>::pack(s[1][2], s[1][3])};
-                const uint32_t r = 16 * warp + ((lane >> 3) & 1u) * 8 + (lane & 7u);
+                const uint32_t r = ((lane >> 3) & 1u) * 8 + (lane & 7u);
                 const uint32_t rb = vb + r * 128, x = r & 7u, hi = lane >> 4;
 #pragma unroll
                 for (uint32_t d = 0; d < D / 16; d++) {
                     uint32_t b[4];
-                    ldsm4_t(b, rb + (d >> 2) * S::kHalf + ((((d & 3u) * 2 + hi) ^ x) << 4));
+                    ldsm4_t(b, rb + (d >> 2) * half_bytes + ((((d & 3u) * 2 + hi) ^ x) << 4));
                     Half<T>::mma(o[2 * d], pa, b[0], b[1]);
                     Half<T>::mma(o[2 * d + 1], pa, b[2], b[3]);
                 }
@@ -394,63 +402,29 @@ __global__ void __launch_bounds__(kThreads, 2) k_rows(const __grid_constant__ CU
             if (lane == 0) bar_arrive(empty + 8 * st);
         }
 
-        // join the four warps: states, then the outputs one warp after another
 #pragma unroll
         for (uint32_t e = 0; e < 2; e++) {
             l[e] += __shfl_xor_sync(kFull, l[e], 1);
             l[e] += __shfl_xor_sync(kFull, l[e], 2);
-            if (qd == 0) ml[warp * kRows + rw + 8 * e] = make_float2(m[e], l[e]);
-        }
-        group_sync(1, kConsumers * 32);
-        float f[2];
-#pragma unroll
-        for (uint32_t e = 0; e < 2; e++) {
-            float mm = -INFINITY;
-            for (uint32_t k = 0; k < kConsumers; k++) mm = fmaxf(mm, ml[k * kRows + rw + 8 * e].x);
-            f[e] = m[e] == mm ? 1.f : ex2(m[e] - mm);
-        }
-        for (uint32_t k = 0; k < kConsumers; k++) {
-            if (warp == k) {
+            if (!ro[e].valid) continue;
+            if (a.P == 0 && a.nh == 4 && p.n == p.of) {  // the whole sequence: the answer
+                const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];
+                uint16_t *dst = a.out + ro[e].r * a.os[0] + ro[e].i * a.os[1] + ro[e].h * a.os[2] + 2 * qd;
 #pragma unroll
                 for (uint32_t d = 0; d < D / 8; d++)
-#pragma unroll
-                    for (uint32_t e = 0; e < 2; e++) {
-                        float2 *at = reinterpret_cast<float2 *>(buf + (rw + 8 * e) * S::kBufStride + d * 8 + 2 * qd);
-                        float2 v = k ? *at : make_float2(0.f, 0.f);
-                        v.x += o[d][2 * e] * f[e];
-                        v.y += o[d][2 * e + 1] * f[e];
-                        *at = v;
-                    }
-            }
-            group_sync(1, kConsumers * 32);
-        }
-        // eight threads a row
-        const uint32_t row = tid >> 3, part = tid & 7u;
-        const Row ro = row_of(a, p, row);
-        if (ro.valid) {
-            float mm = -INFINITY, ll = 0.f;
-            for (uint32_t k = 0; k < kConsumers; k++) mm = fmaxf(mm, ml[k * kRows + row].x);
-            for (uint32_t k = 0; k < kConsumers; k++) {
-                const float2 v = ml[k * kRows + row];
-                ll += v.y * (v.x == mm ? 1.f : ex2(v.x - mm));
-            }
-            const float *src = buf + row * S::kBufStride + part * (D / 8);
-            if (a.P == 0 && p.n == p.of) {  // the whole sequence: the answer
-                const float inv = ll == 0.f ? 0.f : 1.f / ll;
-                uint16_t *dst = a.out + ro.r * a.os[0] + ro.i * a.os[1] + ro.h * a.os[2] + part * (D / 8);
-                for (uint32_t d = 0; d < D / 8; d += 2)
-                    *reinterpret_cast<uint32_t *>(dst + d) = Half<T>::pack(src[d] * inv, src[d + 1] * inv);
-                if (a.lse && part == 0)
-                    a.lse[((uint64_t)ro.r * a.nq + ro.i) * (a.g * a.Hkv) + ro.h] =
-                        ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+                    *reinterpret_cast<uint32_t *>(dst + 8 * d) = Half<T>::pack(o[d][2 * e] * inv, o[d][2 * e + 1] * inv);
+                if (a.lse && qd == 0)
+                    a.lse[((uint64_t)ro[e].r * a.nq + ro[e].i) * (a.g * a.Hkv) + ro[e].h] =
+                        l[e] == 0.f ? -INFINITY : (m[e] + log2f(l[e])) * kLn2;
             } else {
-                const uint64_t at = ((uint64_t)blockIdx.x + p.item) * a.piece_rows + row;
-                float4 *dst = reinterpret_cast<float4 *>(a.part_o + at * D + part * (D / 8));
-                for (uint32_t d = 0; d < D / 32; d++) dst[d] = *reinterpret_cast<const float4 *>(src + 4 * d);
-                if (part == 0) a.part_ml[at] = make_float2(mm, ll);
+                const uint64_t at = (((uint64_t)blockIdx.x + p.item) * 4 + col) * a.piece_rows + (warp >> 2) * kRows + rw + 8 * e;
+                float *dst = a.part_o + at * D + 2 * qd;
+#pragma unroll
+                for (uint32_t d = 0; d < D / 8; d++)
+                    *reinterpret_cast<float2 *>(dst + 8 * d) = make_float2(o[d][2 * e], o[d][2 * e + 1]);
+                if (qd == 0) a.part_ml[at] = make_float2(m[e], l[e]);
             }
         }
-        group_sync(1, kConsumers * 32);
     }
     if (!ok && lane == 0) flag_why(a.status, CG_ERR_TIMEOUT, kWhyWait);
 }
@@ -794,72 +768,105 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm));
 }
 
-// Joins the pieces of each query row, a warp per row.
+// Joins the pieces of each query row, a warp per row: four groups of eight
+// lanes take every fourth piece, and the groups join at the end.
 template <class T, uint32_t D>
 __global__ void __launch_bounds__(256) k_merge(const Args a) {
-    const uint32_t lane = threadIdx.x & 31u;
-    const uint32_t Hq = a.g * a.Hkv;
+    const uint32_t lane = threadIdx.x & 31u, grp = lane >> 3, gl = lane & 7u;
+    const uint32_t Hq = a.g * a.Hkv, per = a.nq * a.g;
     const uint64_t row = ((uint64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
     if (row >= (uint64_t)a.R * a.nq * Hq) return;
     const uint32_t h = (uint32_t)(row % Hq), ri = (uint32_t)(row / Hq), i = ri % a.nq, r = ri / a.nq;
-    const uint32_t head = h / a.g, x = i * a.g + h % a.g;
-    constexpr uint32_t kPer = D / 32;
+    const uint32_t head = h / a.g, x = i * a.g + h % a.g, group = head / a.nh, hd = head - group * a.nh;
+    constexpr uint32_t kPer = D / 8;
     bool bad = false;
     const uint32_t len = tokens_of(a, r, &bad);
-    const uint64_t total = a.cum[a.R] + (uint64_t)a.npt * a.Hkv * tiles_of(a.P);
-    const uint64_t n_cta = min((uint64_t)a.n_cta, total);
-    float m = -INFINITY, l = 0.f, o[kPer];
-    for (uint32_t k = 0; k < kPer; k++) o[k] = 0.f;
-    // the pieces of one item: its tiles [t0, t0 + nt) are spread over blocks c0..c1
-    auto add = [&](const float2 *ml, const float *po, uint64_t at) {
-        const float2 v = ml[at];
-        if (v.y == 0.f) return;  // a piece the row sees nothing of
-        const float *src = po + at * D + lane * kPer;
-        const float nm = fmaxf(m, v.x);
-        const float f = m == nm ? 1.f : ex2(m - nm), e = v.x == nm ? 1.f : ex2(v.x - nm);
-        m = nm;
-        l = l * f + v.y * e;
-        for (uint32_t k = 0; k < kPer; k++) o[k] = o[k] * f + src[k] * e;
-    };
-    auto join = [&](uint64_t t0, uint32_t nt, uint32_t item, uint32_t local) {
-        const uint64_t c0 = ((t0 + 1) * n_cta - 1) / total, c1 = ((t0 + nt) * n_cta - 1) / total;
-        for (uint64_t c = c0; c <= c1; c++) add(a.part_ml, a.part_o, (c + item) * a.piece_rows + local);
-        return c0 == c1;
-    };
+    const uint64_t own = a.cum[a.R], total = own + (uint64_t)a.npt * a.ng * tiles_of(a, a.P);
+    const uint64_t n_cta = shares(a, total);
+    const uint32_t parts = 4 / a.nh;
+    // three runs of pieces: of k_shared, of the shared part in k_rows, of the request's own tokens
+    uint32_t n_tc = 0, n_sh = 0, n_own = 0;
+    uint64_t at_tc = 0, at_sh = 0, at_own = 0;
     if (len) {
+        const uint32_t xp = r * per + x;
         if (a.pairs) {
-            const uint32_t of = (a.P + kTcTok - 1) / kTcTok, xp = r * a.nq * a.g + x;
-            const uint32_t item = head * a.pairs + (xp >> 8);
+            const uint32_t of = (a.P + kTcTok - 1) / kTcTok, item = head * a.pairs + (xp >> 8);
             const uint64_t tt = (uint64_t)a.pairs * a.Hkv * of, n = min((uint64_t)a.n_tc, tt), t0 = (uint64_t)item * of;
             const uint64_t c0 = ((t0 + 1) * n - 1) / tt, c1 = ((t0 + of) * n - 1) / tt;
-            for (uint64_t c = c0; c <= c1; c++) {
-                add(a.tc_ml, a.tc_o, (c + item) * 256 + (xp & 255u));
-                if (a.one) add(a.tc_ml, a.tc_o, (c + item) * 256 + 128 + xp);
-            }
+            n_tc = (uint32_t)(c1 - c0 + 1) << a.one;
+            at_tc = (c0 + item) * 256 + (xp & 255u);
         }
-        const uint32_t nt = len > a.P ? tiles_of(len - a.P) : 0;
+        // tiles [t0, t0 + nt) of an item are spread over blocks c0..c1; a piece has `parts` parts of the row
+        auto run = [&](uint64_t t0, uint32_t nt, uint32_t item, uint32_t local, uint64_t &at) {
+            const uint64_t c0 = ((t0 + 1) * n_cta - 1) / total, c1 = ((t0 + nt) * n_cta - 1) / total;
+            at = ((c0 + item) * 4 + hd) * a.piece_rows + local;
+            return (uint32_t)(c1 - c0 + 1) * parts;
+        };
         if (a.npt) {
-            const uint32_t xp = r * a.nq * a.g + x, item = (xp / kRows) * a.Hkv + head;
-            const uint32_t ntp = tiles_of(a.P);
-            join(a.cum[a.R] + (uint64_t)item * ntp, ntp, a.R * a.rt * a.Hkv + item, xp % kRows);
+            const uint32_t item = xp / a.range_rows * a.ng + group, nt = tiles_of(a, a.P);
+            n_sh = run(own + (uint64_t)item * nt, nt, a.R * a.rt * a.ng + item, xp % a.range_rows, at_sh);
         }
+        const uint32_t nt = len > a.P ? tiles_of(a, len - a.P) : 0;
         if (nt) {
-            const uint32_t item = (x / kRows) * a.Hkv + head;
-            const bool one = join(a.cum[r] + (uint64_t)item * nt, nt, r * a.rt * a.Hkv + item, x % kRows);
-            if (one && a.P == 0) return;  // k_rows has written the answer
+            const uint32_t item = x / a.range_rows * a.ng + group;
+            n_own = run(a.cum[r] + (uint64_t)item * nt, nt, r * a.rt * a.ng + item, x % a.range_rows, at_own);
+            if (n_own == 1 && a.P == 0) return;  // k_rows has written the answer
         }
     }
+    float m = -INFINITY, l = 0.f, o[kPer];
+#pragma unroll
+    for (uint32_t k = 0; k < kPer; k++) o[k] = 0.f;
+    for (uint32_t e = grp; e < n_tc + n_sh + n_own; e += 4) {
+        const float2 *ml;
+        const float *src;
+        if (e < n_tc) {
+            const uint64_t at = at_tc + (e >> a.one) * 256ull + (e & a.one) * 128;
+            ml = a.tc_ml + at;
+            src = a.tc_o + at * D;
+        } else {
+            const uint32_t f = e - n_tc < n_sh ? e - n_tc : e - n_tc - n_sh;
+            const uint64_t at = (e - n_tc < n_sh ? at_sh : at_own) + ((f / parts) * 4ull + (f % parts) * a.nh) * a.piece_rows;
+            ml = a.part_ml + at;
+            src = a.part_o + at * D;
+        }
+        const float2 v = *ml;
+        if (v.y == 0.f) continue;  // a piece the row sees nothing of
+        const float nm = fmaxf(m, v.x);
+        const float f = m == nm ? 1.f : ex2(m - nm), w = v.x == nm ? 1.f : ex2(v.x - nm);
+        m = nm;
+        l = l * f + v.y * w;
+#pragma unroll
+        for (uint32_t k = 0; k < kPer / 4; k++) {
+            const float4 y = *reinterpret_cast<const float4 *>(src + 4 * (gl + 8 * k));
+            o[4 * k] = o[4 * k] * f + y.x * w;
+            o[4 * k + 1] = o[4 * k + 1] * f + y.y * w;
+            o[4 * k + 2] = o[4 * k + 2] * f + y.z * w;
+            o[4 * k + 3] = o[4 * k + 3] * f + y.w * w;
+        }
+    }
+#pragma unroll
+    for (uint32_t d = 8; d < 32; d <<= 1) {
+        const float om = __shfl_xor_sync(kFull, m, d), ol = __shfl_xor_sync(kFull, l, d), nm = fmaxf(m, om);
+        const float f = m == nm ? 1.f : ex2(m - nm), w = om == nm ? 1.f : ex2(om - nm);
+        m = nm;
+        l = l * f + ol * w;
+#pragma unroll
+        for (uint32_t k = 0; k < kPer; k++) o[k] = o[k] * f + __shfl_xor_sync(kFull, o[k], d) * w;
+    }
+    if (grp) return;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint16_t *dst = a.out + r * a.os[0] + i * a.os[1] + h * a.os[2] + lane * kPer;
-    for (uint32_t k = 0; k < kPer; k += 2)
-        *reinterpret_cast<uint32_t *>(dst + k) = Half<T>::pack(o[k] * inv, o[k + 1] * inv);
-    if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    uint16_t *dst = a.out + r * a.os[0] + i * a.os[1] + h * a.os[2];
+#pragma unroll
+    for (uint32_t k = 0; k < kPer / 4; k++)
+        *reinterpret_cast<uint2 *>(dst + 4 * (gl + 8 * k)) =
+            make_uint2(Half<T>::pack(o[4 * k] * inv, o[4 * k + 1] * inv), Half<T>::pack(o[4 * k + 2] * inv, o[4 * k + 3] * inv));
+    if (a.lse && gl == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 bool misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1u)) != 0; }
 
 struct Plan {
-    uint32_t g, rt, npt, pairs, one, piece_rows;
+    uint32_t g, nh, ng, range_rows, rt, npt, pairs, one, piece_rows;
     uint64_t items, pieces, cum_bytes, o_bytes, ml_bytes, tc_o_bytes, bytes;
 };
 
@@ -889,18 +896,23 @@ bool make_plan(const cg_pages *p, const cg_attention *a, Plan *o) {
     o->g = a->n_q_heads / a->n_kv_heads;
     const uint64_t per = (uint64_t)a->n_queries * o->g, all = per * a->n_requests;
     if (all * a->n_kv_heads > (1ull << 31)) return false;
-    o->rt = (uint32_t)((per + kRows - 1) / kRows);
+    o->nh = a->n_kv_heads % 4 == 0 ? 4 : a->n_kv_heads % 2 == 0 ? 2 : 1;
+    o->ng = a->n_kv_heads / o->nh;
     const bool tc = a->shared_blocks && all > kTcRows;
     o->pairs = tc ? (uint32_t)((all + 255) / 256) : 0;
     o->one = all <= 128;
-    o->npt = a->shared_blocks && !tc ? (uint32_t)((all + kRows - 1) / kRows) : 0;
-    o->piece_rows = o->npt ? (uint32_t)(all < kRows ? all : kRows) : (uint32_t)(per < kRows ? per : kRows);
-    o->items = ((uint64_t)a->n_requests * o->rt + o->npt) * a->n_kv_heads;
+    const bool here = a->shared_blocks && !tc;  // the shared part goes through k_rows too
+    const uint64_t most = here ? all : per;
+    o->range_rows = most > kRows ? 2 * kRows : kRows;
+    o->rt = (uint32_t)((per + o->range_rows - 1) / o->range_rows);
+    o->npt = here ? (uint32_t)((all + o->range_rows - 1) / o->range_rows) : 0;
+    o->piece_rows = (uint32_t)(most < o->range_rows ? most : o->range_rows);
+    o->items = ((uint64_t)a->n_requests * o->rt + o->npt) * o->ng;
     if (o->items > (1ull << 31)) return false;
     o->pieces = o->items + kMaxCtas;
     o->cum_bytes = round_up((a->n_requests + 1ull) * 8, 256);
-    o->o_bytes = round_up(o->pieces * o->piece_rows * a->head_dim * 4, 256);
-    o->ml_bytes = round_up(o->pieces * o->piece_rows * 8, 256);
+    o->o_bytes = round_up(o->pieces * 4 * o->piece_rows * a->head_dim * 4, 256);
+    o->ml_bytes = round_up(o->pieces * 4 * o->piece_rows * 8, 256);
     const uint64_t tc_rows = tc ? ((uint64_t)o->pairs * a->n_kv_heads + kMaxCtas) * 256 : 0;
     o->tc_o_bytes = tc_rows * a->head_dim * 4;
     o->bytes = o->cum_bytes + o->o_bytes + o->ml_bytes + o->tc_o_bytes + tc_rows * 8;
@@ -936,10 +948,20 @@ bool make_map(const cg_pages *p, const cg_attention *a, uint32_t rows, CUtensorM
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class T, uint32_t D>
-cudaError_t launch(const CUtensorMap &map, Args &a, int sms, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(k_rows<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+template <class T, uint32_t D, uint32_t kR>
+cudaError_t launch_rows(const CUtensorMap &map, Args &a, int sms, cudaStream_t s) {
+    using S = Smem<D, kR>;
+    cudaError_t e = cudaFuncSetAttribute(k_rows<T, D, kR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
     if (e != cudaSuccess) return e;
+    const uint32_t n = (uint32_t)sms * (3 - kR);
+    a.n_cta = n < kMaxCtas ? n : kMaxCtas;
+    k_rows<T, D, kR><<<a.n_cta, S::kThreads, S::kBytes, s>>>(map, a);
+    return cudaGetLastError();
+}
+
+template <class T, uint32_t D>
+cudaError_t launch(const CUtensorMap &rows_map, const CUtensorMap &map, Args &a, int sms, cudaStream_t s) {
+    cudaError_t e;
     if (a.pairs) {
         e = cudaFuncSetAttribute(k_shared<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<D>::kBytes);
         if (e != cudaSuccess) return e;
@@ -948,9 +970,7 @@ cudaError_t launch(const CUtensorMap &map, Args &a, int sms, cudaStream_t s) {
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    a.n_cta = (uint32_t)sms * 2u < kMaxCtas ? (uint32_t)sms * 2u : kMaxCtas;
-    k_rows<T, D><<<a.n_cta, kThreads, Smem<D>::kBytes, s>>>(map, a);
-    e = cudaGetLastError();
+    e = a.range_rows == kRows ? launch_rows<T, D, 1>(rows_map, a, sms, s) : launch_rows<T, D, 2>(rows_map, a, sms, s);
     if (e != cudaSuccess) return e;
     const uint64_t rows = (uint64_t)a.R * a.nq * a.g * a.Hkv;
     k_merge<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a);
@@ -978,8 +998,10 @@ extern "C" cg_status cg_attend(const cg_pages *p, const cg_attention *at, void *
     CG_CUDA_TRY(cudaGetDevice(&dev));
     CG_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
     const uint32_t bshift = (uint32_t)__builtin_ctz(p->block_tokens);
-    CUtensorMap map;
-    if (!make_map(p, at, p->block_tokens < kTok ? p->block_tokens : kTok, &map)) return CG_ERR_CUDA;
+    // boxes of k_rows are at most a tile high, those of k_shared 64 rows
+    const uint32_t tt = kTileRows / pl.nh, bt = p->block_tokens;
+    CUtensorMap map, rows_map;
+    if (!make_map(p, at, bt < tt ? bt : tt, &rows_map) || !make_map(p, at, bt < 64 ? bt : 64, &map)) return CG_ERR_CUDA;
     Args a{};
     a.q = at->q;
     a.out = at->out;
@@ -997,6 +1019,10 @@ extern "C" cg_status cg_attend(const cg_pages *p, const cg_attention *at, void *
     a.Hkv = at->n_kv_heads;
     a.P = at->shared_blocks << bshift;
     a.shared_slot = at->shared_slot;
+    a.nh = pl.nh;
+    a.ng = pl.ng;
+    a.tlog = (uint32_t)__builtin_ctz(tt);
+    a.range_rows = pl.range_rows;
     a.rt = pl.rt;
     a.npt = pl.npt;
     for (int k = 0; k < 3; k++) {
@@ -1017,7 +1043,7 @@ extern "C" cg_status cg_attend(const cg_pages *p, const cg_attention *at, void *
     a.tc_ml = reinterpret_cast<float2 *>(w + pl.cum_bytes + pl.o_bytes + pl.ml_bytes + pl.tc_o_bytes);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool fp16 = at->dtype == CG_FP16;
-    if (at->head_dim == 128) CG_CUDA_TRY((fp16 ? launch<__half, 128>(map, a, sms, s) : launch<__nv_bfloat16, 128>(map, a, sms, s)));
-    else CG_CUDA_TRY((fp16 ? launch<__half, 64>(map, a, sms, s) : launch<__nv_bfloat16, 64>(map, a, sms, s)));
+    if (at->head_dim == 128) CG_CUDA_TRY((fp16 ? launch<__half, 128>(rows_map, map, a, sms, s) : launch<__nv_bfloat16, 128>(rows_map, map, a, sms, s)));
+    else CG_CUDA_TRY((fp16 ? launch<__half, 64>(rows_map, map, a, sms, s) : launch<__nv_bfloat16, 64>(rows_map, map, a, sms, s)));
     return CG_OK;
 }
