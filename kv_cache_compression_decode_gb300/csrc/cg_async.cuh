@@ -162,6 +162,31 @@ template <> struct Half<__nv_bfloat16> {
     static __device__ __forceinline__ __nv_bfloat16 one(float x) { return __float2bfloat16_rn(x); }
 };
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ void fma2(float &x, float &y, float a, float b, float m, float c) {
+    asm("{\n\t.reg .b64 s, t, u, v;\n\tmov.b64 s, {%2, %3};\n\tmov.b64 t, {%4, %4};\n\tmov.b64 u, {%5, %5};\n\t"
+        "fma.rn.f32x2 v, s, t, u;\n\tmov.b64 {%0, %1}, v;\n\t}"
+        : "=f"(x), "=f"(y)
+        : "f"(a), "f"(b), "f"(m), "f"(c));
+}
+__device__ __forceinline__ void add2(float &x, float &y, float a, float b) {
+    asm("{\n\t.reg .b64 s, t, v;\n\tmov.b64 s, {%0, %1};\n\tmov.b64 t, {%2, %3};\n\t"
+        "add.rn.f32x2 v, s, t;\n\tmov.b64 {%0, %1}, v;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void mul2(float &x, float &y, float f) {
+    asm("{\n\t.reg .b64 s, t, v;\n\tmov.b64 s, {%0, %1};\n\tmov.b64 t, {%2, %2};\n\t"
+        "mul.rn.f32x2 v, s, t;\n\tmov.b64 {%0, %1}, v;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(f));
+}
+
+// Programmatic launch: the next kernel of the stream may start, and wait for
+// the kernels before this one to be complete and their writes visible.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

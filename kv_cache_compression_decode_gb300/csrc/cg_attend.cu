@@ -36,6 +36,7 @@ struct Args {
     uint32_t pairs;          // k_shared: pairs of 128-row tiles of the whole batch (0: k_rows has the shared part)
     uint32_t one;            // k_shared: the batch fits one 128-row tile
     uint32_t n_tc;           // blocks of k_shared
+    uint32_t merge_rows;     // rows of a warp of k_merge
     uint32_t n_cta;          // blocks of k_rows
     uint64_t qs[3], os[3];
     float scale2;            // |scale| * log2 e
@@ -278,9 +279,11 @@ __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __
                 bar_wait(full + 8 * (k % kStages), (k / kStages) & 1u);
             if (lane == 0) flag_why(a.status, CG_ERR_TIMEOUT, kWhyWait);
         }
+        if (a.pairs) wait_for_previous();  // this kernel is complete only after k_shared, whose pieces k_merge reads
         return;
     }
 
+    let_next_start();
     const uint32_t qd = lane & 3u, rw = lane >> 2;
     const uint32_t col = warp & 3u, hd = col % a.nh, part = col / a.nh;  // head of the group, 16 tokens of the tile
     const uint32_t kbase = hd * head_bytes + part * 16 * 128, vbase = S::kTile + kbase;
@@ -488,15 +491,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (s_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t sm = s_addr(smem), tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
-    // barriers: slot full / empty, then per stream: scores ready, weights ready, output ready; queries ready; drain
+    // barriers: slot full / empty, then per stream: scores ready, weights ready (two halves), output ready;
+    // queries ready; drain
     const uint32_t full = sm + M::oBar, empty = full + 8 * kTcSlots, s_rdy = empty + 8 * kTcSlots, p_rdy = s_rdy + 16,
-                   o_rdy = p_rdy + 16, q_rdy = o_rdy + 16, drain = q_rdy + 8;
-    uint32_t *tm_at = reinterpret_cast<uint32_t *>(smem + M::oBar + 8 * (2 * kTcSlots + 8));
+                   o_rdy = p_rdy + 32, q_rdy = o_rdy + 16, drain = q_rdy + 8;
+    uint32_t *tm_at = reinterpret_cast<uint32_t *>(smem + M::oBar + 8 * (2 * kTcSlots + 10));
     if (tid == 0) {
         for (uint32_t k = 0; k < 2 * kTcSlots; k++) bar_init(full + 8 * k, 1);
         for (uint32_t s = 0; s < 2; s++) {
             bar_init(s_rdy + 8 * s, 1);
-            bar_init(p_rdy + 8 * s, 128);
+            bar_init(p_rdy + 16 * s, 128);
+            bar_init(p_rdy + 16 * s + 8, 128);
             bar_init(o_rdy + 8 * s, 1);
         }
         bar_init(q_rdy, 256);
@@ -511,6 +516,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = *tm_at;
+    let_next_start();
 
     const uint32_t of = (a.P + kTcTok - 1) / kTcTok;  // tiles of an item
     const uint64_t total = (uint64_t)a.pairs * a.Hkv * of;
@@ -583,13 +589,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
                     tc_commit(s_rdy + 8 * s);
                 };
                 auto pv = [&](uint32_t s, uint32_t c, bool first) {
-                    if (ok) ok = bar_wait(p_rdy + 8 * s, np[s]++ & 1u);
-                    tc_fence_after();
-                    if (!ok) return;
                     const uint32_t v = mma_desc(sm + (c % kTcSlots) * M::kTile, false, M::kHalf);
-    #pragma unroll
-                    for (uint32_t x = 0; x < kTcTok / 16; x++)
-                        tc_mma_ts(tm + Tmem<D>::O(s), tm + Tmem<D>::P(s) + 8 * x, v + x * 128, kPv, !first || x != 0);
+#pragma unroll
+                    for (uint32_t h = 0; h < 2; h++) {
+                        if (ok) ok = bar_wait(p_rdy + 16 * s + 8 * h, np[s] & 1u);
+                        tc_fence_after();
+                        if (!ok) return;
+#pragma unroll
+                        for (uint32_t x = h * (kTcTok / 32); x < (h + 1) * (kTcTok / 32); x++)
+                            tc_mma_ts(tm + Tmem<D>::O(s), tm + Tmem<D>::P(s) + 8 * x, v + x * 128, kPv, !first || x != 0);
+                    }
+                    np[s]++;
                 };
                 auto free_slot = [&](uint32_t c) {
                     if (ok) tc_commit(empty + 8 * (c % kTcSlots));
@@ -693,11 +703,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
                         for (uint32_t j = 0; j < 32; j++)
                             if (32 * c + j >= left) x[c][j] = 0xFF800000u;
                 }
-                float mx = -INFINITY;
+                float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (uint32_t c = 0; c < 4; c++)
 #pragma unroll
-                    for (uint32_t j = 0; j < 32; j++) mx = fmaxf(mx, __uint_as_float(x[c][j]));
+                    for (uint32_t j = 0; j < 32; j += 2)
+                        mq[(j >> 1) & 3u] = fmaxf(fmaxf(mq[(j >> 1) & 3u], __uint_as_float(x[c][j])), __uint_as_float(x[c][j + 1]));
+                float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
                 mx = mx == -INFINITY ? mx : mx * a.scale2;
                 const bool grow = k == 0 || mx - m > kGrow;
                 if (__any_sync(kFull, grow)) {
@@ -717,24 +729,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
                     }
                 }
                 const float z = m == -INFINITY ? 0.f : kShift - m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                float su[2] = {0.f, 0.f}, sv[2] = {0.f, 0.f};
 #pragma unroll
-                for (uint32_t c = 0; c < 2; c++) {
+                for (uint32_t c = 0; c < 2; c++) {  // half a tile: the MMAs on it start while the other half is made
                     uint32_t w[32];
 #pragma unroll
                     for (uint32_t j = 0; j < 32; j++) {
                         const uint32_t e = 2 * j;
-                        const float u = ex2(fmaf(__uint_as_float(x[2 * c + (e >> 5)][e & 31u]), a.scale2, z));
-                        const float v = ex2(fmaf(__uint_as_float(x[2 * c + (e >> 5)][(e & 31u) + 1]), a.scale2, z));
-                        sum[j & 3u] += u + v;
+                        float u, v;
+                        fma2(u, v, __uint_as_float(x[2 * c + (e >> 5)][e & 31u]),
+                             __uint_as_float(x[2 * c + (e >> 5)][(e & 31u) + 1]), a.scale2, z);
+                        u = ex2(u);
+                        v = ex2(v);
+                        add2(su[j & 1u], sv[j & 1u], u, v);
                         w[j] = Half<T>::pack(u, v);
                     }
                     tc_st32(tml + Tmem<D>::P(s) + 32 * c, w);
+                    tc_wait_st();
+                    tc_fence_before();
+                    bar_arrive(p_rdy + 16 * s + 8 * c);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tc_wait_st();
-                tc_fence_before();
-                bar_arrive(p_rdy + 8 * s);
+                l += (su[0] + su[1]) + (sv[0] + sv[1]);
             }
             // the piece's result
             const uint64_t at = (((uint64_t)blockIdx.x + p.item) * 2 + s) * 128 + rl;
@@ -768,99 +783,108 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm));
 }
 
-// Joins the pieces of each query row, a warp per row: four groups of eight
-// lanes take every fourth piece, and the groups join at the end.
+// Joins the pieces of the query rows.  A warp takes a.merge_rows rows of one
+// request and KV head, whose pieces lie in the same places; four groups of
+// eight lanes take every fourth piece of a row and join at the end.
 template <class T, uint32_t D>
 __global__ void __launch_bounds__(256) k_merge(const Args a) {
+    wait_for_previous();
     const uint32_t lane = threadIdx.x & 31u, grp = lane >> 3, gl = lane & 7u;
-    const uint32_t Hq = a.g * a.Hkv, per = a.nq * a.g;
-    const uint64_t row = ((uint64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
-    if (row >= (uint64_t)a.R * a.nq * Hq) return;
-    const uint32_t h = (uint32_t)(row % Hq), ri = (uint32_t)(row / Hq), i = ri % a.nq, r = ri / a.nq;
-    const uint32_t head = h / a.g, x = i * a.g + h % a.g, group = head / a.nh, hd = head - group * a.nh;
+    const uint32_t per = a.nq * a.g, chunks = (per + a.merge_rows - 1) / a.merge_rows;
+    const uint32_t id = blockIdx.x * 8 + (threadIdx.x >> 5);  // at most 2^31 rows
+    if (id >= a.R * a.Hkv * chunks) return;
+    const uint32_t rh = id / chunks, r = rh / a.Hkv, head = rh - r * a.Hkv, x_begin = (id - rh * chunks) * a.merge_rows;
+    const uint32_t x_end = min(x_begin + a.merge_rows, per);
+    const uint32_t group = head / a.nh, hd = head - group * a.nh, parts = 4 / a.nh;
     constexpr uint32_t kPer = D / 8;
     bool bad = false;
-    const uint32_t len = tokens_of(a, r, &bad);
-    const uint64_t own = a.cum[a.R], total = own + (uint64_t)a.npt * a.ng * tiles_of(a, a.P);
+    const uint32_t len = tokens_of(a, r, &bad), nt_sh = a.npt ? tiles_of(a, a.P) : 0;
+    const uint32_t nt_own = len > a.P ? tiles_of(a, len - a.P) : 0;
+    const uint64_t own = a.cum[a.R], first = a.cum[r], total = own + (uint64_t)a.npt * a.ng * nt_sh;
     const uint64_t n_cta = shares(a, total);
-    const uint32_t parts = 4 / a.nh;
-    // three runs of pieces: of k_shared, of the shared part in k_rows, of the request's own tokens
-    uint32_t n_tc = 0, n_sh = 0, n_own = 0;
+    const uint32_t of = (a.P + kTcTok - 1) / kTcTok;
+    const uint64_t total_tc = (uint64_t)a.pairs * a.Hkv * of, n_cta_tc = min((uint64_t)a.n_tc, total_tc);
+    // three runs of pieces: of k_shared, of the shared part in k_rows, of the
+    // request's own tokens; tiles [t0, t0 + nt) of an item are spread over blocks c0..c1
+    uint32_t item_tc = ~0u, item_sh = ~0u, item_own = ~0u, n_tc = 0, n_sh = 0, n_own = 0;
     uint64_t at_tc = 0, at_sh = 0, at_own = 0;
-    if (len) {
+    auto run = [](uint64_t t0, uint32_t nt, uint64_t n, uint64_t all, uint64_t &c0) {
+        c0 = ((t0 + 1) * n - 1) / all;
+        return (uint32_t)(((t0 + nt) * n - 1) / all - c0) + 1;
+    };
+    for (uint32_t x = x_begin; x < x_end; x++) {
         const uint32_t xp = r * per + x;
-        if (a.pairs) {
-            const uint32_t of = (a.P + kTcTok - 1) / kTcTok, item = head * a.pairs + (xp >> 8);
-            const uint64_t tt = (uint64_t)a.pairs * a.Hkv * of, n = min((uint64_t)a.n_tc, tt), t0 = (uint64_t)item * of;
-            const uint64_t c0 = ((t0 + 1) * n - 1) / tt, c1 = ((t0 + of) * n - 1) / tt;
-            n_tc = (uint32_t)(c1 - c0 + 1) << a.one;
-            at_tc = (c0 + item) * 256 + (xp & 255u);
+        if (len && a.pairs && item_tc != head * a.pairs + (xp >> 8)) {
+            item_tc = head * a.pairs + (xp >> 8);
+            n_tc = run((uint64_t)item_tc * of, of, n_cta_tc, total_tc, at_tc) << a.one;
+            at_tc = (at_tc + item_tc) * 256;
         }
-        // tiles [t0, t0 + nt) of an item are spread over blocks c0..c1; a piece has `parts` parts of the row
-        auto run = [&](uint64_t t0, uint32_t nt, uint32_t item, uint32_t local, uint64_t &at) {
-            const uint64_t c0 = ((t0 + 1) * n_cta - 1) / total, c1 = ((t0 + nt) * n_cta - 1) / total;
-            at = ((c0 + item) * 4 + hd) * a.piece_rows + local;
-            return (uint32_t)(c1 - c0 + 1) * parts;
-        };
-        if (a.npt) {
-            const uint32_t item = xp / a.range_rows * a.ng + group, nt = tiles_of(a, a.P);
-            n_sh = run(own + (uint64_t)item * nt, nt, a.R * a.rt * a.ng + item, xp % a.range_rows, at_sh);
+        if (len && a.npt && item_sh != xp / a.range_rows * a.ng + group) {
+            item_sh = xp / a.range_rows * a.ng + group;
+            n_sh = run(own + (uint64_t)item_sh * nt_sh, nt_sh, n_cta, total, at_sh) * parts;
+            at_sh = ((at_sh + a.R * a.rt * a.ng + item_sh) * 4 + hd) * a.piece_rows;
         }
-        const uint32_t nt = len > a.P ? tiles_of(a, len - a.P) : 0;
-        if (nt) {
-            const uint32_t item = x / a.range_rows * a.ng + group;
-            n_own = run(a.cum[r] + (uint64_t)item * nt, nt, r * a.rt * a.ng + item, x % a.range_rows, at_own);
-            if (n_own == 1 && a.P == 0) return;  // k_rows has written the answer
+        if (nt_own && item_own != x / a.range_rows * a.ng + group) {
+            item_own = x / a.range_rows * a.ng + group;
+            n_own = run(first + (uint64_t)item_own * nt_own, nt_own, n_cta, total, at_own) * parts;
+            at_own = ((at_own + r * a.rt * a.ng + item_own) * 4 + hd) * a.piece_rows;
         }
+        if (n_own == 1 && a.P == 0) continue;  // k_rows has written the answer
+        float m = -INFINITY, l = 0.f, o[kPer];
+#pragma unroll
+        for (uint32_t k = 0; k < kPer; k++) o[k] = 0.f;
+        for (uint32_t e = grp; e < n_tc + n_sh + n_own; e += 4) {
+            const float2 *ml;
+            const float *src;
+            if (e < n_tc) {
+                const uint64_t at = at_tc + (xp & 255u) + (e >> a.one) * 256ull + (e & a.one) * 128;
+                ml = a.tc_ml + at;
+                src = a.tc_o + at * D;
+            } else {
+                const bool sh = e - n_tc < n_sh;
+                const uint32_t f = sh ? e - n_tc : e - n_tc - n_sh;
+                const uint64_t at = (sh ? at_sh + xp % a.range_rows : at_own + x % a.range_rows) +
+                                    (f / parts * 4ull + f % parts * a.nh) * a.piece_rows;
+                ml = a.part_ml + at;
+                src = a.part_o + at * D;
+            }
+            const float2 v = *ml;
+            float4 y[kPer / 4];
+#pragma unroll
+            for (uint32_t k = 0; k < kPer / 4; k++) y[k] = *reinterpret_cast<const float4 *>(src + 4 * (gl + 8 * k));
+            if (v.y == 0.f) continue;  // a piece the row sees nothing of; its outputs may be unwritten
+            const float nm = fmaxf(m, v.x);
+            const float f = m == nm ? 1.f : ex2(m - nm), w = v.x == nm ? 1.f : ex2(v.x - nm);
+            m = nm;
+            l = l * f + v.y * w;
+#pragma unroll
+            for (uint32_t k = 0; k < kPer / 4; k++) {
+                o[4 * k] = o[4 * k] * f + y[k].x * w;
+                o[4 * k + 1] = o[4 * k + 1] * f + y[k].y * w;
+                o[4 * k + 2] = o[4 * k + 2] * f + y[k].z * w;
+                o[4 * k + 3] = o[4 * k + 3] * f + y[k].w * w;
+            }
+        }
+#pragma unroll
+        for (uint32_t d = 8; d < 32; d <<= 1) {
+            const float om = __shfl_xor_sync(kFull, m, d), ol = __shfl_xor_sync(kFull, l, d), nm = fmaxf(m, om);
+            const float f = m == nm ? 1.f : ex2(m - nm), w = om == nm ? 1.f : ex2(om - nm);
+            m = nm;
+            l = l * f + ol * w;
+#pragma unroll
+            for (uint32_t k = 0; k < kPer; k++) o[k] = o[k] * f + __shfl_xor_sync(kFull, o[k], d) * w;
+        }
+        if (grp) continue;
+        const uint32_t i = x / a.g, h = head * a.g + x - i * a.g;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint16_t *dst = a.out + r * a.os[0] + i * a.os[1] + h * a.os[2];
+#pragma unroll
+        for (uint32_t k = 0; k < kPer / 4; k++)
+            *reinterpret_cast<uint2 *>(dst + 4 * (gl + 8 * k)) = make_uint2(
+                Half<T>::pack(o[4 * k] * inv, o[4 * k + 1] * inv), Half<T>::pack(o[4 * k + 2] * inv, o[4 * k + 3] * inv));
+        if (a.lse && gl == 0)
+            a.lse[((uint64_t)r * a.nq + i) * (a.g * a.Hkv) + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
-    float m = -INFINITY, l = 0.f, o[kPer];
-#pragma unroll
-    for (uint32_t k = 0; k < kPer; k++) o[k] = 0.f;
-    for (uint32_t e = grp; e < n_tc + n_sh + n_own; e += 4) {
-        const float2 *ml;
-        const float *src;
-        if (e < n_tc) {
-            const uint64_t at = at_tc + (e >> a.one) * 256ull + (e & a.one) * 128;
-            ml = a.tc_ml + at;
-            src = a.tc_o + at * D;
-        } else {
-            const uint32_t f = e - n_tc < n_sh ? e - n_tc : e - n_tc - n_sh;
-            const uint64_t at = (e - n_tc < n_sh ? at_sh : at_own) + ((f / parts) * 4ull + (f % parts) * a.nh) * a.piece_rows;
-            ml = a.part_ml + at;
-            src = a.part_o + at * D;
-        }
-        const float2 v = *ml;
-        if (v.y == 0.f) continue;  // a piece the row sees nothing of
-        const float nm = fmaxf(m, v.x);
-        const float f = m == nm ? 1.f : ex2(m - nm), w = v.x == nm ? 1.f : ex2(v.x - nm);
-        m = nm;
-        l = l * f + v.y * w;
-#pragma unroll
-        for (uint32_t k = 0; k < kPer / 4; k++) {
-            const float4 y = *reinterpret_cast<const float4 *>(src + 4 * (gl + 8 * k));
-            o[4 * k] = o[4 * k] * f + y.x * w;
-            o[4 * k + 1] = o[4 * k + 1] * f + y.y * w;
-            o[4 * k + 2] = o[4 * k + 2] * f + y.z * w;
-            o[4 * k + 3] = o[4 * k + 3] * f + y.w * w;
-        }
-    }
-#pragma unroll
-    for (uint32_t d = 8; d < 32; d <<= 1) {
-        const float om = __shfl_xor_sync(kFull, m, d), ol = __shfl_xor_sync(kFull, l, d), nm = fmaxf(m, om);
-        const float f = m == nm ? 1.f : ex2(m - nm), w = om == nm ? 1.f : ex2(om - nm);
-        m = nm;
-        l = l * f + ol * w;
-#pragma unroll
-        for (uint32_t k = 0; k < kPer; k++) o[k] = o[k] * f + __shfl_xor_sync(kFull, o[k], d) * w;
-    }
-    if (grp) return;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint16_t *dst = a.out + r * a.os[0] + i * a.os[1] + h * a.os[2];
-#pragma unroll
-    for (uint32_t k = 0; k < kPer / 4; k++)
-        *reinterpret_cast<uint2 *>(dst + 4 * (gl + 8 * k)) =
-            make_uint2(Half<T>::pack(o[4 * k] * inv, o[4 * k + 1] * inv), Half<T>::pack(o[4 * k + 2] * inv, o[4 * k + 3] * inv));
-    if (a.lse && gl == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 bool misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1u)) != 0; }
@@ -870,7 +894,7 @@ struct Plan {
     uint64_t items, pieces, cum_bytes, o_bytes, ml_bytes, tc_o_bytes, bytes;
 };
 
-constexpr uint32_t kTcRows = 32;    // k_shared takes the shared part from more query rows than this per KV head
+constexpr uint32_t kTcRows = 16;    // k_shared takes the shared part from more query rows than this per KV head
 constexpr uint32_t kMaxCtas = 512;  // bound of the grid that the workspace is sized for
 
 bool make_plan(const cg_pages *p, const cg_attention *a, Plan *o) {
@@ -948,6 +972,23 @@ bool make_map(const cg_pages *p, const cg_attention *a, uint32_t rows, CUtensorM
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A kernel that may start, with `early`, while the one before it runs.
+template <class... P, class... A>
+cudaError_t launch_next(void (*k)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s, bool early,
+                        const A &...args) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = block;
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &at;
+    c.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&c, k, args...);
+}
+
 template <class T, uint32_t D, uint32_t kR>
 cudaError_t launch_rows(const CUtensorMap &map, Args &a, int sms, cudaStream_t s) {
     using S = Smem<D, kR>;
@@ -955,8 +996,7 @@ cudaError_t launch_rows(const CUtensorMap &map, Args &a, int sms, cudaStream_t s
     if (e != cudaSuccess) return e;
     const uint32_t n = (uint32_t)sms * (3 - kR);
     a.n_cta = n < kMaxCtas ? n : kMaxCtas;
-    k_rows<T, D, kR><<<a.n_cta, S::kThreads, S::kBytes, s>>>(map, a);
-    return cudaGetLastError();
+    return launch_next(k_rows<T, D, kR>, a.n_cta, S::kThreads, S::kBytes, s, a.pairs != 0, map, a);
 }
 
 template <class T, uint32_t D>
@@ -965,16 +1005,24 @@ cudaError_t launch(const CUtensorMap &rows_map, const CUtensorMap &map, Args &a,
     if (a.pairs) {
         e = cudaFuncSetAttribute(k_shared<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<D>::kBytes);
         if (e != cudaSuccess) return e;
-        a.n_tc = (uint32_t)sms < kMaxCtas ? (uint32_t)sms : kMaxCtas;
-        k_shared<T, D><<<a.n_tc, kTcThreads, TcSmem<D>::kBytes, s>>>(map, a);
-        e = cudaGetLastError();
+        // An even deal of all tiles lets a block cross from one item to the
+        // next, which costs about kCross tiles (the streams drain, new
+        // queries come in); where whole blocks per item take no longer than that, deal so.
+        constexpr uint64_t kCross = 4;
+        const uint64_t n = (uint64_t)sms < kMaxCtas ? sms : kMaxCtas, items = (uint64_t)a.pairs * a.Hkv;
+        const uint64_t of = (a.P + kTcTok - 1) / kTcTok, k = n / items < of ? n / items : of;
+        a.n_tc = (uint32_t)(k && (of + k - 1) / k <= items * of / n + kCross ? k * items : n);
+        e = launch_next(k_shared<T, D>, a.n_tc, kTcThreads, TcSmem<D>::kBytes, s, false, map, a);
         if (e != cudaSuccess) return e;
     }
     e = a.range_rows == kRows ? launch_rows<T, D, 1>(rows_map, a, sms, s) : launch_rows<T, D, 2>(rows_map, a, sms, s);
     if (e != cudaSuccess) return e;
-    const uint64_t rows = (uint64_t)a.R * a.nq * a.g * a.Hkv;
-    k_merge<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a);
-    return cudaGetLastError();
+    // a few rows a warp where there are rows enough to fill the GPU
+    const uint64_t per = (uint64_t)a.nq * a.g, rows = (uint64_t)a.R * a.Hkv * per;
+    const uint64_t want = rows / ((uint64_t)sms * 32);
+    a.merge_rows = (uint32_t)(want < 1 ? 1 : want < per ? want : per);
+    const uint64_t warps = (uint64_t)a.R * a.Hkv * ((per + a.merge_rows - 1) / a.merge_rows);
+    return launch_next(k_merge<T, D>, (unsigned)((warps + 7) / 8), 256, 0, s, true, a);
 }
 
 }  // namespace
