@@ -490,7 +490,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
     constexpr bool kBf16 = sizeof(T) == 2 && !__is_same(T, __half);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (s_addr(smem_raw) & 1023u)) & 1023u);
-    const uint32_t sm = s_addr(smem), tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+    const uint32_t sm = s_addr(smem), tid = threadIdx.x, lane = tid & 31u;
+    const uint32_t warp = __shfl_sync(kFull, tid >> 5, 0);
     // barriers: slot full / empty, then per stream: scores ready, weights ready (two halves), output ready;
     // queries ready; drain
     const uint32_t full = sm + M::oBar, empty = full + 8 * kTcSlots, s_rdy = empty + 8 * kTcSlots, p_rdy = s_rdy + 16,
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
     }
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm = *tm_at;
+    const uint32_t tm = __shfl_sync(kFull, *tm_at, 0);  // the same in every lane, and known to be
     let_next_start();
 
     const uint32_t of = (a.P + kTcTok - 1) / kTcTok;  // tiles of an item
@@ -570,92 +571,89 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
                 if (lane == 0) flag_why(a.status, CG_ERR_TIMEOUT, kWhyWait);
             }
         } else if (warp == 9) {
-            if (lane == 0) {
-                constexpr uint32_t kQk = mma_shape(kBf16, kTcTok, true), kPv = mma_shape(kBf16, D, false);
-                uint32_t cnt = 0, piece = 0, np[2] = {0, 0};
-                auto slot_ready = [&](uint32_t c) {
-                    if (ok) ok = bar_wait(full + 8 * (c % kTcSlots), (c / kTcSlots) & 1u);
-                    tc_fence_after();
-                };
-                auto qk = [&](uint32_t s, uint32_t c) {
-                    if (!ok) return;
-                    const uint32_t q = mma_desc(sm + M::oQ + (a.one ? 0 : s) * M::kTile, true, 0),
-                                   k = mma_desc(sm + (c % kTcSlots) * M::kTile, true, 0);
+            constexpr uint32_t kQk = mma_shape(kBf16, kTcTok, true), kPv = mma_shape(kBf16, D, false);
+            uint32_t cnt = 0, piece = 0, np[2] = {0, 0};
+            auto slot_ready = [&](uint32_t c) {
+                if (ok) ok = __all_sync(kFull, bar_wait(full + 8 * (c % kTcSlots), (c / kTcSlots) & 1u));
+                tc_fence_after();
+            };
+            auto qk = [&](uint32_t s, uint32_t c) {
+                if (!ok) return;
+                const uint32_t q = mma_desc(sm + M::oQ + (a.one ? 0 : s) * M::kTile, true, 0),
+                               k = mma_desc(sm + (c % kTcSlots) * M::kTile, true, 0);
     #pragma unroll
-                    for (uint32_t x = 0; x < D / 16; x++) {
-                        const uint32_t o = ((x >> 2) * M::kHalf + (x & 3u) * 32) >> 4;
-                        tc_mma_ss(tm + Tmem<D>::S(s), q + o, k + o, kQk, x != 0);
-                    }
-                    tc_commit(s_rdy + 8 * s);
-                };
-                auto pv = [&](uint32_t s, uint32_t c, bool first) {
-                    const uint32_t v = mma_desc(sm + (c % kTcSlots) * M::kTile, false, M::kHalf);
-#pragma unroll
-                    for (uint32_t h = 0; h < 2; h++) {
-                        if (ok) ok = bar_wait(p_rdy + 16 * s + 8 * h, np[s] & 1u);
-                        tc_fence_after();
-                        if (!ok) return;
-#pragma unroll
-                        for (uint32_t x = h * (kTcTok / 32); x < (h + 1) * (kTcTok / 32); x++)
-                            tc_mma_ts(tm + Tmem<D>::O(s), tm + Tmem<D>::P(s) + 8 * x, v + x * 128, kPv, !first || x != 0);
-                    }
-                    np[s]++;
-                };
-                auto free_slot = [&](uint32_t c) {
-                    if (ok) tc_commit(empty + 8 * (c % kTcSlots));
-                };
-                auto done = [&](uint32_t s) {
-                    if (ok) tc_commit(o_rdy + 8 * s);
-                };
-                while (next_tc_piece(a, t, end, of, p)) {
-                    if (ok) ok = bar_wait(q_rdy, piece++ & 1u);
-                    tc_fence_after();
-                    if (a.one) {  // even token tiles: stream 0, odd ones: stream 1
-                        for (uint32_t k = 0; k < 2 && k < p.n; k++) {
-                            slot_ready(cnt);
-                            qk(k, cnt);
-                            free_slot(cnt++);
-                        }
-                        for (uint32_t k = 0; k < p.n; k++) {
-                            const uint32_t s = k & 1u;
-                            slot_ready(cnt);
-                            pv(s, cnt, k < 2);
-                            free_slot(cnt++);
-                            if (k + 2 < p.n) {
-                                slot_ready(cnt);
-                                qk(s, cnt);
-                                free_slot(cnt++);
-                            } else {
-                                done(s);
-                            }
-                        }
-                    } else {
-                        slot_ready(cnt);
-                        qk(0, cnt);
-                        qk(1, cnt);
-                        free_slot(cnt++);
-                        for (uint32_t k = 0; k < p.n; k++) {
-                            const uint32_t v = cnt++;
-                            const bool more = k + 1 < p.n;
-                            slot_ready(v);
-                            if (more) slot_ready(cnt);
-                            for (uint32_t s = 0; s < 2; s++) {
-                                pv(s, v, k == 0);
-                                if (s) free_slot(v);
-                                if (more) qk(s, cnt);
-                                else done(s);
-                            }
-                            if (more) free_slot(cnt++);
-                        }
-                    }
+                for (uint32_t x = 0; x < D / 16; x++) {
+                    const uint32_t o = ((x >> 2) * M::kHalf + (x & 3u) * 32) >> 4;
+                    tc_mma_ss(tm + Tmem<D>::S(s), q + o, k + o, kQk, x != 0);
                 }
-                if (!ok) {
-                    tc_commit(drain);
-                    bar_wait(drain, 0);
-                    flag_why(a.status, CG_ERR_TIMEOUT, kWhyWait);
+                tc_commit(s_rdy + 8 * s);
+            };
+            auto pv = [&](uint32_t s, uint32_t c, bool first) {
+                const uint32_t v = mma_desc(sm + (c % kTcSlots) * M::kTile, false, M::kHalf);
+#pragma unroll
+                for (uint32_t h = 0; h < 2; h++) {
+                    if (ok) ok = __all_sync(kFull, bar_wait(p_rdy + 16 * s + 8 * h, np[s] & 1u));
+                    tc_fence_after();
+                    if (!ok) return;
+#pragma unroll
+                    for (uint32_t x = h * (kTcTok / 32); x < (h + 1) * (kTcTok / 32); x++)
+                        tc_mma_ts(tm + Tmem<D>::O(s), tm + Tmem<D>::P(s) + 8 * x, v + x * 128, kPv, !first || x != 0);
+                }
+                np[s]++;
+            };
+            auto free_slot = [&](uint32_t c) {
+                if (ok) tc_commit(empty + 8 * (c % kTcSlots));
+            };
+            auto done = [&](uint32_t s) {
+                if (ok) tc_commit(o_rdy + 8 * s);
+            };
+            while (next_tc_piece(a, t, end, of, p)) {
+                if (ok) ok = __all_sync(kFull, bar_wait(q_rdy, piece++ & 1u));
+                tc_fence_after();
+                if (a.one) {  // even token tiles: stream 0, odd ones: stream 1
+                    for (uint32_t k = 0; k < 2 && k < p.n; k++) {
+                        slot_ready(cnt);
+                        qk(k, cnt);
+                        free_slot(cnt++);
+                    }
+                    for (uint32_t k = 0; k < p.n; k++) {
+                        const uint32_t s = k & 1u;
+                        slot_ready(cnt);
+                        pv(s, cnt, k < 2);
+                        free_slot(cnt++);
+                        if (k + 2 < p.n) {
+                            slot_ready(cnt);
+                            qk(s, cnt);
+                            free_slot(cnt++);
+                        } else {
+                            done(s);
+                        }
+                    }
+                } else {
+                    slot_ready(cnt);
+                    qk(0, cnt);
+                    qk(1, cnt);
+                    free_slot(cnt++);
+                    for (uint32_t k = 0; k < p.n; k++) {
+                        const uint32_t v = cnt++;
+                        const bool more = k + 1 < p.n;
+                        slot_ready(v);
+                        if (more) slot_ready(cnt);
+                        for (uint32_t s = 0; s < 2; s++) {
+                            pv(s, v, k == 0);
+                            if (s) free_slot(v);
+                            if (more) qk(s, cnt);
+                            else done(s);
+                        }
+                        if (more) free_slot(cnt++);
+                    }
                 }
             }
-            __syncwarp();
+            if (!ok) {
+                tc_commit(drain);
+                bar_wait(drain, 0);
+                if (lane == 0) flag_why(a.status, CG_ERR_TIMEOUT, kWhyWait);
+            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
