@@ -189,11 +189,6 @@ __device__ __forceinline__ void mul2(float &x, float &y, float f) {
         : "f"(f));
 }
 
-// Programmatic launch: the next kernel of the stream may start, and wait for
-// the kernels before this one to be complete and their writes visible.
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -13,6 +13,7 @@
 #include <math.h>
 
 #include "cg_async.cuh"
+#include "cg_launch.cuh"
 
 namespace cg {
 namespace {
@@ -968,23 +969,6 @@ bool make_map(const cg_pages *p, const cg_attention *a, uint32_t rows, CUtensorM
                p->pool + a->layer * p->layer_stride, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// A kernel that may start, with `early`, while the one before it runs.
-template <class... P, class... A>
-cudaError_t launch_next(void (*k)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s, bool early,
-                        const A &...args) {
-    cudaLaunchConfig_t c{};
-    c.gridDim = grid;
-    c.blockDim = block;
-    c.dynamicSmemBytes = smem;
-    c.stream = s;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    c.attrs = &at;
-    c.numAttrs = early ? 1 : 0;
-    return cudaLaunchKernelEx(&c, k, args...);
 }
 
 template <class T, uint32_t D, uint32_t kR>

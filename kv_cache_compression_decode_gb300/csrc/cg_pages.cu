@@ -3,6 +3,7 @@
 // planning kernel turns them into a list of block moves, and one mover
 // kernel carries the moves out and writes the new tables.
 #include "cg_internal.cuh"
+#include "cg_launch.cuh"
 
 namespace cg {
 namespace {
@@ -16,7 +17,7 @@ constexpr uint32_t kUnitVecs = 32u * kVecs;      // a warp's unit: 4 KiB with 16
 // per-move ones; both give the mover (src, dst, rows) lists.
 struct PlanWs {
     uint32_t *n_moves;   // header[0]
-    uint32_t *src, *dst; // [max(n_pool, n_slots)]
+    uint32_t *src, *dst; // [max(n_pool, n_slots)] (fork's destinations are fresh[base])
     uint32_t *rows;      // [n_slots] fork: rows of the move (0: none)
     uint32_t *base;      // [n_slots] fork: the child's first entry in `fresh`
     uint32_t *plen;      // [n_slots] fork: the parent's length
@@ -82,12 +83,30 @@ struct Tab {
     uint32_t n_slots, n_blocks, n_pool, bshift;
 };
 
+// The use counts of blocks 4 tid .. 4 tid + 3 of a run of 4096: bit k set
+// where block k is in use (kLive) or free; blocks past the pool are neither.
+template <bool kLive>
+__device__ __forceinline__ uint32_t use_bits(const Tab &t, uint64_t b) {
+    uint32_t v[4];
+#pragma unroll
+    for (uint32_t k = 0; k < 4; k++) v[k] = b + k < t.n_pool ? t.refs[b + k] : (kLive ? 0u : 1u);
+    uint32_t bits = 0;
+#pragma unroll
+    for (uint32_t k = 0; k < 4; k++) bits |= (uint32_t)((v[k] != 0) == kLive) << k;
+    return bits;
+}
+constexpr uint32_t kRun = 4u * kPlanThreads;
+
 // One block: check every child, hand out the free blocks, list the tail
 // copies.  Any fault leaves n_moves = 0 in the header and nothing changed.
+// The time is that of its chain of dependent loads, so the first run of use
+// counts and the tail blocks are fetched beside the checks.
 __global__ void __launch_bounds__(kPlanThreads) k_fork_plan(Tab t, ForkArgs f, PlanWs w, uint32_t *status) {
+    let_next_start();
     __shared__ uint32_t sh[32];
     __shared__ uint64_t sh8[32];  // the wanted blocks are summed in 64 bits: each child may ask for up to 2^31
     const uint32_t tid = threadIdx.x, bt = 1u << t.bshift;
+    uint32_t fr = use_bits<false>(t, 4u * tid);
     for (uint32_t s = tid; s < t.n_slots; s += kPlanThreads) w.claimed[s] = 0;
     __syncthreads();
     uint64_t total = 0;
@@ -107,8 +126,12 @@ __global__ void __launch_bounds__(kPlanThreads) k_fork_plan(Tab t, ForkArgs f, P
             else if (atomicExch(&w.claimed[c], 1u) != 0) bad = true;
             const uint64_t rows = (uint64_t)t.n_blocks << t.bshift;
             const uint64_t want = (uint64_t)pl + (f.reserve ? f.reserve[i] : 0u);
-            if (want > rows) bad = true;  // covers pl > rows too
-            else need = (uint32_t)((want + bt - 1u) >> t.bshift) - (pl >> t.bshift);
+            if (want > rows) {  // covers pl > rows too
+                bad = true;
+            } else {
+                need = (uint32_t)((want + bt - 1u) >> t.bshift) - (pl >> t.bshift);
+                if (pl & (bt - 1u)) w.src[i] = t.tables[(uint64_t)p * t.n_blocks + (pl >> t.bshift)];
+            }
         }
         uint64_t sum;
         const uint64_t off = block_scan<uint64_t>(need, &sum, sh8);
@@ -128,54 +151,46 @@ __global__ void __launch_bounds__(kPlanThreads) k_fork_plan(Tab t, ForkArgs f, P
         }
     }
     uint32_t found = 0;
-    for (uint64_t b0 = 0; b0 < t.n_pool && found < total; b0 += 4u * kPlanThreads) {
-        const uint64_t b = b0 + 4u * tid;
-        uint32_t fr = 0;
-        for (uint32_t k = 0; k < 4; k++)
-            if (b + k < t.n_pool && t.refs[b + k] == 0) fr |= 1u << k;
+    for (uint64_t b0 = 0; b0 < t.n_pool && found < total; b0 += kRun) {
+        const uint32_t next = b0 + kRun < t.n_pool ? use_bits<false>(t, b0 + kRun + 4u * tid) : 0u;
         uint32_t sum;
         uint32_t at = found + block_scan<uint32_t>(__popc(fr), &sum, sh);
         for (uint32_t k = 0; k < 4; k++)
             if ((fr >> k) & 1u) {
-                if (at < total) w.fresh[at] = (uint32_t)(b + k);
+                if (at < total) w.fresh[at] = (uint32_t)(b0 + 4u * tid + k);
                 at++;
             }
         found += sum;
+        fr = next;
     }
-    __syncthreads();  // w.fresh is read below by other threads of the block
-    if (found < total) {
-        if (tid == 0) {
-            *w.n_moves = 0;
-            flag(status, CG_ERR_RANGE);
-        }
-        return;
+    if (tid == 0) {
+        *w.n_moves = found < total ? 0u : f.n;
+        if (found < total) flag(status, CG_ERR_RANGE);
     }
-    for (uint32_t i = tid; i < f.n; i += kPlanThreads) {
-        if (w.rows[i] == 0) continue;
-        w.src[i] = t.tables[(uint64_t)f.parent[i] * t.n_blocks + (w.plen[i] >> t.bshift)];
-        w.dst[i] = w.fresh[w.base[i]];
-    }
-    if (tid == 0) *w.n_moves = f.n;
 }
 
 // One block: count the blocks in use, pair the ones past that count with the
 // holes below it (both in ascending order), move their references.
 __global__ void __launch_bounds__(kPlanThreads) k_compact_plan(Tab t, uint32_t *remap, PlanWs w) {
+    let_next_start();
     __shared__ uint32_t sh[32];
     const uint32_t tid = threadIdx.x;
-    uint32_t mine = 0, n_live;
-    for (uint32_t b = tid; b < t.n_pool; b += kPlanThreads) mine += t.refs[b] != 0;
+    uint32_t live = use_bits<true>(t, 4u * tid);
+    uint32_t mine = __popc(live), n_live;
+#pragma unroll 4
+    for (uint64_t b0 = kRun; b0 < t.n_pool; b0 += kRun) mine += __popc(use_bits<true>(t, b0 + 4u * tid));
     block_scan<uint32_t>(mine, &n_live, sh);
     uint32_t movers = 0, holes = 0;
-    for (uint64_t b0 = 0; b0 < t.n_pool; b0 += 4u * kPlanThreads) {
+    for (uint64_t b0 = 0; b0 < t.n_pool; b0 += kRun) {
         const uint64_t b = b0 + 4u * tid;
+        const uint32_t next = b0 + kRun < t.n_pool ? use_bits<true>(t, b + kRun) : 0u;
         uint32_t mv = 0, ho = 0;
         for (uint32_t k = 0; k < 4; k++) {
             if (b + k >= t.n_pool) break;
-            const bool live = t.refs[b + k] != 0;
-            remap[b + k] = live ? (uint32_t)(b + k) : CG_NO_BLOCK;
-            if (live && b + k >= n_live) mv |= 1u << k;
-            if (!live && b + k < n_live) ho |= 1u << k;
+            const bool used = (live >> k) & 1u;
+            remap[b + k] = used ? (uint32_t)(b + k) : CG_NO_BLOCK;
+            if (used && b + k >= n_live) mv |= 1u << k;
+            if (!used && b + k < n_live) ho |= 1u << k;
         }
         uint32_t sum;  // both counts in one word: at most 4096 each
         const uint32_t off = block_scan<uint32_t>(__popc(mv) | (__popc(ho) << 16), &sum, sh);
@@ -186,6 +201,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_compact_plan(Tab t, uint32_t *
         }
         movers += sum & 0xFFFFu;
         holes += sum >> 16;
+        live = next;
     }
     __syncthreads();
     for (uint32_t i = tid; i < movers; i += kPlanThreads) {  // movers == holes
@@ -267,6 +283,7 @@ __device__ void compact_tables(const MoveArgs &a) {
 template <int V, Mode kMode>
 __global__ void __launch_bounds__(kMoveThreads) k_move(MoveArgs a) {
     using T = typename Vec<V>::T;
+    if (kMode != kCopy) wait_for_previous();  // the plan
     const uint32_t n = a.n_dev ? *a.n_dev : a.n;
     if (kMode == kFork && n) fork_tables(a);
     if (kMode == kCompact) compact_tables(a);
@@ -284,7 +301,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_move(MoveArgs a) {
         const uint64_t v0 = (r - slice * chunks) * kUnitVecs;
         const uint64_t nv = a.rows ? (uint64_t)per_row * a.rows[m] : most;
         if (v0 >= nv) continue;
-        const uint32_t s = a.src[m], d = a.dst[m];
+        const uint32_t s = a.src[m], d = kMode == kFork ? a.w.fresh[a.w.base[m]] : a.dst[m];
         if (s >= a.from.n_pool || d >= a.to.n_pool) {
             if (lane == 0) flag(a.status, kMode == kCopy ? CG_ERR_RANGE : CG_ERR_CORRUPT);
             continue;
@@ -372,11 +389,8 @@ cudaError_t launch_move(const MoveArgs &a, uint64_t align, uint64_t max_moves, u
     want = want < table_blocks ? table_blocks : want;
     const uint64_t most = (uint64_t)sms * 8u;
     const unsigned grid = (unsigned)(want < 1 ? 1 : want < most ? want : most);
-    if (V == 16) k_move<16, kMode><<<grid, kMoveThreads, 0, s>>>(a);
-    else if (V == 8) k_move<8, kMode><<<grid, kMoveThreads, 0, s>>>(a);
-    else if (V == 4) k_move<4, kMode><<<grid, kMoveThreads, 0, s>>>(a);
-    else k_move<2, kMode><<<grid, kMoveThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    const auto k = V == 16 ? k_move<16, kMode> : V == 8 ? k_move<8, kMode> : V == 4 ? k_move<4, kMode> : k_move<2, kMode>;
+    return launch_next(k, grid, kMoveThreads, 0, s, kMode != kCopy, a);
 }
 
 bool misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1u)) != 0; }
@@ -440,7 +454,6 @@ extern "C" cg_status cg_pages_fork(const cg_pages *p, const uint32_t *parent, co
     a.bt = p->block_tokens;
     a.row_bytes = 2 * p->C;
     a.src = w.src;
-    a.dst = w.dst;
     a.rows = w.rows;
     a.n_dev = w.n_moves;
     a.t = tab_of(p);

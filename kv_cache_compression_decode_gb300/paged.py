@@ -23,15 +23,20 @@ from typing import Optional
 import torch
 
 from . import codec
-from .codec import CG_BF16, CG_FP16, Config, _check, _stream_ptr, cg_attention, cg_pages, lib
+from .codec import CG_BF16, CG_FP16, Config, _check, cg_attention, cg_pages, lib
 
 NO_BLOCK = NO_SLOT = -1  # CG_NO_BLOCK / CG_NO_SLOT as int32
 
 _DTYPES = {torch.float16: CG_FP16, torch.bfloat16: CG_BF16}
 
 
+_INT32 = (torch.int32, torch.uint32)
+# The current stream's handle without building a Stream object around it (3 us of a 7 us call).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _ids(t: torch.Tensor, device: torch.device, what: str) -> int:
-    if t.dtype not in (torch.int32, torch.uint32) or t.dim() != 1 or not t.is_contiguous() or t.device != device:
+    if t.dtype not in _INT32 or t.dim() != 1 or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{what}: a contiguous 1-D int32 tensor on {device} is wanted, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
@@ -59,11 +64,14 @@ class PagedCache:
         sl, sb, skv, st, _ = pool.stride()
         self._c = cg_pages(pool.data_ptr(), L, C, n_pool, bt, sl, skv, sb, st, tables.data_ptr(), lens.data_ptr(),
                            refs.data_ptr(), tables.shape[0], tables.shape[1])
+        self._ref = ct.byref(self._c)
         n = ct.c_size_t()
-        _check(lib().cg_pages_ws_bytes(ct.byref(self._c), ct.byref(n)), "cg_pages_ws_bytes")
+        _check(lib().cg_pages_ws_bytes(self._ref, ct.byref(n)), "cg_pages_ws_bytes")
         self._ws = torch.empty(n.value, dtype=torch.uint8, device=pool.device)
         self._outgrown = []  # earlier workspaces: a captured graph may still use them
-        self._attn = {}  # argument blocks of attend by shape: sizes only, filled anew on every call
+        self._status_ptr = self.status.data_ptr()
+        self._index = pool.device.index if pool.is_cuda else None
+        self._attn = {}  # argument blocks and workspace sizes of attend by shape; the blocks are filled anew on every call
 
     @classmethod
     def empty(cls, L: int, n_pool: int, block_tokens: int, C: int, n_slots: int, n_blocks: int,
@@ -76,6 +84,11 @@ class PagedCache:
 
     def c(self) -> cg_pages:
         return self._c
+
+    def _stream(self, stream) -> Optional[int]:
+        if stream is not None:
+            return stream.cuda_stream
+        return _raw_stream(self._index) if self._index is not None else None
 
     @property
     def block_tokens(self) -> int:
@@ -102,15 +115,15 @@ class PagedCache:
         n = parent.shape[0]
         if child.shape[0] != n or (reserve is not None and reserve.shape[0] != n):
             raise ValueError("fork: parent, child and reserve have one entry per new sequence")
-        _check(lib().cg_pages_fork(ct.byref(self._c), _ids(parent, d, "parent"), _ids(child, d, "child"),
+        _check(lib().cg_pages_fork(self._ref, _ids(parent, d, "parent"), _ids(child, d, "child"),
                                    _ids(reserve, d, "reserve") if reserve is not None else None, n,
-                                   self._ws.data_ptr(), self._ws.numel(), self.status.data_ptr(),
-                                   _stream_ptr(stream)), "cg_pages_fork")
+                                   self._ws.data_ptr(), self._ws.numel(), self._status_ptr,
+                                   self._stream(stream)), "cg_pages_fork")
 
     def free(self, slots: torch.Tensor, stream=None) -> None:
         """End the sequences in `slots` (cg_pages_free)."""
-        _check(lib().cg_pages_free(ct.byref(self._c), _ids(slots, self.pool.device, "slots"), slots.shape[0],
-                                   self.status.data_ptr(), _stream_ptr(stream)), "cg_pages_free")
+        _check(lib().cg_pages_free(self._ref, _ids(slots, self.pool.device, "slots"), slots.shape[0],
+                                   self._status_ptr, self._stream(stream)), "cg_pages_free")
 
     def compact(self, remap: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """Move the blocks in use to the front of the pool; returns each
@@ -120,8 +133,8 @@ class PagedCache:
             remap = torch.empty(self.pool.shape[1], dtype=torch.int32, device=d)
         if remap.shape[0] != self.pool.shape[1]:
             raise ValueError("remap has one entry per block of the pool")
-        _check(lib().cg_pages_compact(ct.byref(self._c), _ids(remap, d, "remap"), self._ws.data_ptr(),
-                                      self._ws.numel(), self.status.data_ptr(), _stream_ptr(stream)),
+        _check(lib().cg_pages_compact(self._ref, _ids(remap, d, "remap"), self._ws.data_ptr(),
+                                      self._ws.numel(), self._status_ptr, self._stream(stream)),
                "cg_pages_compact")
         return remap
 
@@ -134,8 +147,8 @@ class PagedCache:
             raise ValueError("copy: src and dst have the same number of blocks")
         if other.pool.dtype != self.pool.dtype or other.pool.device != d:
             raise ValueError("copy: both pools have one type and one device")
-        _check(lib().cg_pages_copy(ct.byref(self._c), ct.byref(other._c), _ids(src, d, "src"), _ids(dst, d, "dst"),
-                                   src.shape[0], self.status.data_ptr(), _stream_ptr(stream)), "cg_pages_copy")
+        _check(lib().cg_pages_copy(self._ref, other._ref, _ids(src, d, "src"), _ids(dst, d, "dst"),
+                                   src.shape[0], self._status_ptr, self._stream(stream)), "cg_pages_copy")
 
     def decode(self, cfg: Config, enc, slot: int, stream=None) -> None:
         """Decode a context into the blocks that a slot holds
@@ -196,10 +209,10 @@ class PagedCache:
         a.scale = scale if scale is not None else 1.0 / math.sqrt(hd) if hd else 0.0
         if not ws_bytes:
             n = ct.c_size_t()
-            _check(lib().cg_attend_ws_bytes(ct.byref(self._c), ct.byref(a), ct.byref(n)), "cg_attend_ws_bytes")
+            _check(lib().cg_attend_ws_bytes(self._ref, ct.byref(a), ct.byref(n)), "cg_attend_ws_bytes")
             ws_bytes = n.value
             self._attn[key] = (a, ws_bytes)
         ws = self._workspace(ws_bytes)
-        _check(lib().cg_attend(ct.byref(self._c), ct.byref(a), ws.data_ptr(), ws.numel(), self.status.data_ptr(),
-                               _stream_ptr(stream)), "cg_attend")
+        _check(lib().cg_attend(self._ref, ct.byref(a), ws.data_ptr(), ws.numel(), self._status_ptr,
+                               self._stream(stream)), "cg_attend")
         return out
