@@ -45,6 +45,7 @@ struct Args {
     uint32_t *status;
     // workspace
     uint64_t *cum;           // [R + 1] first tile of request r; [R]: tiles of all requests
+    uint32_t *tokens;        // [R] tokens of request r (tokens_of)
     float *part_o;           // [piece][4][piece_rows][D], a quarter per warp column of k_rows
     float2 *part_ml;         // [piece][4][piece_rows] (m, l)
     uint32_t piece_rows, range_rows; // rows of a piece that are stored; rows of an item's range
@@ -96,14 +97,20 @@ struct Piece {
 struct Walk {
     uint64_t t, end, base;  // position, end of this block's share, first tile of request r
     uint32_t r;
+    const uint32_t *lens;   // tokens of the requests in shared memory, or null
 };
+
+// floor(x / y): the numbers are small most of the time, and 64-bit division is long.
+__device__ __forceinline__ uint64_t quot(uint64_t x, uint64_t y) {
+    return (x | y) >> 32 ? x / y : (uint32_t)x / (uint32_t)y;
+}
 
 __device__ __forceinline__ bool next_piece(const Args &a, Walk &w, Piece &p) {
     if (w.t >= w.end) return false;
     bool bad = false;
     uint32_t nt = 0, len = 0;
     while (w.r < a.R) {
-        len = tokens_of(a, w.r, &bad);
+        len = w.lens ? w.lens[w.r] : tokens_of(a, w.r, &bad);
         nt = len > a.P ? tiles_of(a, len - a.P) : 0;
         const uint64_t all = (uint64_t)nt * a.rt * a.ng;
         if (w.t < w.base + all) break;
@@ -116,7 +123,7 @@ __device__ __forceinline__ bool next_piece(const Args &a, Walk &w, Piece &p) {
         nt = tiles_of(a, a.P);
     }
     const uint64_t at = w.t - w.base;
-    const uint32_t local = (uint32_t)(at / nt);
+    const uint32_t local = (uint32_t)quot(at, nt);
     p.item = w.r * a.rt * a.ng + local;
     p.range = local / a.ng;
     p.group = local - p.range * a.ng;
@@ -158,7 +165,9 @@ template <uint32_t D, uint32_t kR> struct Smem {
     static constexpr uint32_t kStage = 2 * kTile;
     static constexpr uint32_t oBar = kStages * kStage;
     static constexpr uint32_t oMisc = oBar + 2 * kStages * 8;
-    static constexpr uint32_t kBytes = oMisc + 128 + 1024;  // and slack to align the tiles to 1 KiB
+    static constexpr uint32_t oLens = oMisc + 128;          // tokens of up to kLens requests
+    static constexpr uint32_t kLens = 1024;
+    static constexpr uint32_t kBytes = oLens + kLens * 4 + 1024;  // and slack to align the tiles to 1 KiB
 };
 
 // Query rows in tiles of 16 against their tokens.  A block takes nh = 4
@@ -190,10 +199,14 @@ __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __
     // This block's share of the work list: every thread sums its own run of requests.
     const uint32_t per = (a.R + S::kThreads - 1) / S::kThreads;
     const uint32_t r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
+    uint32_t *lens = reinterpret_cast<uint32_t *>(smem + S::oLens);
+    const bool keep = a.R <= S::kLens;
     uint64_t mine = 0;
     bool bad = false;
     for (uint32_t r = r0; r < r1; r++) {
         const uint32_t n = tokens_of(a, r, &bad);
+        if (keep) lens[r] = n;
+        if (blockIdx.x == 0) a.tokens[r] = n;
         mine += (uint64_t)(n > a.P ? tiles_of(a, n - a.P) : 0) * a.rt * a.ng;
     }
     if (bad && blockIdx.x == 0) flag(a.status, CG_ERR_RANGE);
@@ -212,30 +225,25 @@ __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __
     const uint64_t total = own + (uint64_t)a.npt * a.ng * tiles_of(a, a.P);
     if (blockIdx.x == 0) {
         uint64_t at = before;
-        bool b = false;
         for (uint32_t r = r0; r < r1; r++) {
             a.cum[r] = at;
-            const uint32_t n = tokens_of(a, r, &b);
+            const uint32_t n = a.tokens[r];  // this thread's own write
             at += (uint64_t)(n > a.P ? tiles_of(a, n - a.P) : 0) * a.rt * a.ng;
         }
         if (tid == 0) a.cum[a.R] = own;
     }
     const uint64_t n_cta = shares(a, total);
     Walk w;
-    w.t = blockIdx.x < n_cta ? blockIdx.x * total / n_cta : total;
-    w.end = blockIdx.x < n_cta ? (blockIdx.x + 1ull) * total / n_cta : total;
-    if (tid == 0) {
-        misc[kWarps + 1] = own;
-        misc[kWarps + 2] = a.R;
-    }
-    __syncthreads();
+    w.t = blockIdx.x < n_cta ? quot(blockIdx.x * total, n_cta) : total;
+    w.end = blockIdx.x < n_cta ? quot((blockIdx.x + 1ull) * total, n_cta) : total;
     if (mine && w.t >= before && w.t < before + mine) {  // one thread at most
         misc[kWarps + 1] = before;
         misc[kWarps + 2] = r0;
     }
     __syncthreads();
-    w.base = misc[kWarps + 1];
-    w.r = (uint32_t)misc[kWarps + 2];
+    w.base = w.t < own ? misc[kWarps + 1] : own;
+    w.r = w.t < own ? (uint32_t)misc[kWarps + 2] : a.R;
+    w.lens = keep ? lens : nullptr;
 
     const uint32_t tt = 1u << a.tlog;                 // tokens of a tile
     const uint32_t head_bytes = tt * D * 2, half_bytes = tt * 128;
@@ -289,20 +297,23 @@ __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __
     const uint32_t col = warp & 3u, hd = col % a.nh, part = col / a.nh;  // head of the group, 16 tokens of the tile
     const uint32_t kbase = hd * head_bytes + part * 16 * 128, vbase = S::kTile + kbase;
     bool ok = true;
-    while (next_piece(a, w, p)) {
+    // The queries of a piece, and how many of the item's tokens each of this
+    // lane's two rows sees.  They are fetched before the results of the piece
+    // before it go out.
+    uint32_t q[D / 16][4], lim[2], least, own_tokens;
+    Row ro[2];
+    auto begin = [&]() {
         const bool shared = p.r == a.R;
-        const uint32_t own_tokens = shared ? a.P : p.len - a.P;
+        own_tokens = least = shared ? a.P : p.len - a.P;
         const uint32_t head = p.group * a.nh + hd, x0 = p.range * (kR * kRows) + (warp >> 2) * kRows;
-        // query fragments, and how many of the item's tokens each of this lane's two rows sees
-        uint32_t q[D / 16][4];
-        uint32_t lim[2], least = own_tokens;
-        Row ro[2];
+#pragma unroll
         for (uint32_t e = 0; e < 2; e++) {
             const Row o = ro[e] = row_of(a, p, x0 + rw + 8 * e, head);
             const uint16_t *src = a.q + o.r * a.qs[0] + o.i * a.qs[1] + o.h * a.qs[2] + 2 * qd;
+#pragma unroll
             for (uint32_t k = 0; k < D / 16; k++) {
-                q[k][e] = o.valid ? *reinterpret_cast<const uint32_t *>(src + 16 * k) ^ a.flip : 0u;
-                q[k][e + 2] = o.valid ? *reinterpret_cast<const uint32_t *>(src + 16 * k + 8) ^ a.flip : 0u;
+                q[k][e] = o.valid ? *reinterpret_cast<const uint32_t *>(src + 16 * k) : 0u;
+                q[k][e + 2] = o.valid ? *reinterpret_cast<const uint32_t *>(src + 16 * k + 8) : 0u;
             }
             lim[e] = own_tokens;
             if (!shared) {
@@ -311,6 +322,15 @@ __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __
                 least = min(least, p.len + 1 > a.nq + a.P ? p.len + 1 - a.nq - a.P : 0u);
             }
         }
+    };
+    bool more = next_piece(a, w, p);
+    if (more) begin();
+    while (more) {
+        if (a.flip)
+#pragma unroll
+            for (uint32_t k = 0; k < D / 16; k++)
+#pragma unroll
+                for (uint32_t e = 0; e < 4; e++) q[k][e] ^= a.flip;
         float o[D / 8][4];
 #pragma unroll
         for (uint32_t d = 0; d < D / 8; d++)
@@ -406,22 +426,25 @@ __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __
             if (lane == 0) bar_arrive(empty + 8 * st);
         }
 
+        const Row done[2] = {ro[0], ro[1]};
+        const bool answer = a.P == 0 && a.nh == 4 && p.n == p.of;  // the whole sequence
+        const uint64_t slot = (((uint64_t)blockIdx.x + p.item) * 4 + col) * a.piece_rows + (warp >> 2) * kRows + rw;
 #pragma unroll
         for (uint32_t e = 0; e < 2; e++) {
             l[e] += __shfl_xor_sync(kFull, l[e], 1);
             l[e] += __shfl_xor_sync(kFull, l[e], 2);
-            if (!ro[e].valid) continue;
-            if (a.P == 0 && a.nh == 4 && p.n == p.of) {  // the whole sequence: the answer
+            if (!done[e].valid) continue;
+            if (answer) {
                 const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];
-                uint16_t *dst = a.out + ro[e].r * a.os[0] + ro[e].i * a.os[1] + ro[e].h * a.os[2] + 2 * qd;
+                uint16_t *dst = a.out + done[e].r * a.os[0] + done[e].i * a.os[1] + done[e].h * a.os[2] + 2 * qd;
 #pragma unroll
                 for (uint32_t d = 0; d < D / 8; d++)
                     *reinterpret_cast<uint32_t *>(dst + 8 * d) = Half<T>::pack(o[d][2 * e] * inv, o[d][2 * e + 1] * inv);
                 if (a.lse && qd == 0)
-                    a.lse[((uint64_t)ro[e].r * a.nq + ro[e].i) * (a.g * a.Hkv) + ro[e].h] =
+                    a.lse[((uint64_t)done[e].r * a.nq + done[e].i) * (a.g * a.Hkv) + done[e].h] =
                         l[e] == 0.f ? -INFINITY : (m[e] + log2f(l[e])) * kLn2;
             } else {
-                const uint64_t at = (((uint64_t)blockIdx.x + p.item) * 4 + col) * a.piece_rows + (warp >> 2) * kRows + rw + 8 * e;
+                const uint64_t at = slot + 8 * e;
                 float *dst = a.part_o + at * D + 2 * qd;
 #pragma unroll
                 for (uint32_t d = 0; d < D / 8; d++)
@@ -429,6 +452,8 @@ __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __
                 if (qd == 0) a.part_ml[at] = make_float2(m[e], l[e]);
             }
         }
+        more = next_piece(a, w, p);
+        if (more) begin();
     }
     if (!ok && lane == 0) flag_why(a.status, CG_ERR_TIMEOUT, kWhyWait);
 }
@@ -783,106 +808,207 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
 }
 
 // Joins the pieces of the query rows.  A warp takes a.merge_rows rows of one
-// request and KV head, whose pieces lie in the same places; four groups of
-// eight lanes take every fourth piece of a row and join at the end.
+// request and KV head; the pieces of a row and of the next lie side by side.
+// Up to four pieces (the usual number in a large batch) are read at once, a
+// lane holding D / 32 channels: one trip to memory a row.  With more, lane j
+// looks at piece j (32 at a time): its maximum, and its weight against the
+// largest; then four groups of eight lanes add up every fourth piece, D / 8
+// channels a lane, and the groups' sums meet in two halving exchanges.
 template <class T, uint32_t D>
-__global__ void __launch_bounds__(256) k_merge(const Args a) {
+__global__ void __launch_bounds__(256, 3) k_merge(const Args a) {
     wait_for_previous();
-    const uint32_t lane = threadIdx.x & 31u, grp = lane >> 3, gl = lane & 7u;
+    const uint32_t lane = threadIdx.x & 31u;
     const uint32_t per = a.nq * a.g, chunks = (per + a.merge_rows - 1) / a.merge_rows;
     const uint32_t id = blockIdx.x * 8 + (threadIdx.x >> 5);  // at most 2^31 rows
     if (id >= a.R * a.Hkv * chunks) return;
     const uint32_t rh = id / chunks, r = rh / a.Hkv, head = rh - r * a.Hkv, x_begin = (id - rh * chunks) * a.merge_rows;
     const uint32_t x_end = min(x_begin + a.merge_rows, per);
-    const uint32_t group = head / a.nh, hd = head - group * a.nh, parts = 4 / a.nh;
-    constexpr uint32_t kPer = D / 8;
-    bool bad = false;
-    const uint32_t len = tokens_of(a, r, &bad), nt_sh = a.npt ? tiles_of(a, a.P) : 0;
-    const uint32_t nt_own = len > a.P ? tiles_of(a, len - a.P) : 0;
-    const uint64_t own = a.cum[a.R], first = a.cum[r], total = own + (uint64_t)a.npt * a.ng * nt_sh;
-    const uint64_t n_cta = shares(a, total);
-    const uint32_t of = (a.P + kTcTok - 1) / kTcTok;
-    const uint64_t total_tc = (uint64_t)a.pairs * a.Hkv * of, n_cta_tc = min((uint64_t)a.n_tc, total_tc);
-    // three runs of pieces: of k_shared, of the shared part in k_rows, of the
-    // request's own tokens; tiles [t0, t0 + nt) of an item are spread over blocks c0..c1
-    uint32_t item_tc = ~0u, item_sh = ~0u, item_own = ~0u, n_tc = 0, n_sh = 0, n_own = 0;
-    uint64_t at_tc = 0, at_sh = 0, at_own = 0;
+    const uint32_t len = a.tokens[r];
+    const uint64_t own = a.cum[a.R], first = a.cum[r];
+    const uint32_t hlog = a.nh >> 1, plog = 2u - hlog;  // log2 of nh, and of the parts of a row, 4 / nh
+    const uint32_t group = head >> hlog, hd = head & (a.nh - 1u);
+    const uint32_t rlog = a.range_rows == kRows ? 4u : 5u, rmask = a.range_rows - 1u;
+    const uint32_t nt_sh = a.npt ? tiles_of(a, a.P) : 0, nt_own = len > a.P ? tiles_of(a, len - a.P) : 0;
+    const uint64_t total = own + (uint64_t)a.npt * a.ng * nt_sh, n_cta = shares(a, total);
+    // tiles [t0, t0 + nt) of an item are spread over blocks c0..c1
     auto run = [](uint64_t t0, uint32_t nt, uint64_t n, uint64_t all, uint64_t &c0) {
-        c0 = ((t0 + 1) * n - 1) / all;
-        return (uint32_t)(((t0 + nt) * n - 1) / all - c0) + 1;
+        c0 = quot((t0 + 1) * n - 1, all);
+        return (uint32_t)(quot((t0 + nt) * n - 1, all) - c0) + 1;
     };
-    for (uint32_t x = x_begin; x < x_end; x++) {
-        const uint32_t xp = r * per + x;
-        if (len && a.pairs && item_tc != head * a.pairs + (xp >> 8)) {
-            item_tc = head * a.pairs + (xp >> 8);
-            n_tc = run((uint64_t)item_tc * of, of, n_cta_tc, total_tc, at_tc) << a.one;
-            at_tc = (at_tc + item_tc) * 256;
+    // rows whose pieces are those of one item of each kind
+    for (uint32_t x0 = x_begin, x1; x0 < x_end; x0 = x1) {
+        const uint32_t xp = r * per + x0;
+        x1 = min(x_end, (x0 | rmask) + 1);
+        if (a.pairs) x1 = min(x1, x0 + 256u - (xp & 255u));
+        if (a.npt) x1 = min(x1, x0 + a.range_rows - (xp & rmask));
+        // three runs of pieces: of k_shared, of the shared part in k_rows, of the request's own tokens
+        uint32_t n_tc = 0, n_sh = 0, n_own = 0;
+        uint64_t at_tc = 0, at_sh = 0, at_own = 0, c0;
+        if (len && a.pairs) {
+            const uint32_t of = (a.P + kTcTok - 1) / kTcTok, item = head * a.pairs + (xp >> 8);
+            const uint64_t all = (uint64_t)a.pairs * a.Hkv * of;
+            n_tc = run((uint64_t)item * of, of, min((uint64_t)a.n_tc, all), all, c0) << a.one;
+            at_tc = (c0 + item) * 256 + (xp & 255u);
         }
-        if (len && a.npt && item_sh != xp / a.range_rows * a.ng + group) {
-            item_sh = xp / a.range_rows * a.ng + group;
-            n_sh = run(own + (uint64_t)item_sh * nt_sh, nt_sh, n_cta, total, at_sh) * parts;
-            at_sh = ((at_sh + a.R * a.rt * a.ng + item_sh) * 4 + hd) * a.piece_rows;
+        if (len && a.npt) {
+            const uint32_t item = (xp >> rlog) * a.ng + group;
+            n_sh = run(own + (uint64_t)item * nt_sh, nt_sh, n_cta, total, c0) << plog;
+            at_sh = ((c0 + a.R * a.rt * a.ng + item) * 4 + hd) * a.piece_rows + (xp & rmask);
         }
-        if (nt_own && item_own != x / a.range_rows * a.ng + group) {
-            item_own = x / a.range_rows * a.ng + group;
-            n_own = run(first + (uint64_t)item_own * nt_own, nt_own, n_cta, total, at_own) * parts;
-            at_own = ((at_own + r * a.rt * a.ng + item_own) * 4 + hd) * a.piece_rows;
+        if (nt_own) {
+            const uint32_t item = (x0 >> rlog) * a.ng + group;
+            n_own = run(first + (uint64_t)item * nt_own, nt_own, n_cta, total, c0) << plog;
+            at_own = ((c0 + r * a.rt * a.ng + item) * 4 + hd) * a.piece_rows + (x0 & rmask);
         }
         if (n_own == 1 && a.P == 0) continue;  // k_rows has written the answer
-        float m = -INFINITY, l = 0.f, o[kPer];
-#pragma unroll
-        for (uint32_t k = 0; k < kPer; k++) o[k] = 0.f;
-        for (uint32_t e = grp; e < n_tc + n_sh + n_own; e += 4) {
-            const float2 *ml;
-            const float *src;
+        const uint32_t n = n_tc + n_sh + n_own;
+        // piece e of row x0
+        auto place = [&](uint32_t e, const float2 *&ml, const float *&src) {
             if (e < n_tc) {
-                const uint64_t at = at_tc + (xp & 255u) + (e >> a.one) * 256ull + (e & a.one) * 128;
+                const uint64_t at = at_tc + (e >> a.one) * 256ull + (e & a.one) * 128;
                 ml = a.tc_ml + at;
                 src = a.tc_o + at * D;
             } else {
                 const bool sh = e - n_tc < n_sh;
                 const uint32_t f = sh ? e - n_tc : e - n_tc - n_sh;
-                const uint64_t at = (sh ? at_sh + xp % a.range_rows : at_own + x % a.range_rows) +
-                                    (f / parts * 4ull + f % parts * a.nh) * a.piece_rows;
+                const uint64_t at = (sh ? at_sh : at_own) + ((f >> plog) * 4ull + ((f & ((1u << plog) - 1u)) << hlog)) * a.piece_rows;
                 ml = a.part_ml + at;
                 src = a.part_o + at * D;
             }
-            const float2 v = *ml;
-            float4 y[kPer / 4];
+        };
+        const float2 *ml = nullptr;
+        const float *src = nullptr;
+        if (lane < n) place(lane, ml, src);
+        if (n <= 4) {
+            constexpr uint32_t kLane = D / 32;
+            const float2 *pm[4];
+            const float *po[4];
 #pragma unroll
-            for (uint32_t k = 0; k < kPer / 4; k++) y[k] = *reinterpret_cast<const float4 *>(src + 4 * (gl + 8 * k));
-            if (v.y == 0.f) continue;  // a piece the row sees nothing of; its outputs may be unwritten
-            const float nm = fmaxf(m, v.x);
-            const float f = m == nm ? 1.f : ex2(m - nm), w = v.x == nm ? 1.f : ex2(v.x - nm);
-            m = nm;
-            l = l * f + v.y * w;
+            for (uint32_t e = 0; e < 4; e++) {
+                pm[e] = reinterpret_cast<const float2 *>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(ml), e));
+                po[e] = reinterpret_cast<const float *>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(src), e)) + lane * kLane;
+            }
+            uint32_t i = x0 / a.g, j = x0 - i * a.g;  // query token, query head of the KV head
+#pragma unroll 1
+            for (uint32_t x = 0; x < x1 - x0; x++) {
+                float2 v[4];
+                float y[4][kLane];
+#pragma unroll
+                for (uint32_t e = 0; e < 4; e++) {
+                    v[e] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                    for (uint32_t k = 0; k < kLane; k++) y[e][k] = 0.f;
+                    if (e < n) {
+                        v[e] = pm[e][x];
+                        if constexpr (kLane == 4) *reinterpret_cast<float4 *>(y[e]) = *reinterpret_cast<const float4 *>(po[e] + x * D);
+                        else *reinterpret_cast<float2 *>(y[e]) = *reinterpret_cast<const float2 *>(po[e] + x * D);
+                    }
+                }
+#pragma unroll
+                for (uint32_t e = 0; e < 4; e++)
+                    if (v[e].y == 0.f) {  // a piece the row sees nothing of; its outputs may be unwritten
+                        v[e].x = -INFINITY;
+#pragma unroll
+                        for (uint32_t k = 0; k < kLane; k++) y[e][k] = 0.f;
+                    }
+                const float m = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
+                float l = 0.f, o[kLane] = {};
+#pragma unroll
+                for (uint32_t e = 0; e < 4; e++) {
+                    const float w = v[e].x == m ? 1.f : ex2(v[e].x - m);
+                    l += v[e].y * w;
+#pragma unroll
+                    for (uint32_t k = 0; k < kLane; k++) o[k] += y[e][k] * w;
+                }
+                const float inv = l == 0.f ? 0.f : __frcp_rn(l);
+                uint16_t *dst = a.out + r * a.os[0] + i * a.os[1] + (head * a.g + j) * a.os[2] + kLane * lane;
+                if constexpr (kLane == 4)
+                    *reinterpret_cast<uint2 *>(dst) =
+                        make_uint2(Half<T>::pack(o[0] * inv, o[1] * inv), Half<T>::pack(o[2] * inv, o[3] * inv));
+                else
+                    *reinterpret_cast<uint32_t *>(dst) = Half<T>::pack(o[0] * inv, o[1] * inv);
+                if (a.lse && lane == 0)
+                    a.lse[((uint64_t)r * a.nq + i) * (a.g * a.Hkv) + head * a.g + j] =
+                        l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                if (++j == a.g) {
+                    j = 0;
+                    i++;
+                }
+            }
+            continue;
+        }
+        constexpr uint32_t kPer = D / 8;
+        const uint32_t grp = lane >> 3, gl = lane & 7u;
+#pragma unroll 1
+        for (uint32_t x = 0; x < x1 - x0; x++) {
+            float m = -INFINITY, l = 0.f, o[kPer];
+#pragma unroll
+            for (uint32_t k = 0; k < kPer; k++) o[k] = 0.f;
+#pragma unroll 1
+            for (uint32_t e0 = 0; e0 < n; e0 += 32) {
+                const float *s = src + x * D;
+                float2 v = make_float2(-INFINITY, 0.f);
+                if (e0 + lane < n) {
+                    const float2 *q = ml;
+                    if (e0) place(e0 + lane, q, s), s += x * D;
+                    v = q[x];
+                }
+                if (v.y == 0.f) {
+                    v.x = -INFINITY;
+                    s = nullptr;
+                }
+                float nm = fmaxf(m, v.x);
+#pragma unroll
+                for (uint32_t d = 16; d; d >>= 1) nm = fmaxf(nm, __shfl_xor_sync(kFull, nm, d));
+                const float f = m == nm ? 1.f : ex2(m - nm);
+                const float w = v.x == nm ? 1.f : ex2(v.x - nm);
+                float sum = v.y * w;
+#pragma unroll
+                for (uint32_t d = 16; d; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
+                m = nm;
+                l = l * f + sum;
+                if (e0)
+#pragma unroll
+                    for (uint32_t k = 0; k < kPer; k++) o[k] *= f;
+                const uint32_t cnt = min(n - e0, 32u);
+#pragma unroll 2
+                for (uint32_t b = 0; b < cnt; b += 4) {
+                    const float wj = __shfl_sync(kFull, w, b + grp);
+                    const float *sj = reinterpret_cast<const float *>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(s), b + grp));
+                    if (!sj) continue;
+#pragma unroll
+                    for (uint32_t k = 0; k < kPer / 4; k++) {
+                        const float4 y = *reinterpret_cast<const float4 *>(sj + 4 * (gl + 8 * k));
+                        o[4 * k] += y.x * wj;
+                        o[4 * k + 1] += y.y * wj;
+                        o[4 * k + 2] += y.z * wj;
+                        o[4 * k + 3] += y.w * wj;
+                    }
+                }
+            }
+            // the groups' sums: half of the channels to either pair of groups, then to either group
+            __syncwarp();
+#pragma unroll
+            for (uint32_t k = 0; k < kPer / 2; k++) {
+                const float give = grp & 2u ? o[k] : o[k + kPer / 2], keep = grp & 2u ? o[k + kPer / 2] : o[k];
+                o[k] = keep + __shfl_xor_sync(kFull, give, 16);
+            }
 #pragma unroll
             for (uint32_t k = 0; k < kPer / 4; k++) {
-                o[4 * k] = o[4 * k] * f + y[k].x * w;
-                o[4 * k + 1] = o[4 * k + 1] * f + y[k].y * w;
-                o[4 * k + 2] = o[4 * k + 2] * f + y[k].z * w;
-                o[4 * k + 3] = o[4 * k + 3] * f + y[k].w * w;
+                const float give = grp & 1u ? o[k] : o[k + kPer / 4], keep = grp & 1u ? o[k + kPer / 4] : o[k];
+                o[k] = keep + __shfl_xor_sync(kFull, give, 8);
             }
+            const float inv = l == 0.f ? 0.f : __frcp_rn(l);
+            const uint32_t i = (x0 + x) / a.g, h = head * a.g + (x0 + x) - i * a.g;
+            uint16_t *dst = a.out + r * a.os[0] + i * a.os[1] + h * a.os[2];
+            if constexpr (D == 128)
+                *reinterpret_cast<uint2 *>(dst + 4 * (gl + 8 * grp)) =
+                    make_uint2(Half<T>::pack(o[0] * inv, o[1] * inv), Half<T>::pack(o[2] * inv, o[3] * inv));
+            else
+                *reinterpret_cast<uint32_t *>(dst + 4 * (gl + 8 * (grp >> 1)) + 2 * (grp & 1u)) = Half<T>::pack(o[0] * inv, o[1] * inv);
+            if (a.lse && lane == 0)
+                a.lse[((uint64_t)r * a.nq + i) * (a.g * a.Hkv) + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
-#pragma unroll
-        for (uint32_t d = 8; d < 32; d <<= 1) {
-            const float om = __shfl_xor_sync(kFull, m, d), ol = __shfl_xor_sync(kFull, l, d), nm = fmaxf(m, om);
-            const float f = m == nm ? 1.f : ex2(m - nm), w = om == nm ? 1.f : ex2(om - nm);
-            m = nm;
-            l = l * f + ol * w;
-#pragma unroll
-            for (uint32_t k = 0; k < kPer; k++) o[k] = o[k] * f + __shfl_xor_sync(kFull, o[k], d) * w;
-        }
-        if (grp) continue;
-        const uint32_t i = x / a.g, h = head * a.g + x - i * a.g;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        uint16_t *dst = a.out + r * a.os[0] + i * a.os[1] + h * a.os[2];
-#pragma unroll
-        for (uint32_t k = 0; k < kPer / 4; k++)
-            *reinterpret_cast<uint2 *>(dst + 4 * (gl + 8 * k)) = make_uint2(
-                Half<T>::pack(o[4 * k] * inv, o[4 * k + 1] * inv), Half<T>::pack(o[4 * k + 2] * inv, o[4 * k + 3] * inv));
-        if (a.lse && gl == 0)
-            a.lse[((uint64_t)r * a.nq + i) * (a.g * a.Hkv) + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
 }
 
@@ -933,7 +1059,7 @@ bool make_plan(const cg_pages *p, const cg_attention *a, Plan *o) {
     o->items = ((uint64_t)a->n_requests * o->rt + o->npt) * o->ng;
     if (o->items > (1ull << 31)) return false;
     o->pieces = o->items + kMaxCtas;
-    o->cum_bytes = round_up((a->n_requests + 1ull) * 8, 256);
+    o->cum_bytes = round_up((a->n_requests + 1ull) * 8 + a->n_requests * 4ull, 256);
     o->o_bytes = round_up(o->pieces * 4 * o->piece_rows * a->head_dim * 4, 256);
     o->ml_bytes = round_up(o->pieces * 4 * o->piece_rows * 8, 256);
     const uint64_t tc_rows = tc ? ((uint64_t)o->pairs * a->n_kv_heads + kMaxCtas) * 256 : 0;
@@ -999,11 +1125,11 @@ cudaError_t launch(const CUtensorMap &rows_map, const CUtensorMap &map, Args &a,
     }
     e = a.range_rows == kRows ? launch_rows<T, D, 1>(rows_map, a, sms, s) : launch_rows<T, D, 2>(rows_map, a, sms, s);
     if (e != cudaSuccess) return e;
-    // a few rows a warp where there are rows enough to fill the GPU
-    const uint64_t per = (uint64_t)a.nq * a.g, rows = (uint64_t)a.R * a.Hkv * per;
-    const uint64_t want = rows / ((uint64_t)sms * 32);
-    a.merge_rows = (uint32_t)(want < 1 ? 1 : want < per ? want : per);
-    const uint64_t warps = (uint64_t)a.R * a.Hkv * ((per + a.merge_rows - 1) / a.merge_rows);
+    // a few rows a warp where there are rows enough to fill the GPU with 24 warps an SM
+    const uint64_t per = (uint64_t)a.nq * a.g, rh = (uint64_t)a.R * a.Hkv, fit = (uint64_t)sms * 24 / rh;
+    const uint64_t chunks = fit < 1 ? 1 : fit < per ? fit : per;
+    a.merge_rows = (uint32_t)((per + chunks - 1) / chunks);
+    const uint64_t warps = rh * ((per + a.merge_rows - 1) / a.merge_rows);
     return launch_next(k_merge<T, D>, (unsigned)((warps + 7) / 8), 256, 0, s, true, a);
 }
 
@@ -1064,6 +1190,7 @@ extern "C" cg_status cg_attend(const cg_pages *p, const cg_attention *at, void *
     a.status = dev_status;
     uint8_t *w = static_cast<uint8_t *>(ws);
     a.cum = reinterpret_cast<uint64_t *>(w);
+    a.tokens = reinterpret_cast<uint32_t *>(a.cum + a.R + 1);
     a.part_o = reinterpret_cast<float *>(w + pl.cum_bytes);
     a.part_ml = reinterpret_cast<float2 *>(w + pl.cum_bytes + pl.o_bytes);
     a.piece_rows = pl.piece_rows;
