@@ -688,21 +688,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
         uint32_t ns = 0, piece = 0;
         const uint32_t rows_all = a.R * a.nq * a.g, per = a.nq * a.g;
         while (next_tc_piece(a, t, end, of, p)) {
-            // the queries: a row per thread; with one row tile the first group brings it
+            // the queries: a warp brings its 32 rows, D / 8 lanes to a row (a
+            // thread to a row took 4.6 us, each load touching 32 lines); with
+            // one row tile the first stream brings it
             if (!(a.one && s)) {
                 const uint32_t x = p.pair * 256 + s * 128 + rl;
-                const bool valid = x < rows_all;
                 const uint32_t r = x / per, y = x - r * per, i = y / a.g, h = p.head * a.g + (y - i * a.g);
-                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + r * a.qs[0] + i * a.qs[1] + h * a.qs[2]);
-                uint8_t *dst = smem + M::oQ + s * M::kTile + rl * 128;
+                const uint16_t *mine = x < rows_all ? a.q + r * a.qs[0] + i * a.qs[1] + h * a.qs[2] : nullptr;
+                constexpr uint32_t kLanes = D / 8, kPass = 32 / kLanes;  // lanes of a row, rows of a pass
+                uint4 v[kLanes];
 #pragma unroll
-                for (uint32_t c = 0; c < D / 8; c++) {
-                    uint4 v = valid ? src[c] : make_uint4(0, 0, 0, 0);
-                    v.x ^= a.flip;
-                    v.y ^= a.flip;
-                    v.z ^= a.flip;
-                    v.w ^= a.flip;
-                    *reinterpret_cast<uint4 *>(dst + (c >> 3) * M::kHalf + (((c & 7u) ^ (rl & 7u)) << 4)) = v;
+                for (uint32_t k = 0; k < kLanes; k++) {
+                    const uint32_t row = k * kPass + lane / kLanes;
+                    const uint4 *src = reinterpret_cast<const uint4 *>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(mine), row));
+                    v[k] = src ? src[lane % kLanes] : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (uint32_t k = 0; k < kLanes; k++) {
+                    const uint32_t row = (rl & 96u) + k * kPass + lane / kLanes, c = lane % kLanes;
+                    v[k].x ^= a.flip;
+                    v[k].y ^= a.flip;
+                    v[k].z ^= a.flip;
+                    v[k].w ^= a.flip;
+                    *reinterpret_cast<uint4 *>(smem + M::oQ + s * M::kTile + (c >> 3) * M::kHalf + row * 128 +
+                                               (((c & 7u) ^ (row & 7u)) << 4)) = v[k];
                 }
             }
             fence_async();
@@ -781,21 +790,37 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
             if (mine) {
                 if (ok) ok = bar_wait(o_rdy + 8 * s, piece & 1u);
                 ok = __all_sync(kFull, ok);
-                if (ok) {
-                    tc_fence_after();
+                piece++;
+            }
+            if (a.one) group_sync(1, 256);  // the other stream's products read the same queries
+            if (mine && ok) {
+                // through the queries' shared memory, 8 KB a warp, so that a row goes out in one run
+                tc_fence_after();
+                const uint32_t stage = M::oQ + s * M::kTile + (warp & 3u) * (M::kTile / 4);
+                constexpr uint32_t kCols = D / 2, kUnits = kCols / 4, kRowsOut = 32 / kUnits;  // columns of a pass in 16-byte units
 #pragma unroll
-                    for (uint32_t c = 0; c < D / 32; c++) {
+                for (uint32_t c = 0; c < 2; c++) {
+#pragma unroll
+                    for (uint32_t b = 0; b < kCols / 32; b++) {
                         uint32_t o[32];
-                        tc_ld32(o, tml + Tmem<D>::O(s) + 32 * c);
+                        tc_ld32(o, tml + Tmem<D>::O(s) + kCols * c + 32 * b);
                         tc_wait_ld();
-                        uint4 *dst = reinterpret_cast<uint4 *>(a.tc_o + at * D + 32 * c);
 #pragma unroll
                         for (uint32_t j = 0; j < 8; j++)
-                            dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                            *reinterpret_cast<uint4 *>(smem + stage + lane * (kCols * 4) + (((8 * b + j) ^ (lane & 7u)) << 4)) =
+                                make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                     }
-                    tc_fence_before();
+                    __syncwarp();
+                    float *dst = a.tc_o + (at - lane) * D + kCols * c;
+#pragma unroll
+                    for (uint32_t k = 0; k < kUnits; k++) {
+                        const uint32_t row = k * kRowsOut + lane / kUnits, u = lane % kUnits;
+                        *reinterpret_cast<uint4 *>(dst + row * D + 4 * u) =
+                            *reinterpret_cast<const uint4 *>(smem + stage + row * (kCols * 4) + ((u ^ (row & 7u)) << 4));
+                    }
+                    __syncwarp();
                 }
-                piece++;
+                tc_fence_before();
             }
             group_sync(1, 256);  // both streams are done with the queries and with TMEM
         }
