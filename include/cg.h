@@ -535,7 +535,9 @@ cg_status cg_pages_compact(const cg_pages *p, uint32_t *remap, void *ws, size_t 
  * gets out = 0 and lse = -inf.  The first shared_blocks entries of every
  * request's row are taken to equal those of slot shared_slot (as
  * cg_pages_fork leaves them) and are read through that slot's row.  Rows of
- * the pool at or past a sequence's length are never used, whatever they hold.
+ * the pool at or past a sequence's length are never used, whatever they hold,
+ * and a token's infinities and NaNs reach the queries that see it alone.  out
+ * may not overlap q or the pool.
  * Scores, softmax sums and outputs are accumulated in fp32; the weights
  * e^{s_t - max} are rounded to the 16-bit type for the product with V.
  * Device-side errors: CG_ERR_RANGE for a slot out of range, a length above
@@ -566,9 +568,11 @@ cg_status cg_attend_ws_bytes(const cg_pages *p, const cg_attention *a, size_t *w
  * head_dim other than 64 or 128, n_kv_heads * head_dim != C, n_q_heads not a
  * multiple of n_kv_heads, zero counts, layer >= L, shared_slot >= n_slots or
  * shared_blocks > n_blocks (where shared_blocks > 0), a non-finite scale,
- * block_tokens < 8, and a pool, q, out or stride that is not a multiple of 16
- * bytes (blocks are fetched by TMA).  ws: device, 256-byte aligned;
- * CG_ERR_RANGE if smaller than cg_attend_ws_bytes. */
+ * block_tokens < 8, and a pool, q, out or stride (of a dimension with more
+ * than one element) that is not a multiple of 16 bytes: blocks are fetched by
+ * TMA.  ws: device, 256-byte aligned; CG_ERR_RANGE if smaller than
+ * cg_attend_ws_bytes.  The call keeps the address of the driver's tensor-map
+ * encoder for the life of the process, and nothing else. */
 cg_status cg_attend(const cg_pages *p, const cg_attention *a, void *ws, size_t ws_bytes, uint32_t *dev_status,
                     void *stream);
 

@@ -139,6 +139,7 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) 
         : "memory");
 }
 
+// The 16-bit types.  kExponent: the exponent bits, all set in an infinity or NaN.
 template <class T> struct Half;
 template <> struct Half<__half> {
     static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -152,7 +153,8 @@ template <> struct Half<__half> {
         __half2 h = __floats2half2_rn(lo, hi);
         return *reinterpret_cast<uint32_t *>(&h);
     }
-    static __device__ __forceinline__ __half one(float x) { return __float2half_rn(x); }
+    static __device__ __forceinline__ float2 unpack(uint32_t x) { return __half22float2(*reinterpret_cast<__half2 *>(&x)); }
+    static constexpr uint32_t kExponent = 0x7C00u;
 };
 template <> struct Half<__nv_bfloat16> {
     static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -166,7 +168,10 @@ template <> struct Half<__nv_bfloat16> {
         __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
         return *reinterpret_cast<uint32_t *>(&h);
     }
-    static __device__ __forceinline__ __nv_bfloat16 one(float x) { return __float2bfloat16_rn(x); }
+    static __device__ __forceinline__ float2 unpack(uint32_t x) {
+        return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&x));
+    }
+    static constexpr uint32_t kExponent = 0x7F80u;
 };
 
 // Two fp32 operations in one instruction.

@@ -167,7 +167,8 @@ template <uint32_t D, uint32_t kR> struct Smem {
     static constexpr uint32_t oMisc = oBar + 2 * kStages * 8;
     static constexpr uint32_t oLens = oMisc + 128;          // tokens of up to kLens requests
     static constexpr uint32_t kLens = 1024;
-    static constexpr uint32_t kBytes = oLens + kLens * 4 + 1024;  // and slack to align the tiles to 1 KiB
+    static constexpr uint32_t oWeights = oLens + kLens * 4;  // 16 x 16 weights a warp, where rows add up one by one
+    static constexpr uint32_t kBytes = oWeights + 4 * kR * kRows * 16 * 4 + 1024;  // and slack to align the tiles to 1 KiB
 };
 
 // Query rows in tiles of 16 against their tokens.  A block takes nh = 4
@@ -409,16 +410,53 @@ __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __
                         s[n][j] = ex2(s[n][j] - z[j >> 1]);
                         l[j >> 1] += s[n][j];
                     }
+                // A token that some of the rows do not see may hold an infinity or a NaN, which
+                // the weight 0 would not keep out of their sums: then each row adds its own.
+                bool odd = false;
+                if (mask && a.nq > 1) {
+                    if (tok + (lane >> 1) >= least)
+                        for (uint32_t b = 16 * (lane & 1u); b < D * 2; b += 32) {
+                            const uint4 y = *reinterpret_cast<const uint4 *>(smem + st * S::kStage + vbase + (b >> 7) * half_bytes +
+                                                                             (lane >> 1) * 128 + (b & 127u));
+                            constexpr uint32_t kX = Half<T>::kExponent;
+                            for (uint32_t z : {y.x, y.y, y.z, y.w}) odd |= (z & kX) == kX || (z >> 16 & kX) == kX;
+                        }
+                    odd = __any_sync(kFull, odd);
+                }
                 const uint32_t pa[4] = {Half<T>::pack(s[0][0], s[0][1]), Half<T>::pack(s[0][2], s[0][3]),
                                         Half<T>::pack(s[1][0], s[1][1]), Half<T>::pack(s[1][2], s[1][3])};
-                const uint32_t r = ((lane >> 3) & 1u) * 8 + (lane & 7u);
-                const uint32_t rb = vb + r * 128, x = r & 7u, hi = lane >> 4;
+                if (!odd) {
+                    const uint32_t r = ((lane >> 3) & 1u) * 8 + (lane & 7u);
+                    const uint32_t rb = vb + r * 128, x = r & 7u, hi = lane >> 4;
 #pragma unroll
-                for (uint32_t d = 0; d < D / 16; d++) {
-                    uint32_t b[4];
-                    ldsm4_t(b, rb + (d >> 2) * half_bytes + ((((d & 3u) * 2 + hi) ^ x) << 4));
-                    Half<T>::mma(o[2 * d], pa, b[0], b[1]);
-                    Half<T>::mma(o[2 * d + 1], pa, b[2], b[3]);
+                    for (uint32_t d = 0; d < D / 16; d++) {
+                        uint32_t b[4];
+                        ldsm4_t(b, rb + (d >> 2) * half_bytes + ((((d & 3u) * 2 + hi) ^ x) << 4));
+                        Half<T>::mma(o[2 * d], pa, b[0], b[1]);
+                        Half<T>::mma(o[2 * d + 1], pa, b[2], b[3]);
+                    }
+                } else {
+                    float2 *wts = reinterpret_cast<float2 *>(smem + S::oWeights) + warp * (kRows * 8);  // [row][token]
+                    for (uint32_t k4 = 0; k4 < 4; k4++)
+                        wts[(rw + 8 * (k4 & 1u)) * 8 + (k4 >> 1) * 4 + qd] = Half<T>::unpack(pa[k4]);
+                    __syncwarp();
+#pragma unroll 1
+                    for (uint32_t t = 0; t < 16; t++) {
+                        const uint8_t *row = smem + st * S::kStage + vbase + t * 128 + 4 * qd;
+#pragma unroll
+                        for (uint32_t e = 0; e < 2; e++) {
+                            if (tok + t >= lim[e]) continue;
+                            const float wt = reinterpret_cast<const float *>(wts)[(rw + 8 * e) * 16 + t];
+#pragma unroll
+                            for (uint32_t d = 0; d < D / 8; d++) {
+                                const float2 v = Half<T>::unpack(*reinterpret_cast<const uint32_t *>(
+                                    row + (d >> 3) * half_bytes + (((d & 7u) ^ (t & 7u)) << 4)));
+                                o[d][2 * e] += wt * v.x;
+                                o[d][2 * e + 1] += wt * v.y;
+                            }
+                        }
+                    }
+                    __syncwarp();
                 }
                 if (tail) fence_async();  // the zeros are ordered before the copy that reuses the stage
             }
@@ -1045,7 +1083,7 @@ struct Plan {
 };
 
 constexpr uint32_t kTcRows = 16;    // k_shared takes the shared part from more query rows than this per KV head
-constexpr uint32_t kMaxCtas = 512;  // bound of the grid that the workspace is sized for
+constexpr uint32_t kMaxCtas = 304, kMaxTcCtas = 152;  // bounds of the grids that the workspace is sized for: 152 SMs
 
 bool make_plan(const cg_pages *p, const cg_attention *a, Plan *o) {
     if (!p || !a || !p->pool || !p->tables || !p->lens || !a->q || !a->out) return false;
@@ -1060,13 +1098,17 @@ bool make_plan(const cg_pages *p, const cg_attention *a, Plan *o) {
     if (a->layer >= p->L || a->shared_blocks > p->n_blocks) return false;
     if (a->shared_blocks && a->shared_slot >= p->n_slots) return false;
     if (!isfinite(a->scale)) return false;
-    const uint64_t strides = p->layer_stride | p->kv_stride | p->block_stride | p->token_stride | a->q_stride[0] |
-                             a->q_stride[1] | a->q_stride[2] | a->out_stride[0] | a->out_stride[1] | a->out_stride[2];
+    // the stride of a dimension with one element is never used
+    const auto used = [](uint64_t n, uint64_t stride) { return n > 1 ? stride : 0; };
+    const uint64_t block = used(p->n_pool_blocks, p->block_stride), layer = used(p->L, p->layer_stride);
+    const uint64_t counts[3] = {a->n_requests, a->n_queries, a->n_q_heads};
+    uint64_t strides = layer | p->kv_stride | block | p->token_stride;
+    for (int k = 0; k < 3; k++) strides |= used(counts[k], a->q_stride[k]) | used(counts[k], a->out_stride[k]);
     if (strides % 8 || misaligned(p->pool, 16) || misaligned(a->q, 16) || misaligned(a->out, 16)) return false;
     if (misaligned(p->tables, 4) || misaligned(p->lens, 4) || misaligned(a->lse, 4) || misaligned(a->slots, 4))
         return false;
     // a tensor map's strides have 40 bits, and its rows and blocks may not be empty strides
-    if ((p->kv_stride | p->block_stride | p->token_stride) >> 39 || !p->kv_stride || !p->block_stride) return false;
+    if ((p->kv_stride | block | p->token_stride) >> 39 || !p->kv_stride || (p->n_pool_blocks > 1 && !block)) return false;
     o->g = a->n_q_heads / a->n_kv_heads;
     const uint64_t per = (uint64_t)a->n_queries * o->g, all = per * a->n_requests;
     if (all * a->n_kv_heads > (1ull << 31)) return false;
@@ -1087,7 +1129,7 @@ bool make_plan(const cg_pages *p, const cg_attention *a, Plan *o) {
     o->cum_bytes = round_up((a->n_requests + 1ull) * 8 + a->n_requests * 4ull, 256);
     o->o_bytes = round_up(o->pieces * 4 * o->piece_rows * a->head_dim * 4, 256);
     o->ml_bytes = round_up(o->pieces * 4 * o->piece_rows * 8, 256);
-    const uint64_t tc_rows = tc ? ((uint64_t)o->pairs * a->n_kv_heads + kMaxCtas) * 256 : 0;
+    const uint64_t tc_rows = tc ? ((uint64_t)o->pairs * a->n_kv_heads + kMaxTcCtas) * 256 : 0;
     o->tc_o_bytes = tc_rows * a->head_dim * 4;
     o->bytes = o->cum_bytes + o->o_bytes + o->ml_bytes + o->tc_o_bytes + tc_rows * 8;
     return true;
@@ -1114,7 +1156,8 @@ bool make_map(const cg_pages *p, const cg_attention *a, uint32_t rows, CUtensorM
     const EncodeTiled enc = encoder();
     if (!enc) return false;
     const cuuint64_t dims[4] = {p->C, p->block_tokens, p->n_pool_blocks, 2};
-    const cuuint64_t strides[3] = {2 * p->token_stride, 2 * p->block_stride, 2 * p->kv_stride};
+    const cuuint64_t block = p->n_pool_blocks > 1 ? p->block_stride : p->token_stride;  // unused with one block, but checked
+    const cuuint64_t strides[3] = {2 * p->token_stride, 2 * block, 2 * p->kv_stride};
     const cuuint32_t box[4] = {64, rows, 1, 1}, step[4] = {1, 1, 1, 1};
     return enc(map, a->dtype == CG_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                p->pool + a->layer * p->layer_stride, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1142,7 +1185,7 @@ cudaError_t launch(const CUtensorMap &rows_map, const CUtensorMap &map, Args &a,
         // next, which costs about kCross tiles (the streams drain, new
         // queries come in); where whole blocks per item take no longer than that, deal so.
         constexpr uint64_t kCross = 4;
-        const uint64_t n = (uint64_t)sms < kMaxCtas ? sms : kMaxCtas, items = (uint64_t)a.pairs * a.Hkv;
+        const uint64_t n = (uint64_t)sms < kMaxTcCtas ? sms : kMaxTcCtas, items = (uint64_t)a.pairs * a.Hkv;
         const uint64_t of = (a.P + kTcTok - 1) / kTcTok, k = n / items < of ? n / items : of;
         a.n_tc = (uint32_t)(k && (of + k - 1) / k <= items * of / n + kCross ? k * items : n);
         e = launch_next(k_shared<T, D>, a.n_tc, kTcThreads, TcSmem<D>::kBytes, s, false, map, a);

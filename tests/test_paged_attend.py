@@ -155,6 +155,74 @@ def test_batches_over_a_long_context(R, nq, Hq, D):
 
 @pytest.mark.gpu
 @needs_gpu
+@pytest.mark.parametrize("Hkv,g,nq", [(4, 8, 1), (8, 8, 4), (12, 1, 1), (6, 5, 2), (32, 1, 1), (4, 3, 7)])
+@pytest.mark.parametrize("D,shared", [(128, 0), (128, 9), (64, 0), (64, 9)])
+def test_groups_of_heads(Hkv, g, nq, D, shared):
+    """Head counts whose heads go four, two and one to a block, on their own
+    and behind shared blocks, for few and for many query rows."""
+    for R in (2, 30):
+        lens = [shared * 16 + (nq + 53 * r % 150 if r % 7 else 0) for r in range(R)]
+        lens = [n if n > shared * 16 else 0 for n in lens]
+        cache, slots = make(lens, shared, 16, Hkv, D, seed=R)
+        q, out, lse = attend(cache, slots, nq=nq, Hq=Hkv * g, D=D, shared_blocks=shared)
+        cache.check()
+        check(cache, q, out, lse, slots, 1, D ** -0.5)
+
+
+@pytest.mark.gpu
+@needs_gpu
+@pytest.mark.parametrize("dtype", [FP16, BF16])
+@pytest.mark.parametrize("shared,Hkv,nq", [(0, 4, 4), (6, 4, 4), (6, 1, 9), (0, 2, 2)])
+def test_a_token_reaches_only_the_queries_that_see_it(dtype, shared, Hkv, nq):
+    """Infinities and NaNs in K and V of the later drafted tokens: the first
+    query's answer is still that of the tokens that it sees."""
+    P = shared * 16
+    lens = [P + n for n in (nq, nq + 1, 16 + nq // 2, 31 + nq, 100)]
+    cache, slots = make(lens, shared, 16, Hkv, 128, dtype)
+    q, out, lse = attend(cache, slots, nq=nq, Hq=8 * Hkv // (2 if Hkv > 1 else 1), shared_blocks=shared)
+    cache.check()
+    check(cache, q, out, lse, slots, 1, 128 ** -0.5)
+    for j, bad in ((1, math.inf), (nq - 1, math.nan)):  # drafted token j of nq
+        for s, n in zip(slots.tolist(), lens):
+            at = n - nq + j
+            cache.pool[1, cache.tables[s, at // 16].long(), :, at % 16, ::3] = bad
+    _, out2, lse2 = attend(cache, slots, q=q, nq=nq, shared_blocks=shared)
+    cache.check()
+    cache.lens[slots.long()] -= nq - 1  # what the first query sees, as a sequence of its own
+    check(cache, q[:, :1], out2[:, :1], lse2[:, :1], slots, 1, 128 ** -0.5)
+    assert not torch.isfinite(out2[:, 1:, :, ::3]).any()
+    assert not torch.isfinite(lse2[:, 1:]).any()
+
+
+@pytest.mark.gpu
+@needs_gpu
+def test_strides_of_single_element_dimensions_are_free():
+    """One layer, one block, one query: their strides say nothing."""
+    base = torch.randn(4096, device="cuda").to(FP16)
+    pool = base[:2 * 8 * 64].as_strided((1, 1, 2, 8, 64), (3, 5, 8 * 64, 64, 1))
+    cache = paged.PagedCache(pool, _ints([0]).view(1, 1), _ints([7]), _ints([1]))
+    q = base[2048:2048 + 256].as_strided((1, 1, 4, 64), (7, 11, 64, 1))
+    out, lse = torch.empty((1, 1, 4, 64), dtype=FP16, device="cuda"), torch.empty((1, 1, 4), device="cuda")
+    cache.attend(0, q, out=out, lse=lse)
+    cache.check()
+    check(cache, q, out, lse, _ints([0]), 0, 64 ** -0.5)
+
+
+@pytest.mark.gpu
+@needs_gpu
+@pytest.mark.parametrize("shared", [0, 6])
+def test_more_requests_than_a_block_keeps(shared):
+    """More requests than a block's shared memory has lengths for."""
+    lens = [shared * 16 + (r * 7) % 40 if r % 40 else 0 for r in range(1100)]
+    lens = [n if n > shared * 16 else 0 for n in lens]
+    cache, slots = make(lens, shared, 16, 1, 64)
+    q, out, lse = attend(cache, slots, Hq=2, D=64, shared_blocks=shared)
+    cache.check()
+    check(cache, q, out, lse, slots, 1, 64 ** -0.5)
+
+
+@pytest.mark.gpu
+@needs_gpu
 @pytest.mark.parametrize("shared", [0, 6])
 def test_more_requests_than_threads(shared):
     rng = np.random.default_rng(5)
@@ -344,7 +412,8 @@ def test_bad_attention_is_refused_on_the_host(kw):
 @pytest.mark.parametrize("kw", [
     dict(pool=None), dict(tables=None), dict(lens=None), dict(pool=(1 << 30) + 8), dict(block_tokens=4), dict(C=96),
     dict(block_tokens=24), dict(layer_stride=100), dict(kv_stride=1020), dict(block_stride=2052), dict(token_stride=68),
-    dict(n_slots=0), dict(n_blocks=0), dict(n_blocks=1 << 27), dict(L=0), dict(kv_stride=1 << 40)])
+    dict(n_slots=0), dict(n_blocks=0), dict(n_blocks=1 << 27), dict(L=0), dict(kv_stride=1 << 40), dict(kv_stride=0),
+    dict(block_stride=0)])
 def test_bad_pool_is_refused_on_the_host(kw):
     L, a, n = C.lib(), fake_attention(), ct.c_size_t()
     p = fake_pages(**kw)
