@@ -877,12 +877,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
 // looks at piece j (32 at a time): its maximum, and its weight against the
 // largest; then four groups of eight lanes add up every fourth piece, D / 8
 // channels a lane, and the groups' sums meet in two halving exchanges.
-template <class T, uint32_t D>
+// kWide, where there are few rows (and so possibly hundreds of pieces to each):
+// a block to a row, its eight warps taking every eighth 32 pieces.
+template <class T, uint32_t D, bool kWide>
 __global__ void __launch_bounds__(256, 3) k_merge(const Args a) {
     wait_for_previous();
-    const uint32_t lane = threadIdx.x & 31u;
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
     const uint32_t per = a.nq * a.g, chunks = (per + a.merge_rows - 1) / a.merge_rows;
-    const uint32_t id = blockIdx.x * 8 + (threadIdx.x >> 5);  // at most 2^31 rows
+    const uint32_t id = kWide ? blockIdx.x : blockIdx.x * 8 + warp;  // at most 2^31 rows
     if (id >= a.R * a.Hkv * chunks) return;
     const uint32_t rh = id / chunks, r = rh / a.Hkv, head = rh - r * a.Hkv, x_begin = (id - rh * chunks) * a.merge_rows;
     const uint32_t x_end = min(x_begin + a.merge_rows, per);
@@ -943,6 +945,7 @@ __global__ void __launch_bounds__(256, 3) k_merge(const Args a) {
         const float *src = nullptr;
         if (lane < n) place(lane, ml, src);
         if (n <= 4) {
+            if (kWide && warp) return;
             constexpr uint32_t kLane = D / 32;
             const float2 *pm[4];
             const float *po[4];
@@ -1008,7 +1011,7 @@ __global__ void __launch_bounds__(256, 3) k_merge(const Args a) {
 #pragma unroll
             for (uint32_t k = 0; k < kPer; k++) o[k] = 0.f;
 #pragma unroll 1
-            for (uint32_t e0 = 0; e0 < n; e0 += 32) {
+            for (uint32_t e0 = kWide ? 32 * warp : 0; e0 < n; e0 += kWide ? 256 : 32) {
                 const float *s = src + x * D;
                 float2 v = make_float2(-INFINITY, 0.f);
                 if (e0 + lane < n) {
@@ -1060,6 +1063,29 @@ __global__ void __launch_bounds__(256, 3) k_merge(const Args a) {
             for (uint32_t k = 0; k < kPer / 4; k++) {
                 const float give = grp & 1u ? o[k] : o[k + kPer / 4], keep = grp & 1u ? o[k + kPer / 4] : o[k];
                 o[k] = keep + __shfl_xor_sync(kFull, give, 8);
+            }
+            if constexpr (kWide) {  // a row a block: the warps' sums meet in shared memory
+                __shared__ float2 sh_ml[8];
+                __shared__ float sh_o[8][D];
+                constexpr uint32_t kOwn = kPer / 4;
+                if (lane == 0) sh_ml[warp] = make_float2(m, l);
+#pragma unroll
+                for (uint32_t k = 0; k < kOwn; k++) sh_o[warp][lane * kOwn + k] = o[k];
+                __syncthreads();
+                if (warp) return;
+#pragma unroll
+                for (uint32_t k = 0; k < 8; k++) m = fmaxf(m, sh_ml[k].x);
+                l = 0.f;
+#pragma unroll
+                for (uint32_t k = 0; k < kOwn; k++) o[k] = 0.f;
+#pragma unroll
+                for (uint32_t b = 0; b < 8; b++) {
+                    const float2 v = sh_ml[b];
+                    const float w = v.x == m ? 1.f : ex2(v.x - m);
+                    l += v.y * w;
+#pragma unroll
+                    for (uint32_t k = 0; k < kOwn; k++) o[k] += sh_o[b][lane * kOwn + k] * w;
+                }
             }
             const float inv = l == 0.f ? 0.f : __frcp_rn(l);
             const uint32_t i = (x0 + x) / a.g, h = head * a.g + (x0 + x) - i * a.g;
@@ -1185,8 +1211,10 @@ cudaError_t launch(const CUtensorMap &rows_map, const CUtensorMap &map, Args &a,
         // next, which costs about kCross tiles (the streams drain, new
         // queries come in); where whole blocks per item take no longer than that, deal so.
         constexpr uint64_t kCross = 4;
-        const uint64_t n = (uint64_t)sms < kMaxTcCtas ? sms : kMaxTcCtas, items = (uint64_t)a.pairs * a.Hkv;
-        const uint64_t of = (a.P + kTcTok - 1) / kTcTok, k = n / items < of ? n / items : of;
+        // A block gets two token tiles a stream at least: a piece less to join saves more than a tile takes.
+        const uint64_t items = (uint64_t)a.pairs * a.Hkv, of = (a.P + kTcTok - 1) / kTcTok, least = a.one ? 4 : 2;
+        const uint64_t most = items * ((of + least - 1) / least), sm = (uint64_t)sms < kMaxTcCtas ? sms : kMaxTcCtas;
+        const uint64_t n = sm < most ? sm : most, k = n / items;
         a.n_tc = (uint32_t)(k && (of + k - 1) / k <= items * of / n + kCross ? k * items : n);
         e = launch_next(k_shared<T, D>, a.n_tc, kTcThreads, TcSmem<D>::kBytes, s, false, map, a);
         if (e != cudaSuccess) return e;
@@ -1196,9 +1224,11 @@ cudaError_t launch(const CUtensorMap &rows_map, const CUtensorMap &map, Args &a,
     // a few rows a warp where there are rows enough to fill the GPU with 24 warps an SM
     const uint64_t per = (uint64_t)a.nq * a.g, rh = (uint64_t)a.R * a.Hkv, fit = (uint64_t)sms * 24 / rh;
     const uint64_t chunks = fit < 1 ? 1 : fit < per ? fit : per;
-    a.merge_rows = (uint32_t)((per + chunks - 1) / chunks);
+    const bool wide = rh * per <= (uint64_t)sms * 4;
+    a.merge_rows = wide ? 1 : (uint32_t)((per + chunks - 1) / chunks);
     const uint64_t warps = rh * ((per + a.merge_rows - 1) / a.merge_rows);
-    return launch_next(k_merge<T, D>, (unsigned)((warps + 7) / 8), 256, 0, s, true, a);
+    return wide ? launch_next(k_merge<T, D, true>, (unsigned)warps, 256, 0, s, true, a)
+                : launch_next(k_merge<T, D, false>, (unsigned)((warps + 7) / 8), 256, 0, s, true, a);
 }
 
 }  // namespace
