@@ -1003,6 +1003,7 @@ __global__ void __launch_bounds__(256, 3) k_merge(const Args a) {
             }
             continue;
         }
+        if (kWide && n <= 32 && warp) return;
         constexpr uint32_t kPer = D / 8;
         const uint32_t grp = lane >> 3, gl = lane & 7u;
 #pragma unroll 1
@@ -1064,7 +1065,7 @@ __global__ void __launch_bounds__(256, 3) k_merge(const Args a) {
                 const float give = grp & 1u ? o[k] : o[k + kPer / 4], keep = grp & 1u ? o[k + kPer / 4] : o[k];
                 o[k] = keep + __shfl_xor_sync(kFull, give, 8);
             }
-            if constexpr (kWide) {  // a row a block: the warps' sums meet in shared memory
+            if (kWide && n > 32) {  // a row a block: the warps' sums meet in shared memory
                 __shared__ float2 sh_ml[8];
                 __shared__ float sh_o[8][D];
                 constexpr uint32_t kOwn = kPer / 4;
