@@ -46,11 +46,12 @@ struct Args {
     // workspace
     uint64_t *cum;           // [R + 1] first tile of request r; [R]: tiles of all requests
     uint32_t *tokens;        // [R] tokens of request r (tokens_of)
-    float *part_o;           // [piece][4][piece_rows][D], a quarter per warp column of k_rows
-    float2 *part_ml;         // [piece][4][piece_rows] (m, l)
+    // rows of partial results: O [D] and (m, l).  First k_shared's, [piece][2][128];
+    // from row part0 on k_rows', [piece][4][piece_rows], a quarter per warp column
+    float *part_o;
+    float2 *part_ml;
+    uint32_t part0;
     uint32_t piece_rows, range_rows; // rows of a piece that are stored; rows of an item's range
-    float *tc_o;             // k_shared: [piece][2][128][D]
-    float2 *tc_ml;           // [piece][2][128]
 };
 
 // Tokens of request r's sequence; 0 for an empty slot and for a request that
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __
 
         const Row done[2] = {ro[0], ro[1]};
         const bool answer = a.P == 0 && a.nh == 4 && p.n == p.of;  // the whole sequence
-        const uint64_t slot = (((uint64_t)blockIdx.x + p.item) * 4 + col) * a.piece_rows + (warp >> 2) * kRows + rw;
+        const uint64_t slot = a.part0 + (((uint64_t)blockIdx.x + p.item) * 4 + col) * a.piece_rows + (warp >> 2) * kRows + rw;
 #pragma unroll
         for (uint32_t e = 0; e < 2; e++) {
             l[e] += __shfl_xor_sync(kFull, l[e], 1);
@@ -844,7 +845,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
             }
             // the piece's result
             const uint64_t at = (((uint64_t)blockIdx.x + p.item) * 2 + s) * 128 + rl;
-            a.tc_ml[at] = make_float2(m == -INFINITY ? m : m - kShift, l);
+            a.part_ml[at] = make_float2(m == -INFINITY ? m : m - kShift, l);
             if (mine) {
                 if (ok) ok = bar_wait(o_rdy + 8 * s, piece & 1u);
                 ok = __all_sync(kFull, ok);
@@ -869,7 +870,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
                                 make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                     }
                     __syncwarp();
-                    float *dst = a.tc_o + (at - lane) * D + kCols * c;
+                    float *dst = a.part_o + (at - lane) * D + kCols * c;
 #pragma unroll
                     for (uint32_t k = 0; k < kUnits; k++) {
                         const uint32_t row = k * kRowsOut + lane / kUnits, u = lane % kUnits;
@@ -890,157 +891,191 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm));
 }
 
-// Joins the pieces of the query rows.  A warp takes a.merge_rows rows of one
-// request and KV head; the pieces of a row and of the next lie side by side.
-// Up to four pieces (the usual number in a large batch) are read at once, a
-// lane holding D / 32 channels: one trip to memory a row.  With more, lane j
-// looks at piece j (32 at a time): its maximum, and its weight against the
-// largest; then four groups of eight lanes add up every fourth piece, D / 8
-// channels a lane, and the groups' sums meet in two halving exchanges.
-// kWide, where there are few rows (and so possibly hundreds of pieces to each):
-// a block to a row, its eight warps taking every eighth 32 pieces.
-template <class T, uint32_t D, bool kWide>
-__global__ void __launch_bounds__(256, 3) k_merge(const Args a) {
-    wait_for_previous();
-    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-    const uint32_t per = a.nq * a.g, chunks = (per + a.merge_rows - 1) / a.merge_rows;
-    const uint32_t id = kWide ? blockIdx.x : blockIdx.x * 8 + warp;  // at most 2^31 rows
-    if (id >= a.R * a.Hkv * chunks) return;
-    const uint32_t rh = id / chunks, r = rh / a.Hkv, head = rh - r * a.Hkv, x_begin = (id - rh * chunks) * a.merge_rows;
-    const uint32_t x_end = min(x_begin + a.merge_rows, per);
-    const uint32_t len = a.tokens[r];
-    const uint64_t own = a.cum[a.R], first = a.cum[r];
+// Where the pieces of a run of query rows lie: three runs of pieces, of
+// k_shared, of the shared part in k_rows, of the request's own tokens.  The
+// pieces of a row and of the next lie side by side.
+struct Runs {
+    uint32_t n_tc, n_sh, n_own, n;
+    uint32_t tc, sh, own;  // the first piece of the first row
+    uint32_t rows;         // rows that this holds for
+};
+
+// The rows x0.. of request r and KV head `head`, at most up to x_end.
+__device__ __forceinline__ Runs runs_of(const Args &a, uint32_t r, uint32_t head, uint32_t x0, uint32_t x_end, uint32_t len,
+                                        uint64_t own, uint64_t first) {
     const uint32_t hlog = a.nh >> 1, plog = 2u - hlog;  // log2 of nh, and of the parts of a row, 4 / nh
     const uint32_t group = head >> hlog, hd = head & (a.nh - 1u);
     const uint32_t rlog = a.range_rows == kRows ? 4u : 5u, rmask = a.range_rows - 1u;
     const uint32_t nt_sh = a.npt ? tiles_of(a, a.P) : 0, nt_own = len > a.P ? tiles_of(a, len - a.P) : 0;
     const uint64_t total = own + (uint64_t)a.npt * a.ng * nt_sh, n_cta = shares(a, total);
     // tiles [t0, t0 + nt) of an item are spread over blocks c0..c1
-    auto run = [](uint64_t t0, uint32_t nt, uint64_t n, uint64_t all, uint64_t &c0) {
-        c0 = quot((t0 + 1) * n - 1, all);
-        return (uint32_t)(quot((t0 + nt) * n - 1, all) - c0) + 1;
+    auto run = [](uint64_t t0, uint32_t nt, uint64_t n, uint64_t all, uint32_t &c0) {
+        c0 = (uint32_t)quot((t0 + 1) * n - 1, all);
+        return (uint32_t)quot((t0 + nt) * n - 1, all) - c0 + 1;
     };
-    // rows whose pieces are those of one item of each kind
-    for (uint32_t x0 = x_begin, x1; x0 < x_end; x0 = x1) {
-        const uint32_t xp = r * per + x0;
-        x1 = min(x_end, (x0 | rmask) + 1);
-        if (a.pairs) x1 = min(x1, x0 + 256u - (xp & 255u));
-        if (a.npt) x1 = min(x1, x0 + a.range_rows - (xp & rmask));
-        // three runs of pieces: of k_shared, of the shared part in k_rows, of the request's own tokens
-        uint32_t n_tc = 0, n_sh = 0, n_own = 0;
-        uint64_t at_tc = 0, at_sh = 0, at_own = 0, c0;
-        if (len && a.pairs) {
-            const uint32_t of = (a.P + kTcTok - 1) / kTcTok, item = head * a.pairs + (xp >> 8);
-            const uint64_t all = (uint64_t)a.pairs * a.Hkv * of;
-            n_tc = run((uint64_t)item * of, of, min((uint64_t)a.n_tc, all), all, c0) << a.one;
-            at_tc = (c0 + item) * 256 + (xp & 255u);
-        }
-        if (len && a.npt) {
-            const uint32_t item = (xp >> rlog) * a.ng + group;
-            n_sh = run(own + (uint64_t)item * nt_sh, nt_sh, n_cta, total, c0) << plog;
-            at_sh = ((c0 + a.R * a.rt * a.ng + item) * 4 + hd) * a.piece_rows + (xp & rmask);
-        }
-        if (nt_own) {
-            const uint32_t item = (x0 >> rlog) * a.ng + group;
-            n_own = run(first + (uint64_t)item * nt_own, nt_own, n_cta, total, c0) << plog;
-            at_own = ((c0 + r * a.rt * a.ng + item) * 4 + hd) * a.piece_rows + (x0 & rmask);
-        }
-        if (n_own == 1 && a.P == 0) continue;  // k_rows has written the answer
-        const uint32_t n = n_tc + n_sh + n_own;
-        // piece e of row x0
-        auto place = [&](uint32_t e, const float2 *&ml, const float *&src) {
-            if (e < n_tc) {
-                const uint64_t at = at_tc + (e >> a.one) * 256ull + (e & a.one) * 128;
-                ml = a.tc_ml + at;
-                src = a.tc_o + at * D;
-            } else {
-                const bool sh = e - n_tc < n_sh;
-                const uint32_t f = sh ? e - n_tc : e - n_tc - n_sh;
-                const uint64_t at = (sh ? at_sh : at_own) + ((f >> plog) * 4ull + ((f & ((1u << plog) - 1u)) << hlog)) * a.piece_rows;
-                ml = a.part_ml + at;
-                src = a.part_o + at * D;
-            }
-        };
-        const float2 *ml = nullptr;
-        const float *src = nullptr;
-        if (lane < n) place(lane, ml, src);
-        if (n <= 4) {
-            if (kWide && warp) return;
-            constexpr uint32_t kLane = D / 32;
-            const float2 *pm[4];
-            const float *po[4];
+    const uint32_t xp = r * (a.nq * a.g) + x0;
+    uint32_t x1 = min(x_end, (x0 | rmask) + 1), c0;
+    Runs o{};
+    if (a.pairs) x1 = min(x1, x0 + 256u - (xp & 255u));
+    if (a.npt) x1 = min(x1, x0 + a.range_rows - (xp & rmask));
+    o.rows = x1 - x0;
+    if (len && a.pairs) {
+        const uint32_t of = (a.P + kTcTok - 1) / kTcTok, item = head * a.pairs + (xp >> 8);
+        const uint64_t all = (uint64_t)a.pairs * a.Hkv * of;
+        o.n_tc = run((uint64_t)item * of, of, min((uint64_t)a.n_tc, all), all, c0) << a.one;
+        o.tc = (c0 + item) * 256 + (xp & 255u);
+    }
+    if (len && a.npt) {
+        const uint32_t item = (xp >> rlog) * a.ng + group;
+        o.n_sh = run(own + (uint64_t)item * nt_sh, nt_sh, n_cta, total, c0) << plog;
+        o.sh = a.part0 + ((c0 + a.R * a.rt * a.ng + item) * 4 + hd) * a.piece_rows + (xp & rmask);
+    }
+    if (nt_own) {
+        const uint32_t item = (x0 >> rlog) * a.ng + group;
+        o.n_own = run(first + (uint64_t)item * nt_own, nt_own, n_cta, total, c0) << plog;
+        o.own = a.part0 + ((c0 + r * a.rt * a.ng + item) * 4 + hd) * a.piece_rows + (x0 & rmask);
+    }
+    o.n = o.n_tc + o.n_sh + o.n_own;
+    return o;
+}
+
+// Row of piece e of the first row of `o`.
+__device__ __forceinline__ uint32_t place(const Args &a, const Runs &o, uint32_t e) {
+    if (e < o.n_tc) return o.tc + (e >> a.one) * 256u + (e & a.one) * 128u;
+    const uint32_t hlog = a.nh >> 1, plog = 2u - hlog;
+    const bool sh = e - o.n_tc < o.n_sh;
+    const uint32_t f = sh ? e - o.n_tc : e - o.n_tc - o.n_sh;
+    return (sh ? o.sh : o.own) + ((f >> plog) * 4u + ((f & ((1u << plog) - 1u)) << hlog)) * a.piece_rows;
+}
+
+__device__ __forceinline__ uint16_t *out_row(const Args &a, uint32_t r, uint32_t head, uint32_t i, uint32_t j) {
+    return a.out + r * a.os[0] + i * a.os[1] + (head * a.g + j) * a.os[2];
+}
+__device__ __forceinline__ void write_lse(const Args &a, uint32_t r, uint32_t head, uint32_t i, uint32_t j, float m, float l) {
+    if (a.lse)
+        a.lse[((uint64_t)r * a.nq + i) * (a.g * a.Hkv) + head * a.g + j] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// Joins the pieces of many query rows.  A warp takes a.merge_rows rows of one
+// request and KV head, a lane D / 32 channels, four pieces at a time (seldom
+// are there more): one trip to memory a row.  What counts is warps, since each
+// waits for its row: 32768 rows of three pieces took 37 us with 16 warps an SM,
+// 27 with 24, 23 with 32 and 21 where twice as many take half as many rows.
+template <class T, uint32_t D>
+__global__ void __launch_bounds__(256, 4) k_merge_rows(const Args a) {
+    wait_for_previous();
+    constexpr uint32_t kLane = D / 32;
+    const uint32_t lane = threadIdx.x & 31u, per = a.nq * a.g, chunks = (per + a.merge_rows - 1) / a.merge_rows;
+    const uint32_t id = blockIdx.x * 8 + (threadIdx.x >> 5);  // at most 2^31 rows
+    if (id >= a.R * a.Hkv * chunks) return;
+    const uint32_t rh = id / chunks, r = rh / a.Hkv, head = rh - r * a.Hkv, x_begin = (id - rh * chunks) * a.merge_rows;
+    const uint32_t x_end = min(x_begin + a.merge_rows, per);
+    const uint32_t len = a.tokens[r];
+    const uint64_t own = a.cum[a.R], first = a.cum[r];
+    uint32_t i = x_begin / a.g, j = x_begin - i * a.g;  // query token, query head of the KV head
+    for (uint32_t x0 = x_begin; x0 < x_end;) {
+        const Runs o = runs_of(a, r, head, x0, x_end, len, own, first);
+        x0 += o.rows;
+        uint32_t at[4];
 #pragma unroll
-            for (uint32_t e = 0; e < 4; e++) {
-                pm[e] = reinterpret_cast<const float2 *>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(ml), e));
-                po[e] = reinterpret_cast<const float *>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(src), e)) + lane * kLane;
-            }
-            uint32_t i = x0 / a.g, j = x0 - i * a.g;  // query token, query head of the KV head
+        for (uint32_t e = 0; e < 4; e++) at[e] = e < o.n ? place(a, o, e) : 0;
+        const bool done = o.n_own == 1 && a.P == 0;  // k_rows has written the answer
 #pragma unroll 1
-            for (uint32_t x = 0; x < x1 - x0; x++) {
-                float2 v[4];
-                float y[4][kLane];
+        for (uint32_t x = 0; x < o.rows; x++) {
+            if (!done) {
+                float m = -INFINITY, l = 0.f, s[kLane] = {};
+#pragma unroll 1
+                for (uint32_t e0 = 0; e0 < o.n; e0 += 4) {
+                    if (o.n > 4)
 #pragma unroll
-                for (uint32_t e = 0; e < 4; e++) {
-                    v[e] = make_float2(-INFINITY, 0.f);
+                        for (uint32_t e = 0; e < 4; e++) at[e] = e0 + e < o.n ? place(a, o, e0 + e) : 0;
+                    float2 v[4];
+                    float y[4][kLane];
 #pragma unroll
-                    for (uint32_t k = 0; k < kLane; k++) y[e][k] = 0.f;
-                    if (e < n) {
-                        v[e] = pm[e][x];
-                        if constexpr (kLane == 4) *reinterpret_cast<float4 *>(y[e]) = *reinterpret_cast<const float4 *>(po[e] + x * D);
-                        else *reinterpret_cast<float2 *>(y[e]) = *reinterpret_cast<const float2 *>(po[e] + x * D);
+                    for (uint32_t e = 0; e < 4; e++) {
+                        v[e] = make_float2(-INFINITY, 0.f);
+                        if (e0 + e < o.n) {
+                            v[e] = a.part_ml[at[e] + x];
+                            const float *src = a.part_o + (uint64_t)(at[e] + x) * D + kLane * lane;
+                            if constexpr (kLane == 4) *reinterpret_cast<float4 *>(y[e]) = *reinterpret_cast<const float4 *>(src);
+                            else *reinterpret_cast<float2 *>(y[e]) = *reinterpret_cast<const float2 *>(src);
+                        }
                     }
-                }
+                    float nm = m;
 #pragma unroll
-                for (uint32_t e = 0; e < 4; e++)
-                    if (v[e].y == 0.f) {  // a piece the row sees nothing of; its outputs may be unwritten
-                        v[e].x = -INFINITY;
+                    for (uint32_t e = 0; e < 4; e++)
+                        if (v[e].y != 0.f) nm = fmaxf(nm, v[e].x);  // 0: a piece the row sees nothing of; its outputs may be unwritten
+                    const float f = m == nm ? 1.f : ex2(m - nm);
+                    m = nm;
+                    l *= f;
 #pragma unroll
-                        for (uint32_t k = 0; k < kLane; k++) y[e][k] = 0.f;
+                    for (uint32_t k = 0; k < kLane; k++) s[k] *= f;
+#pragma unroll
+                    for (uint32_t e = 0; e < 4; e++) {
+                        if (e0 + e >= o.n || v[e].y == 0.f) continue;
+                        const float w = v[e].x == m ? 1.f : ex2(v[e].x - m);
+                        l += v[e].y * w;
+#pragma unroll
+                        for (uint32_t k = 0; k < kLane; k++) s[k] += y[e][k] * w;
                     }
-                const float m = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
-                float l = 0.f, o[kLane] = {};
-#pragma unroll
-                for (uint32_t e = 0; e < 4; e++) {
-                    const float w = v[e].x == m ? 1.f : ex2(v[e].x - m);
-                    l += v[e].y * w;
-#pragma unroll
-                    for (uint32_t k = 0; k < kLane; k++) o[k] += y[e][k] * w;
                 }
                 const float inv = l == 0.f ? 0.f : __frcp_rn(l);
-                uint16_t *dst = a.out + r * a.os[0] + i * a.os[1] + (head * a.g + j) * a.os[2] + kLane * lane;
+                uint16_t *dst = out_row(a, r, head, i, j) + kLane * lane;
                 if constexpr (kLane == 4)
                     *reinterpret_cast<uint2 *>(dst) =
-                        make_uint2(Half<T>::pack(o[0] * inv, o[1] * inv), Half<T>::pack(o[2] * inv, o[3] * inv));
+                        make_uint2(Half<T>::pack(s[0] * inv, s[1] * inv), Half<T>::pack(s[2] * inv, s[3] * inv));
                 else
-                    *reinterpret_cast<uint32_t *>(dst) = Half<T>::pack(o[0] * inv, o[1] * inv);
-                if (a.lse && lane == 0)
-                    a.lse[((uint64_t)r * a.nq + i) * (a.g * a.Hkv) + head * a.g + j] =
-                        l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-                if (++j == a.g) {
-                    j = 0;
-                    i++;
-                }
+                    *reinterpret_cast<uint32_t *>(dst) = Half<T>::pack(s[0] * inv, s[1] * inv);
+                if (lane == 0) write_lse(a, r, head, i, j, m, l);
             }
-            continue;
+            if (++j == a.g) {
+                j = 0;
+                i++;
+            }
         }
+    }
+}
+
+// Joins the pieces of fewer rows, of which each may have hundreds.  Lane j
+// looks at piece j (32 at a time): its maximum, and its weight against the
+// largest; then four groups of eight lanes add up every fourth piece, D / 8
+// channels a lane, and the groups' sums meet in two halving exchanges.
+// kWide, for the fewest rows: a block to a row, its eight warps taking every
+// eighth 32 pieces; otherwise a warp takes a.merge_rows rows.
+template <class T, uint32_t D, bool kWide>
+__global__ void __launch_bounds__(256, 3) k_merge(const Args a) {
+    wait_for_previous();
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    const uint32_t per = a.nq * a.g, chunks = (per + a.merge_rows - 1) / a.merge_rows;
+    const uint32_t id = kWide ? blockIdx.x : blockIdx.x * 8 + warp;
+    if (id >= a.R * a.Hkv * chunks) return;
+    const uint32_t rh = id / chunks, r = rh / a.Hkv, head = rh - r * a.Hkv, x_begin = (id - rh * chunks) * a.merge_rows;
+    const uint32_t x_end = min(x_begin + a.merge_rows, per);
+    const uint32_t len = a.tokens[r];
+    const uint64_t own = a.cum[a.R], first = a.cum[r];
+    constexpr uint32_t kPer = D / 8;
+    const uint32_t grp = lane >> 3, gl = lane & 7u;
+    for (uint32_t x0 = x_begin; x0 < x_end;) {
+        const Runs z = runs_of(a, r, head, x0, x_end, len, own, first);
+        const uint32_t n = z.n, x_first = x0;
+        x0 += z.rows;
+        if (z.n_own == 1 && a.P == 0) continue;  // k_rows has written the answer
         if (kWide && n <= 32 && warp) return;
-        constexpr uint32_t kPer = D / 8;
-        const uint32_t grp = lane >> 3, gl = lane & 7u;
 #pragma unroll 1
-        for (uint32_t x = 0; x < x1 - x0; x++) {
+        for (uint32_t x = 0; x < z.rows; x++) {
             float m = -INFINITY, l = 0.f, o[kPer];
 #pragma unroll
             for (uint32_t k = 0; k < kPer; k++) o[k] = 0.f;
 #pragma unroll 1
             for (uint32_t e0 = kWide ? 32 * warp : 0; e0 < n; e0 += kWide ? 256 : 32) {
-                const float *s = src + x * D;
+                const float *s = nullptr;
                 float2 v = make_float2(-INFINITY, 0.f);
                 if (e0 + lane < n) {
-                    const float2 *q = ml;
-                    if (e0) place(e0 + lane, q, s), s += x * D;
-                    v = q[x];
+                    const uint32_t at = place(a, z, e0 + lane) + x;
+                    v = a.part_ml[at];
+                    s = a.part_o + (uint64_t)at * D;
                 }
-                if (v.y == 0.f) {
+                if (v.y == 0.f) {  // a piece the row sees nothing of; its outputs may be unwritten
                     v.x = -INFINITY;
                     s = nullptr;
                 }
@@ -1109,15 +1144,14 @@ __global__ void __launch_bounds__(256, 3) k_merge(const Args a) {
                 }
             }
             const float inv = l == 0.f ? 0.f : __frcp_rn(l);
-            const uint32_t i = (x0 + x) / a.g, h = head * a.g + (x0 + x) - i * a.g;
-            uint16_t *dst = a.out + r * a.os[0] + i * a.os[1] + h * a.os[2];
+            const uint32_t i = (x_first + x) / a.g, j = x_first + x - i * a.g;
+            uint16_t *dst = out_row(a, r, head, i, j);
             if constexpr (D == 128)
                 *reinterpret_cast<uint2 *>(dst + 4 * (gl + 8 * grp)) =
                     make_uint2(Half<T>::pack(o[0] * inv, o[1] * inv), Half<T>::pack(o[2] * inv, o[3] * inv));
             else
                 *reinterpret_cast<uint32_t *>(dst + 4 * (gl + 8 * (grp >> 1)) + 2 * (grp & 1u)) = Half<T>::pack(o[0] * inv, o[1] * inv);
-            if (a.lse && lane == 0)
-                a.lse[((uint64_t)r * a.nq + i) * (a.g * a.Hkv) + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (lane == 0) write_lse(a, r, head, i, j, m, l);
         }
     }
 }
@@ -1126,7 +1160,7 @@ bool misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t
 
 struct Plan {
     uint32_t g, nh, ng, range_rows, rt, npt, pairs, one, piece_rows;
-    uint64_t items, pieces, cum_bytes, o_bytes, ml_bytes, tc_o_bytes, bytes;
+    uint64_t items, tc_rows, cum_bytes, o_bytes, bytes;
 };
 
 constexpr uint32_t kTcRows = 16;    // k_shared takes the shared part from more query rows than this per KV head
@@ -1172,13 +1206,12 @@ bool make_plan(const cg_pages *p, const cg_attention *a, Plan *o) {
     o->piece_rows = (uint32_t)(most < o->range_rows ? most : o->range_rows);
     o->items = ((uint64_t)a->n_requests * o->rt + o->npt) * o->ng;
     if (o->items > (1ull << 31)) return false;
-    o->pieces = o->items + kMaxCtas;
+    o->tc_rows = tc ? ((uint64_t)o->pairs * a->n_kv_heads + kMaxTcCtas) * 256 : 0;
+    const uint64_t rows = o->tc_rows + (o->items + kMaxCtas) * 4 * o->piece_rows;  // of partial results
+    if (rows > 0xFFFFFFFFull) return false;
     o->cum_bytes = round_up((a->n_requests + 1ull) * 8 + a->n_requests * 4ull, 256);
-    o->o_bytes = round_up(o->pieces * 4 * o->piece_rows * a->head_dim * 4, 256);
-    o->ml_bytes = round_up(o->pieces * 4 * o->piece_rows * 8, 256);
-    const uint64_t tc_rows = tc ? ((uint64_t)o->pairs * a->n_kv_heads + kMaxTcCtas) * 256 : 0;
-    o->tc_o_bytes = tc_rows * a->head_dim * 4;
-    o->bytes = o->cum_bytes + o->o_bytes + o->ml_bytes + o->tc_o_bytes + tc_rows * 8;
+    o->o_bytes = round_up(rows * a->head_dim * 4, 256);
+    o->bytes = o->cum_bytes + o->o_bytes + round_up(rows * 8, 256);
     return true;
 }
 
@@ -1242,14 +1275,14 @@ cudaError_t launch(const CUtensorMap &rows_map, const CUtensorMap &map, Args &a,
     }
     e = a.range_rows == kRows ? launch_rows<T, D, 1>(rows_map, a, sms, s) : launch_rows<T, D, 2>(rows_map, a, sms, s);
     if (e != cudaSuccess) return e;
-    // a few rows a warp where there are rows enough to fill the GPU with 24 warps an SM
-    const uint64_t per = (uint64_t)a.nq * a.g, rh = (uint64_t)a.R * a.Hkv, fit = (uint64_t)sms * 24 / rh;
-    const uint64_t chunks = fit < 1 ? 1 : fit < per ? fit : per;
-    const bool wide = rh * per <= (uint64_t)sms * 4;
+    // warps for the joins: as many as an SM holds (many rows: twice that), with a few rows each where there are rows enough
+    const uint64_t per = (uint64_t)a.nq * a.g, rh = (uint64_t)a.R * a.Hkv;
+    const bool wide = rh * per <= (uint64_t)sms * 4, many = rh * per >= (uint64_t)sms * 16;
+    const uint64_t fit = (uint64_t)sms * (many ? 64 : 24) / rh, chunks = fit < 1 ? 1 : fit < per ? fit : per;
     a.merge_rows = wide ? 1 : (uint32_t)((per + chunks - 1) / chunks);
     const uint64_t warps = rh * ((per + a.merge_rows - 1) / a.merge_rows);
-    return wide ? launch_next(k_merge<T, D, true>, (unsigned)warps, 256, 0, s, true, a)
-                : launch_next(k_merge<T, D, false>, (unsigned)((warps + 7) / 8), 256, 0, s, true, a);
+    if (wide) return launch_next(k_merge<T, D, true>, (unsigned)warps, 256, 0, s, true, a);
+    return launch_next(many ? k_merge_rows<T, D> : k_merge<T, D, false>, (unsigned)((warps + 7) / 8), 256, 0, s, true, a);
 }
 
 }  // namespace
@@ -1315,8 +1348,7 @@ extern "C" cg_status cg_attend(const cg_pages *p, const cg_attention *at, void *
     a.piece_rows = pl.piece_rows;
     a.pairs = pl.pairs;
     a.one = pl.one;
-    a.tc_o = reinterpret_cast<float *>(w + pl.cum_bytes + pl.o_bytes + pl.ml_bytes);
-    a.tc_ml = reinterpret_cast<float2 *>(w + pl.cum_bytes + pl.o_bytes + pl.ml_bytes + pl.tc_o_bytes);
+    a.part0 = (uint32_t)pl.tc_rows;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool fp16 = at->dtype == CG_FP16;
     if (at->head_dim == 128) CG_CUDA_TRY((fp16 ? launch<__half, 128>(rows_map, map, a, sms, s) : launch<__nv_bfloat16, 128>(rows_map, map, a, sms, s)));
