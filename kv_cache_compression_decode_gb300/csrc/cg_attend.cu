@@ -7,8 +7,11 @@
 // The shared part has the same keys for every request, so the query rows of
 // all requests that use one KV head form one matrix against it, and its K
 // and V are read once for the batch.  Every part may be split along its
-// tokens again; the pieces go to the workspace and k_merge joins them in a
-// fixed order.  Scores are kept in log2 units (scale * log2 e folded in).
+// tokens again; the pieces go to the workspace and a last kernel joins them in
+// a fixed order.  Scores are kept in log2 units (scale * log2 e folded in).
+// Three kernels, each started while the one before it drains: k_shared (many
+// query rows on the shared part, tcgen05), k_rows (a few query rows on their
+// tokens, bound by memory), k_merge or k_merge_rows.
 #include <cuda.h>
 #include <math.h>
 
@@ -179,7 +182,13 @@ template <uint32_t D, uint32_t kR> struct Smem {
 // tiles are 32 or 64 tokens long and the warps of a head take every second or
 // fourth 16 of them; their results go out as separate parts.  With kR = 2, two
 // sets of warps take two row tiles against the same K and V.  One more warp
-// fetches the tiles by TMA.
+// fetches the tiles by TMA, 96 KB a block and 192 KB an SM ahead.
+// Bound by DRAM: 24 requests of 32 heads, 747 MB of K and V, take 128 us, 5.8
+// TB/s (with a block to one head, whose rows are runs of 256 bytes, 168 us).
+// Where the pieces are short it is their beginnings and ends, about 2 us each:
+// 128 requests of 200 tokens and 32 rows, 101 MB, take 39 us.  The products
+// are mma.sync: 16 rows of 16 tokens are too few for the 128-row tcgen05
+// tiles, and their unit is 19% busy.
 template <class T, uint32_t D, uint32_t kR>
 __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __grid_constant__ CUtensorMap map, const Args a) {
     using S = Smem<D, kR>;
@@ -512,6 +521,9 @@ __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __
 // The running maximum m is only raised, and O rescaled, when a tile's maximum
 // lies more than 8 (a factor of 2^8) above it; P is kept kShift octaves high,
 // so that fp16 weights neither overflow (2^(8 + 6)) nor lose their small end.
+// Bound by the tensor cores: 4096 rows on each of 8 heads' 32768 tokens (550
+// GFLOP) take 309 us, 1770 TFLOP/s; with 512 rows on 16384 tokens (34 GFLOP,
+// 134 MB) 34 us, of which K and V from DRAM are 20.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kTcTok = 128, kTcSlots = 5;
 // Three warpgroups: two of softmax, one whose first warps fetch tiles and
@@ -1163,7 +1175,11 @@ struct Plan {
     uint64_t items, tc_rows, cum_bytes, o_bytes, bytes;
 };
 
-constexpr uint32_t kTcRows = 16;    // k_shared takes the shared part from more query rows than this per KV head
+// k_shared takes the shared part from more query rows than this per KV head: up
+// to 16, one row tile of k_rows reads each K and V once; from 17 on k_rows
+// would need a second one (24 rows on 512 tokens of 32 heads: k_shared is 11 us
+// of the call, and the call 134 us against 152 with k_rows doing them in pairs).
+constexpr uint32_t kTcRows = 16;
 constexpr uint32_t kMaxCtas = 304, kMaxTcCtas = 152;  // bounds of the grids that the workspace is sized for: 152 SMs
 
 bool make_plan(const cg_pages *p, const cg_attention *a, Plan *o) {
