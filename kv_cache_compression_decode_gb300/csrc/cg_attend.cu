@@ -1175,11 +1175,14 @@ struct Plan {
     uint64_t items, tc_rows, cum_bytes, o_bytes, bytes;
 };
 
-// k_shared takes the shared part from more query rows than this per KV head: up
-// to 16, one row tile of k_rows reads each K and V once; from 17 on k_rows
-// would need a second one (24 rows on 512 tokens of 32 heads: k_shared is 11 us
-// of the call, and the call 134 us against 152 with k_rows doing them in pairs).
-constexpr uint32_t kTcRows = 16;
+// Who takes the shared part, by its query rows per KV head.  Up to 16: k_rows,
+// one row tile (16 rows of 8 heads on 512 / 8192 / 32768 tokens: 15 / 23 / 40
+// us a call; with k_shared 20 / 25 / 48).  17 to 32 rows of up to four
+// requests: k_rows in blocks of two row tiles (24 rows: 16 / 26 / 44; k_shared
+// 21 / 25 / 49).  Of more requests: k_shared, since such blocks are half empty
+// on the requests' own tokens (24 requests of one row, 32 heads: 131 us;
+// k_rows 150).  More than 32 rows: k_shared.
+bool by_tensor(uint64_t rows, uint64_t requests) { return rows > 32 || (rows > kRows && requests > 4); }
 constexpr uint32_t kMaxCtas = 304, kMaxTcCtas = 152;  // bounds of the grids that the workspace is sized for: 152 SMs
 
 bool make_plan(const cg_pages *p, const cg_attention *a, Plan *o) {
@@ -1211,7 +1214,7 @@ bool make_plan(const cg_pages *p, const cg_attention *a, Plan *o) {
     if (all * a->n_kv_heads > (1ull << 31)) return false;
     o->nh = a->n_kv_heads % 4 == 0 ? 4 : a->n_kv_heads % 2 == 0 ? 2 : 1;
     o->ng = a->n_kv_heads / o->nh;
-    const bool tc = a->shared_blocks && all > kTcRows;
+    const bool tc = a->shared_blocks && by_tensor(all, a->n_requests);
     o->pairs = tc ? (uint32_t)((all + 255) / 256) : 0;
     o->one = all <= 128;
     const bool here = a->shared_blocks && !tc;  // the shared part goes through k_rows too
