@@ -71,7 +71,7 @@ class PagedCache:
         self._outgrown = []  # earlier workspaces: a captured graph may still use them
         self._status_ptr = self.status.data_ptr()
         self._index = pool.device.index if pool.is_cuda else None
-        self._attn = {}  # argument blocks and workspace sizes of attend by shape; the blocks are filled anew on every call
+        self._attn = {}  # workspace bytes of attend by shape
 
     @classmethod
     def empty(cls, L: int, n_pool: int, block_tokens: int, C: int, n_slots: int, n_blocks: int,
@@ -85,10 +85,10 @@ class PagedCache:
     def c(self) -> cg_pages:
         return self._c
 
-    def _stream(self, stream) -> Optional[int]:
-        if stream is not None:
-            return stream.cuda_stream
-        return _raw_stream(self._index) if self._index is not None else None
+    def _stream(self, stream) -> int:
+        if self._index is None:
+            raise ValueError("the pool is not in GPU memory")
+        return stream.cuda_stream if stream is not None else _raw_stream(self._index)
 
     @property
     def block_tokens(self) -> int:
@@ -194,10 +194,7 @@ class PagedCache:
             raise ValueError("more requests than slots")
         if min(layer, shared_slot, shared_blocks) < 0:
             raise ValueError("layer, shared_slot and shared_blocks are not negative")
-        key = (R, nq, hq, hd, shared_blocks)
-        a, ws_bytes = self._attn.get(key, (None, 0))
-        if a is None:
-            a = cg_attention()
+        a = cg_attention()
         a.q, a.out = q.data_ptr(), out.data_ptr()
         a.lse = lse.data_ptr() if lse is not None else None
         a.slots = _ids(slots, d, "slots") if slots is not None else None
@@ -207,11 +204,12 @@ class PagedCache:
         a.layer, a.shared_slot, a.shared_blocks = layer, shared_slot, shared_blocks
         a.q_stride[:], a.out_stride[:] = q.stride()[:3], out.stride()[:3]
         a.scale = scale if scale is not None else 1.0 / math.sqrt(hd) if hd else 0.0
-        if not ws_bytes:
+        key = (R, nq, hq, hd, shared_blocks)
+        ws_bytes = self._attn.get(key)
+        if ws_bytes is None:
             n = ct.c_size_t()
             _check(lib().cg_attend_ws_bytes(self._ref, ct.byref(a), ct.byref(n)), "cg_attend_ws_bytes")
-            ws_bytes = n.value
-            self._attn[key] = (a, ws_bytes)
+            ws_bytes = self._attn[key] = n.value
         ws = self._workspace(ws_bytes)
         _check(lib().cg_attend(self._ref, ct.byref(a), ws.data_ptr(), ws.numel(), self._status_ptr,
                                self._stream(stream)), "cg_attend")

@@ -252,6 +252,18 @@ def test_layouts_strides_slot_order_and_scale(layout, shared, R):
 
 @pytest.mark.gpu
 @needs_gpu
+@pytest.mark.parametrize("R", [3, 40])
+@pytest.mark.parametrize("scale", [0.0, 1e-20, 3.0])
+def test_scales(R, scale):
+    """Scale 0 gives the mean of the values that a query sees."""
+    cache, slots = make([9 * 16 + 3 + 7 * r for r in range(R)], 9, 16, 2, 64)
+    q, out, lse = attend(cache, slots, nq=2, Hq=8, D=64, scale=scale, shared_blocks=9)
+    cache.check()
+    check(cache, q, out, lse, slots, 1, scale)
+
+
+@pytest.mark.gpu
+@needs_gpu
 def test_default_slots_and_no_lse():
     cache, slots = make([40, 7], bt=16, Hkv=1)
     q = torch.randn((3, 1, 4, 128), device="cuda").to(FP16)  # slots 0 (empty), 1, 2

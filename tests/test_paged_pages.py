@@ -393,7 +393,12 @@ def test_python_checks():
         cache.copy(one, two)
     with pytest.raises(ValueError):
         cache.compact(two)
+    for call in (lambda: cache.fork(one, one), lambda: cache.free(one), lambda: cache.compact(), lambda: cache.copy(one, one)):
+        with pytest.raises(ValueError, match="not in GPU memory"):  # every tensor here is a CPU tensor
+            call()
     q = torch.zeros((2, 1, 4, 64), dtype=torch.float16)
+    with pytest.raises(ValueError, match="not in GPU memory"):
+        cache.attend(0, q)
     for kw in (dict(q=q.float()), dict(q=q[0]), dict(q=q, slots=one), dict(q=q, out=q[:1]), dict(q=q, lse=q),
                dict(q=q, shared_blocks=-1), dict(q=torch.zeros((4, 1, 4, 64), dtype=torch.float16))):
         with pytest.raises(ValueError):
