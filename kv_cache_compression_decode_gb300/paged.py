@@ -31,6 +31,7 @@ _DTYPES = {torch.float16: CG_FP16, torch.bfloat16: CG_BF16}
 
 
 _INT32 = (torch.int32, torch.uint32)
+_Strides = ct.c_uint64 * 3
 # The current stream's handle without building a Stream object around it (3 us of a 7 us call).
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -71,6 +72,7 @@ class PagedCache:
         self._outgrown = []  # earlier workspaces: a captured graph may still use them
         self._status_ptr = self.status.data_ptr()
         self._index = pool.device.index if pool.is_cuda else None
+        self._device, self._dtype = pool.device, _DTYPES[pool.dtype]
         self._attn = {}  # workspace bytes of attend by shape
 
     @classmethod
@@ -176,14 +178,15 @@ class PagedCache:
         shared_blocks blocks of every sequence are those of shared_slot.
         scale defaults to head_dim ** -0.5.  Returns out (shape and type of
         q); lse, if given, is a fp32 [R][n_queries][n_q_heads]."""
-        d, pool = self.pool.device, self.pool
-        if q.dtype != pool.dtype or q.dim() != 4 or q.device != d or q.stride(3) != 1:
+        d, pool, qs = self._device, self.pool, q.stride()
+        if q.dtype != pool.dtype or len(qs) != 4 or q.device != d or qs[3] != 1:
             raise ValueError("q: a tensor [R][n_queries][n_q_heads][head_dim] of the pool's type and device with "
                              "contiguous head channels is wanted")
         R, nq, hq, hd = q.shape
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=d)
-        if out.shape != q.shape or out.dtype != q.dtype or out.device != d or out.stride(3) != 1:
+        os_ = out.stride()
+        if out.shape != q.shape or out.dtype != q.dtype or out.device != d or os_[3] != 1:
             raise ValueError("out: shape, type and device of q, contiguous head channels")
         if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:3] or not lse.is_contiguous()
                                 or lse.device != d):
@@ -194,16 +197,10 @@ class PagedCache:
             raise ValueError("more requests than slots")
         if min(layer, shared_slot, shared_blocks) < 0:
             raise ValueError("layer, shared_slot and shared_blocks are not negative")
-        a = cg_attention()
-        a.q, a.out = q.data_ptr(), out.data_ptr()
-        a.lse = lse.data_ptr() if lse is not None else None
-        a.slots = _ids(slots, d, "slots") if slots is not None else None
-        a.dtype = _DTYPES[pool.dtype]
-        a.n_requests, a.n_queries, a.n_q_heads, a.head_dim = R, nq, hq, hd
-        a.n_kv_heads = pool.shape[4] // hd if hd else 0
-        a.layer, a.shared_slot, a.shared_blocks = layer, shared_slot, shared_blocks
-        a.q_stride[:], a.out_stride[:] = q.stride()[:3], out.stride()[:3]
-        a.scale = scale if scale is not None else 1.0 / math.sqrt(hd) if hd else 0.0
+        a = cg_attention(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
+                         _ids(slots, d, "slots") if slots is not None else None, self._dtype, R, nq, hq,
+                         pool.shape[4] // hd if hd else 0, hd, layer, shared_slot, shared_blocks, _Strides(*qs[:3]),
+                         _Strides(*os_[:3]), scale if scale is not None else 1.0 / math.sqrt(hd) if hd else 0.0)
         key = (R, nq, hq, hd, shared_blocks)
         ws_bytes = self._attn.get(key)
         if ws_bytes is None:
