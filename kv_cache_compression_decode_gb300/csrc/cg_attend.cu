@@ -40,7 +40,7 @@ struct Args {
     uint32_t pairs;          // k_shared: pairs of 128-row tiles of the whole batch (0: k_rows has the shared part)
     uint32_t one;            // k_shared: the batch fits one 128-row tile
     uint32_t n_tc;           // blocks of k_shared
-    uint32_t merge_rows;     // rows of a warp of k_merge
+    uint32_t merge_rows;     // rows of a warp of the joins
     uint32_t n_cta;          // blocks of k_rows
     uint64_t qs[3], os[3];
     float scale2;            // |scale| * log2 e
@@ -126,8 +126,10 @@ __device__ __forceinline__ bool next_piece(const Args &a, Walk &w, Piece &p) {
         len = a.P;
         nt = tiles_of(a, a.P);
     }
+    if (nt == 0) return false;  // this and the next: lengths that changed under the call leave tiles over
     const uint64_t at = w.t - w.base;
     const uint32_t local = (uint32_t)quot(at, nt);
+    if (w.r == a.R && local >= a.npt * a.ng) return false;
     p.item = w.r * a.rt * a.ng + local;
     p.range = local / a.ng;
     p.group = local - p.range * a.ng;

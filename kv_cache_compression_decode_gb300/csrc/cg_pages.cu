@@ -206,7 +206,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_compact_plan(Tab t, uint32_t *
         live = next;
     }
     __syncthreads();
-    for (uint32_t i = tid; i < movers; i += kPlanThreads) {  // movers == holes
+    movers = min(movers, holes);  // as many of either, unless counts changed under the call
+    for (uint32_t i = tid; i < movers; i += kPlanThreads) {
         const uint32_t s = w.src[i], d = w.dst[i];
         remap[s] = d;
         t.refs[d] = t.refs[s];
