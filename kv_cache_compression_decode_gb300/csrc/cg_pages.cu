@@ -8,7 +8,7 @@
 namespace cg {
 namespace {
 
-constexpr uint32_t kPlanThreads = 1024;
+constexpr uint32_t kPlanThreads = 512;
 constexpr uint32_t kMoveThreads = 256;
 constexpr uint32_t kVecs = 8;                    // vectors per lane in one unit of a move
 constexpr uint32_t kUnitVecs = 32u * kVecs;      // a warp's unit: 4 KiB with 16-byte vectors
@@ -83,7 +83,7 @@ struct Tab {
     uint32_t n_slots, n_blocks, n_pool, bshift;
 };
 
-// The use counts of blocks 4 tid .. 4 tid + 3 of a run of 4096: bit k set
+// The use counts of blocks 4 tid .. 4 tid + 3 of a run of 2048: bit k set
 // where block k is in use (kLive) or free; blocks past the pool are neither.
 template <bool kLive>
 __device__ __forceinline__ uint32_t use_bits(const Tab &t, uint64_t b) {
@@ -99,14 +99,26 @@ constexpr uint32_t kRun = 4u * kPlanThreads;
 
 // One block: check every child, hand out the free blocks, list the tail
 // copies.  Any fault leaves n_moves = 0 in the header and nothing changed.
-// The time, 5 us, is that of its chain of dependent loads and barriers, so the
-// first run of use counts and the tail blocks are fetched beside the checks.
+// The time, 4.6 us, is that of its chain of dependent loads and barriers, so the
+// first children, the first run of use counts and the tail blocks are fetched
+// beside the checks, by 512 threads (1024, with costlier barriers: 4.8 us).
 __global__ void __launch_bounds__(kPlanThreads) k_fork_plan(Tab t, ForkArgs f, PlanWs w, uint32_t *status) {
     let_next_start();
     __shared__ uint32_t sh[32];
     __shared__ uint64_t sh8[32];  // the wanted blocks are summed in 64 bits: each child may ask for up to 2^31
     const uint32_t tid = threadIdx.x, bt = 1u << t.bshift;
     uint32_t fr = use_bits<false>(t, 4u * tid);
+    uint32_t p_next = CG_NO_SLOT, c_next = 0, len_next = 0, held_next = 0, clen_next = 0, rv_next = 0;
+    auto load = [&](uint32_t i) {
+        p_next = i < f.n ? f.parent[i] : CG_NO_SLOT;
+        c_next = i < f.n ? f.child[i] : 0u;
+        rv_next = i < f.n && f.reserve ? f.reserve[i] : 0u;
+        len_next = p_next < t.n_slots ? t.lens[p_next] : 0u;
+        const bool in = i < f.n && c_next < t.n_slots;
+        clen_next = in ? t.lens[c_next] : 0u;
+        held_next = in ? t.tables[(uint64_t)c_next * t.n_blocks] : CG_NO_BLOCK;
+    };
+    load(tid);
     for (uint32_t s = tid; s < t.n_slots; s += kPlanThreads) w.claimed[s] = 0;
     __syncthreads();
     uint64_t total = 0;
@@ -115,17 +127,16 @@ __global__ void __launch_bounds__(kPlanThreads) k_fork_plan(Tab t, ForkArgs f, P
         const uint32_t i = i0 + tid;
         uint32_t need = 0, pl = 0, p = CG_NO_SLOT;
         if (i < f.n) {
-            p = f.parent[i];
-            const uint32_t c = f.child[i];
-            if (p != CG_NO_SLOT) {
-                if (p >= t.n_slots) bad = true;
-                else pl = t.lens[p];
-            }
+            if (i0) load(i);
+            p = p_next;
+            pl = len_next;
+            const uint32_t c = c_next;
+            if (p != CG_NO_SLOT && p >= t.n_slots) bad = true;
             if (c >= t.n_slots) bad = true;
-            else if (t.lens[c] != 0 || t.tables[(uint64_t)c * t.n_blocks] != CG_NO_BLOCK) bad = true;
+            else if (clen_next != 0 || held_next != CG_NO_BLOCK) bad = true;
             else if (atomicExch(&w.claimed[c], 1u) != 0) bad = true;
             const uint64_t rows = (uint64_t)t.n_blocks << t.bshift;
-            const uint64_t want = (uint64_t)pl + (f.reserve ? f.reserve[i] : 0u);
+            const uint64_t want = (uint64_t)pl + rv_next;
             if (want > rows) {  // covers pl > rows too
                 bad = true;
             } else {
@@ -171,7 +182,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_fork_plan(Tab t, ForkArgs f, P
 
 // One block: count the blocks in use, pair the ones past that count with the
 // holes below it (both in ascending order), move their references.  A run of
-// 4096 blocks is counted and scanned in about 4 us, and larger pools take one
+// 2048 blocks is counted and scanned in about 3.5 us, and larger pools take one
 // scan more a run.
 __global__ void __launch_bounds__(kPlanThreads) k_compact_plan(Tab t, uint32_t *remap, PlanWs w) {
     let_next_start();
@@ -194,7 +205,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_compact_plan(Tab t, uint32_t *
             if (used && b + k >= n_live) mv |= 1u << k;
             if (!used && b + k < n_live) ho |= 1u << k;
         }
-        uint32_t sum;  // both counts in one word: at most 4096 each
+        uint32_t sum;  // both counts in one word: at most 2048 each
         const uint32_t off = block_scan<uint32_t>(__popc(mv) | (__popc(ho) << 16), &sum, sh);
         uint32_t im = movers + (off & 0xFFFFu), ih = holes + (off >> 16);
         for (uint32_t k = 0; k < 4; k++) {
