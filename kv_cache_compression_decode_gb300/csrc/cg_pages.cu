@@ -347,11 +347,9 @@ __global__ void __launch_bounds__(kMoveThreads) k_move(MoveArgs a) {
     }
 }
 
-// A block per listed slot; 256 rows of 1024 entries, 180 thousand references,
-// take 6 us, one slot 2 us.  The first entry is taken with an exchange, so
-// that a slot named twice is ended by one of the two.
+// A block per listed slot.  Every entry is taken with an exchange, so that a
+// row with gaps loses all of its blocks and a slot named twice is ended once.
 __global__ void __launch_bounds__(256) k_free(Tab t, const uint32_t *slots, uint32_t n, uint32_t *status) {
-    __shared__ uint32_t first;
     for (uint32_t i = blockIdx.x; i < n; i += gridDim.x) {
         const uint32_t s = slots[i];
         if (s >= t.n_slots) {
@@ -359,17 +357,10 @@ __global__ void __launch_bounds__(256) k_free(Tab t, const uint32_t *slots, uint
             continue;
         }
         uint32_t *row = t.tables + (uint64_t)s * t.n_blocks;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            first = atomicExch(&row[0], CG_NO_BLOCK);
-            t.lens[s] = 0;
-        }
-        __syncthreads();
-        if (first == CG_NO_BLOCK) continue;  // empty, or ended by another block
+        if (threadIdx.x == 0) t.lens[s] = 0;
         for (uint32_t k = threadIdx.x; k < t.n_blocks; k += blockDim.x) {
-            const uint32_t b = k ? row[k] : first;
-            if (b == CG_NO_BLOCK) continue;
-            if (k) row[k] = CG_NO_BLOCK;
+            const uint32_t b = atomicExch(&row[k], CG_NO_BLOCK);
+            if (b == CG_NO_BLOCK) continue;  // none, or taken by another block of the call
             if (b >= t.n_pool) {
                 flag(status, CG_ERR_CORRUPT);
             } else if (atomicSub(&t.refs[b], 1u) == 0) {

@@ -1,0 +1,50 @@
+"""Paged caches in states and uses off the usual path: rows with gaps, lost
+references, corrupt entries, other streams, reassigned tensors, empty calls."""
+import ctypes as ct
+
+import numpy as np
+import pytest
+import torch
+
+from kv_cache_compression_decode_gb300 import codec as C
+from kv_cache_compression_decode_gb300 import paged
+from tests.test_paged_pages import NB, Model, _cache, _ints
+
+needs_gpu = pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")
+
+
+def flagged(cache, code):
+    with pytest.raises(C.CodecError) as e:
+        cache.check()
+    assert e.value.code == code
+
+
+@pytest.mark.gpu
+@needs_gpu
+@pytest.mark.parametrize("first", ["lost to a compaction", "lost to a fork"])
+def test_a_row_without_its_first_block_is_ended_whole(first):
+    """A compaction and a fork write NO_BLOCK over a corrupt first entry; the
+    other blocks of that row still lose their references when it ends."""
+    cache = _cache()
+    cache.fork(_ints([-1]), _ints([0]), _ints([50]))  # blocks 0..3
+    cache.lens[0] = 50
+    cache.tables[0, 0] = 4000
+    cache.refs[0] = 0  # the block that the entry named is nobody's now
+    if first == "lost to a compaction":
+        cache.compact()  # live: 1, 2, 3 -> block 3 moves to 0
+        flagged(cache, C.CG_ERR_CORRUPT)
+        assert cache.tables[0].tolist()[:4] == [NB, 1, 2, 0]
+        ended = 0
+    else:
+        cache.fork(_ints([0]), _ints([5]), _ints([0]))
+        flagged(cache, C.CG_ERR_CORRUPT)
+        assert cache.tables[5, 0].item() == NB and cache.lens[5].item() == 50
+        ended = 5
+    before = np.bincount([b for b in cache.tables.view(-1).tolist() if 0 <= b < 40], minlength=40)
+    assert np.array_equal(cache.refs.cpu().numpy(), before)
+    row = [b for b in cache.tables[ended].tolist() if b >= 0]
+    cache.free(_ints([ended, ended]))
+    cache.check()
+    want = before - np.bincount(row, minlength=40)
+    assert np.array_equal(cache.refs.cpu().numpy(), want)
+    assert (cache.tables[ended] == NB).all() and cache.lens[ended].item() == 0
