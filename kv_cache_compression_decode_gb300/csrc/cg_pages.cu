@@ -349,6 +349,9 @@ __global__ void __launch_bounds__(kMoveThreads) k_move(MoveArgs a) {
 
 // A block per listed slot.  Every entry is taken with an exchange, so that a
 // row with gaps loses all of its blocks and a slot named twice is ended once.
+// A count may pass below zero for as long as a thread that found no reference
+// takes its step back; read as signed, it counts as none all that time, so as
+// many rows succeed as there were references (fewer than 2^31), in any order.
 __global__ void __launch_bounds__(256) k_free(Tab t, const uint32_t *slots, uint32_t n, uint32_t *status) {
     for (uint32_t i = blockIdx.x; i < n; i += gridDim.x) {
         const uint32_t s = slots[i];
@@ -363,7 +366,7 @@ __global__ void __launch_bounds__(256) k_free(Tab t, const uint32_t *slots, uint
             if (b == CG_NO_BLOCK) continue;  // none, or taken by another block of the call
             if (b >= t.n_pool) {
                 flag(status, CG_ERR_CORRUPT);
-            } else if (atomicSub(&t.refs[b], 1u) == 0) {
+            } else if ((int32_t)atomicSub(&t.refs[b], 1u) <= 0) {
                 atomicAdd(&t.refs[b], 1u);
                 flag(status, CG_ERR_CORRUPT);
             }

@@ -48,3 +48,21 @@ def test_a_row_without_its_first_block_is_ended_whole(first):
     want = before - np.bincount(row, minlength=40)
     assert np.array_equal(cache.refs.cpu().numpy(), want)
     assert (cache.tables[ended] == NB).all() and cache.lens[ended].item() == 0
+
+
+@pytest.mark.gpu
+@needs_gpu
+@pytest.mark.parametrize("refs", [0, 1, 5, 299])
+def test_rows_that_share_lost_references_end_at_zero(refs):
+    """300 rows hold the same twelve blocks, which have fewer references than
+    that: ended in one call, the counts stop at zero, whatever the order."""
+    cache = _cache(slots=300)
+    row = _ints(range(7, 19))
+    for _ in range(20):
+        cache.tables[:] = row
+        cache.lens.fill_(12 * 16)
+        cache.refs.zero_()
+        cache.refs[row.long()] = refs
+        cache.free(_ints(range(300)))
+        flagged(cache, C.CG_ERR_CORRUPT)
+        assert (cache.refs == 0).all() and (cache.tables == NB).all() and (cache.lens == 0).all()
