@@ -13,10 +13,14 @@ constexpr uint32_t kMoveThreads = 256;
 constexpr uint32_t kVecs = 8;                    // vectors per lane in one unit of a move
 constexpr uint32_t kUnitVecs = 32u * kVecs;      // a warp's unit: 4 KiB with 16-byte vectors
 
+constexpr uint32_t kMaxRowBlocks = 255;  // blocks that check the children's rows beside the plan
+static_assert(kMaxRowBlocks <= kMoveThreads, "the mover reads their results a thread to a block");
+
 // Workspace: header, then u32 arrays.  Fork fills per-child entries, compact
 // per-move ones; both give the mover (src, dst, rows) lists.
 struct PlanWs {
     uint32_t *n_moves;   // header[0]
+    uint32_t *held;      // [kMaxRowBlocks] fork: what each row-checking block found
     uint32_t *src, *dst; // [max(n_pool, n_slots)] (fork's destinations are fresh[base])
     uint32_t *rows;      // [n_slots] fork: rows of the move (0: none)
     uint32_t *base;      // [n_slots] fork: the child's first entry in `fresh`
@@ -28,7 +32,7 @@ struct PlanWs {
 __host__ __device__ inline size_t plan_ws(uint32_t n_pool, uint32_t n_slots, void *ws, PlanWs *w) {
     uint32_t *p = static_cast<uint32_t *>(ws);
     const size_t m = n_pool > n_slots ? n_pool : n_slots;
-    size_t o = 64;
+    size_t o = 64 + 256;
     auto take = [&](size_t n) {
         uint32_t *at = p + o;
         o += n;
@@ -36,6 +40,7 @@ __host__ __device__ inline size_t plan_ws(uint32_t n_pool, uint32_t n_slots, voi
     };
     PlanWs t;
     t.n_moves = p;
+    t.held = p + 64;
     t.src = take(m);
     t.dst = take(m);
     t.rows = take(n_slots);
@@ -97,8 +102,10 @@ __device__ __forceinline__ uint32_t use_bits(const Tab &t, uint64_t b) {
 }
 constexpr uint32_t kRun = 4u * kPlanThreads;
 
-// One block: check every child, hand out the free blocks, list the tail
+// Block 0: check every child, hand out the free blocks, list the tail
 // copies.  Any fault leaves n_moves = 0 in the header and nothing changed.
+// The other blocks look through the children's rows, a row at a time, for a
+// block that is still held; the mover drops the call if one found any.
 // The time, 4.6 us, is that of its chain of dependent loads and barriers, so the
 // first children, the first run of use counts and the tail blocks are fetched
 // beside the checks, by 512 threads (1024, with costlier barriers: 4.8 us).
@@ -107,16 +114,30 @@ __global__ void __launch_bounds__(kPlanThreads) k_fork_plan(Tab t, ForkArgs f, P
     __shared__ uint32_t sh[32];
     __shared__ uint64_t sh8[32];  // the wanted blocks are summed in 64 bits: each child may ask for up to 2^31
     const uint32_t tid = threadIdx.x, bt = 1u << t.bshift;
+    if (blockIdx.x) {
+        bool held = false;
+        for (uint64_t i = blockIdx.x - 1u; i < f.n; i += gridDim.x - 1u) {
+            const uint32_t c = f.child[i];
+            if (c >= t.n_slots) continue;  // block 0 refuses the call
+            const uint32_t *row = t.tables + (uint64_t)c * t.n_blocks;
+#pragma unroll 4
+            for (uint64_t k = tid; k < t.n_blocks; k += kPlanThreads) held |= row[k] != CG_NO_BLOCK;
+        }
+        held = __syncthreads_or(held);
+        if (tid == 0) {
+            w.held[blockIdx.x - 1u] = held;
+            if (held) flag(status, CG_ERR_RANGE);
+        }
+        return;
+    }
     uint32_t fr = use_bits<false>(t, 4u * tid);
-    uint32_t p_next = CG_NO_SLOT, c_next = 0, len_next = 0, held_next = 0, clen_next = 0, rv_next = 0;
+    uint32_t p_next = CG_NO_SLOT, c_next = 0, len_next = 0, clen_next = 0, rv_next = 0;
     auto load = [&](uint32_t i) {
         p_next = i < f.n ? f.parent[i] : CG_NO_SLOT;
         c_next = i < f.n ? f.child[i] : 0u;
         rv_next = i < f.n && f.reserve ? f.reserve[i] : 0u;
         len_next = p_next < t.n_slots ? t.lens[p_next] : 0u;
-        const bool in = i < f.n && c_next < t.n_slots;
-        clen_next = in ? t.lens[c_next] : 0u;
-        held_next = in ? t.tables[(uint64_t)c_next * t.n_blocks] : CG_NO_BLOCK;
+        clen_next = i < f.n && c_next < t.n_slots ? t.lens[c_next] : 0u;
     };
     load(tid);
     for (uint32_t s = tid; s < t.n_slots; s += kPlanThreads) w.claimed[s] = 0;
@@ -133,7 +154,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_fork_plan(Tab t, ForkArgs f, P
             const uint32_t c = c_next;
             if (p != CG_NO_SLOT && p >= t.n_slots) bad = true;
             if (c >= t.n_slots) bad = true;
-            else if (clen_next != 0 || held_next != CG_NO_BLOCK) bad = true;
+            else if (clen_next != 0) bad = true;
             else if (atomicExch(&w.claimed[c], 1u) != 0) bad = true;
             const uint64_t rows = (uint64_t)t.n_blocks << t.bshift;
             const uint64_t want = (uint64_t)pl + rv_next;
@@ -244,6 +265,7 @@ struct MoveArgs {
     Tab t;
     ForkArgs f;
     PlanWs w;
+    uint32_t row_blocks;               // fork: blocks that checked rows
     const uint32_t *remap;
     uint32_t *status;
 };
@@ -302,7 +324,11 @@ template <int V, Mode kMode>
 __global__ void __launch_bounds__(kMoveThreads) k_move(MoveArgs a) {
     using T = typename Vec<V>::T;
     if (kMode != kCopy) wait_for_previous();  // the plan
-    const uint32_t n = a.n_dev ? *a.n_dev : a.n;
+    uint32_t n = a.n_dev ? *a.n_dev : a.n;
+    if (kMode == kFork) {
+        const bool held = threadIdx.x < a.row_blocks && a.w.held[threadIdx.x];
+        if (__syncthreads_or(held)) n = 0;
+    }
     if (kMode == kFork && n) fork_tables(a);
     if (kMode == kCompact) compact_tables(a);
     const uint32_t lane = threadIdx.x & 31u;
@@ -473,7 +499,8 @@ extern "C" cg_status cg_pages_fork(const cg_pages *p, const uint32_t *parent, co
     a.f = ForkArgs{parent, child, reserve, n};
     a.w = w;
     a.status = dev_status;
-    k_fork_plan<<<1, kPlanThreads, 0, s>>>(a.t, a.f, w, dev_status);
+    a.row_blocks = n < kMaxRowBlocks ? n : kMaxRowBlocks;
+    k_fork_plan<<<1 + a.row_blocks, kPlanThreads, 0, s>>>(a.t, a.f, w, dev_status);
     CG_CUDA_TRY(cudaGetLastError());
     CG_CUDA_TRY(launch_move<kFork>(a, align_of(p), n, n, s));
     return CG_OK;

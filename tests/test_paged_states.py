@@ -66,3 +66,26 @@ def test_rows_that_share_lost_references_end_at_zero(refs):
         cache.free(_ints(range(300)))
         flagged(cache, C.CG_ERR_CORRUPT)
         assert (cache.refs == 0).all() and (cache.tables == NB).all() and (cache.lens == 0).all()
+
+
+@pytest.mark.gpu
+@needs_gpu
+@pytest.mark.parametrize("slots,width,gap", [(8, 12, 1), (8, 12, 11), (700, 3000, 2999), (700, 3000, 513)])
+def test_fork_refuses_a_child_that_holds_any_block(slots, width, gap):
+    """A slot of length 0 whose row begins empty and holds a block further on
+    is not empty: nothing of the call is done, its siblings' part neither."""
+    cache = _cache(n_pool=40, bt=1, Cc=8, slots=slots, width=width)
+    cache.fork(_ints([-1]), _ints([0]), _ints([5]))
+    cache.lens[0] = 5
+    cache.tables[slots - 1, gap] = 30
+    cache.refs[30] = 1
+    m = Model(cache)
+    children = [1, slots - 1] if slots == 8 else list(range(1, slots))
+    cache.fork(_ints([0] * len(children)), _ints(children))
+    flagged(cache, C.CG_ERR_RANGE)
+    m.check(cache)
+    cache.free(_ints([slots - 1]))
+    m.free([slots - 1])
+    cache.fork(_ints([0] * len(children)), _ints(children))  # the next call is not affected
+    m.fork([0] * len(children), children, [0] * len(children))
+    m.check(cache)
