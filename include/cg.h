@@ -499,7 +499,8 @@ cg_status cg_pages_copy(const cg_pages *to, const cg_pages *from, const uint32_t
  * All or nothing: CG_ERR_RANGE in *dev_status and no change when a slot is
  * out of range, a child is not empty or named twice, a row would need more
  * than n_blocks entries, or too few blocks are free.  A parent's block
- * outside the pool sets CG_ERR_CORRUPT; the child gets CG_NO_BLOCK there.
+ * outside the pool sets CG_ERR_CORRUPT; the child gets CG_NO_BLOCK there (for
+ * the partly filled one too, whose fresh block then stays free).
  * ws: device, cg_pages_ws_bytes bytes, 256-byte aligned. */
 cg_status cg_pages_fork(const cg_pages *p, const uint32_t *parent, const uint32_t *child, const uint32_t *reserve,
                         uint32_t n, void *ws, size_t ws_bytes, uint32_t *dev_status, void *stream);

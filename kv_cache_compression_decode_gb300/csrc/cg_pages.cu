@@ -283,9 +283,12 @@ __device__ void fork_tables(const MoveArgs &a) {
         const uint32_t full = pl >> a.t.bshift;
         const uint32_t all = (uint32_t)(((uint64_t)pl + (a.f.reserve ? a.f.reserve[i] : 0u) + a.bt - 1u) >> a.t.bshift);
         uint32_t *row = a.t.tables + (uint64_t)c * a.t.n_blocks;
+        const bool no_tail = a.w.rows[i] && a.w.src[i] >= a.t.n_pool;  // nothing to copy: the fresh block stays free
         for (uint32_t k = threadIdx.x; k < a.t.n_blocks; k += blockDim.x) {
             uint32_t b = CG_NO_BLOCK;
-            if (k < full) {
+            if (k == full && no_tail) {
+                flag(a.status, CG_ERR_CORRUPT);
+            } else if (k < full) {
                 b = a.t.tables[(uint64_t)p * a.t.n_blocks + k];
                 if (b < a.t.n_pool) {
                     atomicAdd(&a.t.refs[b], 1u);

@@ -89,3 +89,32 @@ def test_fork_refuses_a_child_that_holds_any_block(slots, width, gap):
     cache.fork(_ints([0] * len(children)), _ints(children))  # the next call is not affected
     m.fork([0] * len(children), children, [0] * len(children))
     m.check(cache)
+
+
+@pytest.mark.gpu
+@needs_gpu
+@pytest.mark.parametrize("bad", [4000, NB])
+@pytest.mark.parametrize("n", [5, 50])
+def test_fork_of_a_context_whose_last_block_is_corrupt(n, bad):
+    """The child has no block where the parent's partly filled one lies outside
+    the pool: not one with whatever its last owner left in it."""
+    cache = _cache()
+    cache.fork(_ints([-1]), _ints([0]), _ints([n]))
+    cache.lens[0] = n
+    full = n // 16
+    cache.tables[0, full] = bad
+    m = Model(cache)
+    cache.fork(_ints([0, 0]), _ints([3, 4]), _ints([20, 0]))
+    flagged(cache, C.CG_ERR_CORRUPT)
+    first = full + 1  # fresh blocks are numbered from here: one for each tail (not taken), then the reserve
+    more = (n + 20 + 15) // 16 - full - 1
+    shared = m.tables[0][:full].tolist()
+    for slot, row in ((3, shared + [NB] + list(range(first + 1, first + 1 + more))), (4, shared + [NB])):
+        m.tables[slot, : len(row)] = row
+        m.lens[slot] = n
+        for b in row:
+            m.refs[b] += b >= 0
+    m.check(cache)
+    cache.free(_ints([3, 4]))
+    m.free([3, 4])
+    m.check(cache)
