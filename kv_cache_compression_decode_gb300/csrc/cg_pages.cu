@@ -298,7 +298,7 @@ __device__ void fork_tables(const MoveArgs &a) {
                 }
             } else if (k < all) {
                 b = a.w.fresh[base + k - full];
-                a.t.refs[b] = 1u;
+                atomicAdd(&a.t.refs[b], 1u);  // not a store: a corrupt parent may name this block too
             }
             row[k] = b;
         }

@@ -118,3 +118,19 @@ def test_fork_of_a_context_whose_last_block_is_corrupt(n, bad):
     cache.free(_ints([3, 4]))
     m.free([3, 4])
     m.check(cache)
+
+
+@pytest.mark.gpu
+@needs_gpu
+def test_a_fresh_block_that_a_corrupt_parent_names_has_both_references():
+    """The parent's row names a free block, which the same call hands out:
+    the count is the same in any order, one for each entry of the children."""
+    for _ in range(50):
+        cache = _cache(n_pool=200, slots=9, width=12)
+        cache.fork(_ints([-1]), _ints([0]), _ints([64]))
+        cache.lens[0] = 64
+        cache.tables[0, 3] = 4  # free; block 3 keeps the reference that the entry had
+        cache.fork(_ints([0] * 8), _ints(range(1, 9)), _ints([16] * 8))
+        cache.check()
+        assert cache.tables[1:, 3].tolist() == [4] * 8 and cache.tables[1:, 4].tolist() == list(range(4, 12))
+        assert cache.refs[:12].tolist() == [9, 9, 9, 1, 9] + [1] * 7
