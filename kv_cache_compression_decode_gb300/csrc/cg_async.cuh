@@ -140,6 +140,8 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) 
 }
 
 // The 16-bit types.  kExponent: the exponent bits, all set in an infinity or NaN.
+// kHigh: what a weight of at most 1 is multiplied by before it is rounded; fp16,
+// whose normal range ends at 2^-14, then keeps weights down to 2^-39.
 template <class T> struct Half;
 template <> struct Half<__half> {
     static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -155,6 +157,7 @@ template <> struct Half<__half> {
     }
     static __device__ __forceinline__ float2 unpack(uint32_t x) { return __half22float2(*reinterpret_cast<__half2 *>(&x)); }
     static constexpr uint32_t kExponent = 0x7C00u;
+    static constexpr float kHigh = 32768.f;
 };
 template <> struct Half<__nv_bfloat16> {
     static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -172,6 +175,7 @@ template <> struct Half<__nv_bfloat16> {
         return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&x));
     }
     static constexpr uint32_t kExponent = 0x7F80u;
+    static constexpr float kHigh = 1.f;
 };
 
 // Two fp32 operations in one instruction.

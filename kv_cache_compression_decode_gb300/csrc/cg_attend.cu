@@ -435,8 +435,10 @@ __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __
                         }
                     odd = __any_sync(kFull, odd);
                 }
-                const uint32_t pa[4] = {Half<T>::pack(s[0][0], s[0][1]), Half<T>::pack(s[0][2], s[0][3]),
-                                        Half<T>::pack(s[1][0], s[1][1]), Half<T>::pack(s[1][2], s[1][3])};
+                uint32_t pa[4];  // O is held kHigh times as large until the end of the piece
+#pragma unroll
+                for (uint32_t k4 = 0; k4 < 4; k4++)
+                    pa[k4] = Half<T>::pack(s[k4 >> 1][2 * (k4 & 1u)] * Half<T>::kHigh, s[k4 >> 1][2 * (k4 & 1u) + 1] * Half<T>::kHigh);
                 if (!odd) {
                     const uint32_t r = ((lane >> 3) & 1u) * 8 + (lane & 7u);
                     const uint32_t rb = vb + r * 128, x = r & 7u, hi = lane >> 4;
@@ -477,6 +479,7 @@ __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __
         }
 
         const Row done[2] = {ro[0], ro[1]};
+        constexpr float kLow = 1.f / Half<T>::kHigh;
         const bool answer = a.P == 0 && a.nh == 4 && p.n == p.of;  // the whole sequence
         const uint64_t slot = a.part0 + (((uint64_t)blockIdx.x + p.item) * 4 + col) * a.piece_rows + (warp >> 2) * kRows + rw;
 #pragma unroll
@@ -485,7 +488,7 @@ __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __
             l[e] += __shfl_xor_sync(kFull, l[e], 2);
             if (!done[e].valid) continue;
             if (answer) {
-                const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];
+                const float inv = l[e] == 0.f ? 0.f : kLow / l[e];
                 uint16_t *dst = a.out + done[e].r * a.os[0] + done[e].i * a.os[1] + done[e].h * a.os[2] + 2 * qd;
 #pragma unroll
                 for (uint32_t d = 0; d < D / 8; d++)
@@ -498,7 +501,7 @@ __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __
                 float *dst = a.part_o + at * D + 2 * qd;
 #pragma unroll
                 for (uint32_t d = 0; d < D / 8; d++)
-                    *reinterpret_cast<float2 *>(dst + 8 * d) = make_float2(o[d][2 * e], o[d][2 * e + 1]);
+                    *reinterpret_cast<float2 *>(dst + 8 * d) = make_float2(o[d][2 * e] * kLow, o[d][2 * e + 1] * kLow);
                 if (qd == 0) a.part_ml[at] = make_float2(m[e], l[e]);
             }
         }

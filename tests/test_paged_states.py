@@ -134,3 +134,41 @@ def test_a_fresh_block_that_a_corrupt_parent_names_has_both_references():
         cache.check()
         assert cache.tables[1:, 3].tolist() == [4] * 8 and cache.tables[1:, 4].tolist() == list(range(4, 12))
         assert cache.refs[:12].tolist() == [9, 9, 9, 1, 9] + [1] * 7
+
+
+@pytest.mark.gpu
+@needs_gpu
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("D,Hkv,nq,shared", [(128, 4, 1, 0), (64, 1, 3, 0), (128, 2, 1, 100), (64, 4, 1, 4)])
+def test_the_small_weights_of_a_long_context_count(dtype, D, Hkv, nq, shared):
+    """One token outweighs each of the others by e^18, past the 2^25 below
+    which an fp16 weight relative to the largest is zero; together the others
+    carry 3% of the output.  There are so many requests that one block takes
+    one's tokens alone, that token first.  A weight is rounded once (u), and
+    below fp16's normal range, with the largest at 2^15, by at most 2^-40 of
+    the largest.  The rest as for the other attention tests."""
+    n, bt, big, R = 32768, 16, 18.0, 304
+    n_pool = n // bt + 1
+    pool = torch.zeros((1, n_pool, 2, bt, Hkv * D), dtype=dtype, device="cuda")
+    pool[:, :, 1] = 64.0
+    row = np.random.default_rng(0).permutation(n_pool)[: n // bt]
+    at = shared * bt + 3  # the token that outweighs the others, among the requests' own
+    pool[0, row[at // bt], 0, at % bt, ::D] = big
+    pool[0, row[at // bt], 1, at % bt] = 1.0
+    tables = _ints(np.tile(row, R)).view(R, -1)
+    cache = paged.PagedCache(pool, tables, _ints([n] * R), torch.full((n_pool,), R, dtype=torch.int32, device="cuda"))
+    q = torch.zeros((R, nq, Hkv, D), dtype=dtype, device="cuda")
+    q[..., 0] = 1.0
+    lse = torch.empty((R, nq, Hkv), device="cuda")
+    out = cache.attend(0, q, shared_slot=0, shared_blocks=shared, scale=1.0, lse=lse)
+    cache.check()
+    u = torch.finfo(dtype).eps / 2
+    es = big * D * 2.0 ** -22
+    for i in range(nq):
+        seen = n - nq + 1 + i
+        z = np.exp(big) + (seen - 1)
+        ref = (np.exp(big) * 1.0 + (seen - 1) * 64.0) / z
+        tol = u * ref + (u + 2 * es + seen * 2.0 ** -23 + 2.0 ** -20) * ref + seen * 2.0 ** -40 * 64.0 + 2.0 ** -25
+        assert (out[:, i].double() - ref).abs().max().item() <= tol
+        want = np.log(z)
+        assert (lse[:, i].double() - want).abs().max().item() <= es + (seen + 8) * 2.0 ** -23 + want * 2.0 ** -22
