@@ -156,6 +156,7 @@ class PagedCache:
         """Decode a context into the blocks that a slot holds
         (cg_decode_paged) and set its length.  The slot needs blocks for all
         cfg.T tokens (fork with parent -1 and reserve T)."""
+        self._stream(stream)  # refuses a pool that the decoder could not write to
         if self.pool.dtype != torch.float16:
             raise ValueError("decode writes fp16: the pool is another type")
         L, n_pool, _, bt, C = self.pool.shape

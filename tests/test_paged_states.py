@@ -172,3 +172,15 @@ def test_the_small_weights_of_a_long_context_count(dtype, D, Hkv, nq, shared):
         assert (out[:, i].double() - ref).abs().max().item() <= tol
         want = np.log(z)
         assert (lse[:, i].double() - want).abs().max().item() <= es + (seen + 8) * 2.0 ** -23 + want * 2.0 ** -22
+
+
+# ---------------------------------------------------------------------------
+# The binding (no GPU)
+# ---------------------------------------------------------------------------
+
+def test_decode_into_host_memory_is_refused():
+    i32 = dict(dtype=torch.int32)
+    cache = paged.PagedCache(torch.zeros((2, 5, 2, 16, 64), dtype=torch.float16), torch.zeros((3, 4), **i32),
+                             torch.zeros(3, **i32), torch.zeros(5, **i32))
+    with pytest.raises(ValueError, match="not in GPU memory"):
+        cache.decode(C.Config(2, 20, 64), None, 0)
