@@ -10,9 +10,10 @@ cg_decode_paged), continued by other slots that share its full blocks
 All calls are asynchronous on `stream` (default: the current one), and errors
 found on the device are OR-ed into `status` as in codec.py.  A cache has one
 workspace: calls that use it (fork, compact, attend) belong on one stream, or
-are ordered by the caller.  The pool, tables, lengths and reference counts
-are plain torch tensors and may be read and written by the caller's own
-kernels between calls, e.g. to store a new token's K and V and advance `lens`.
+are ordered by the caller.  The pool's device has to be the current one.  The
+pool, tables, lengths and reference counts are plain torch tensors and may be
+read and written by the caller's own kernels between calls, e.g. to store a
+new token's K and V and advance `lens`.
 """
 from __future__ import annotations
 
@@ -34,6 +35,7 @@ _INT32 = (torch.int32, torch.uint32)
 _Strides = ct.c_uint64 * 3
 # The current stream's handle without building a Stream object around it (3 us of a 7 us call).
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _ids(t: torch.Tensor, device: torch.device, what: str) -> int:
@@ -90,6 +92,8 @@ class PagedCache:
     def _stream(self, stream) -> int:
         if self._index is None:
             raise ValueError("the pool is not in GPU memory")
+        if _current_device() != self._index:  # the device that libcg launches on
+            raise ValueError(f"the pool is on cuda:{self._index}, which is not the current device")
         return stream.cuda_stream if stream is not None else _raw_stream(self._index)
 
     @property

@@ -175,8 +175,52 @@ def test_the_small_weights_of_a_long_context_count(dtype, D, Hkv, nq, shared):
 
 
 # ---------------------------------------------------------------------------
-# The binding (no GPU)
+# The binding, with the library and the GPU replaced (no GPU)
 # ---------------------------------------------------------------------------
+
+class FakeLib:
+    """Counts the calls that would have launched something."""
+
+    def __init__(self, ws_bytes=1000):
+        self.launched, self.ws_bytes = [], ws_bytes
+
+    def cg_attend_ws_bytes(self, pages, attention, n):
+        n._obj.value = self.ws_bytes
+        return C.CG_OK
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.launched.append((name, args))
+            return C.CG_OK
+        return call
+
+
+def host_cache(monkeypatch, index=0, current=0):
+    """A cache of CPU tensors that takes itself for one on GPU `index`."""
+    i32 = dict(dtype=torch.int32)
+    cache = paged.PagedCache(torch.zeros((2, 5, 2, 16, 64), dtype=torch.float16), torch.zeros((3, 4), **i32),
+                             torch.zeros(3, **i32), torch.zeros(5, **i32))
+    fake = FakeLib()
+    monkeypatch.setattr(paged, "lib", lambda: fake)
+    monkeypatch.setattr(C, "lib", lambda: fake)
+    monkeypatch.setattr(paged, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(paged, "_current_device", lambda: current, raising=False)
+    cache._index = index
+    return cache, fake
+
+
+def test_a_pool_on_another_device_is_refused(monkeypatch):
+    """Kernels run on the current device: with the pool on another one nothing is launched."""
+    cache, fake = host_cache(monkeypatch, index=1, current=0)
+    one = torch.zeros(1, dtype=torch.int32)
+    q = torch.zeros((2, 1, 4, 64), dtype=torch.float16)
+    for call in (lambda: cache.fork(one, one), lambda: cache.free(one), lambda: cache.compact(),
+                 lambda: cache.copy(one, one), lambda: cache.attend(0, q),
+                 lambda: cache.decode(C.Config(2, 20, 64), None, 0)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+    assert not fake.launched
+
 
 def test_decode_into_host_memory_is_refused():
     i32 = dict(dtype=torch.int32)
