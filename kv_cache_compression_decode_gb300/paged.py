@@ -10,8 +10,9 @@ cg_decode_paged), continued by other slots that share its full blocks
 All calls are asynchronous on `stream` (default: the current one), and errors
 found on the device are OR-ed into `status` as in codec.py.  A cache has one
 workspace: calls that use it (fork, compact, attend) belong on one stream, or
-are ordered by the caller.  The pool's device has to be the current one.  The
-pool, tables, lengths and reference counts are plain torch tensors and may be
+are ordered by the caller, as calls on another stream are after the cache's
+construction.  What a call returns was allocated on the call's stream, as if
+that one were current.  The pool's device has to be the current one.  The pool, tables, lengths and reference counts are plain torch tensors and may be
 read and written by the caller's own kernels between calls, e.g. to store a
 new token's K and V and advance `lens`.
 """
@@ -73,6 +74,7 @@ class PagedCache:
         self._ws = torch.empty(n.value, dtype=torch.uint8, device=pool.device)
         self._outgrown = []  # earlier workspaces: a captured graph may still use them
         self._status_ptr = self.status.data_ptr()
+        self._seen = set()  # streams that status and workspace are recorded on
         self._index = pool.device.index if pool.is_cuda else None
         self._device, self._dtype = pool.device, _DTYPES[pool.dtype]
         self._attn = {}  # workspace bytes of attend by shape
@@ -94,7 +96,21 @@ class PagedCache:
             raise ValueError("the pool is not in GPU memory")
         if _current_device() != self._index:  # the device that libcg launches on
             raise ValueError(f"the pool is on cuda:{self._index}, which is not the current device")
-        return stream.cuda_stream if stream is not None else _raw_stream(self._index)
+        handle = stream.cuda_stream if stream is not None else _raw_stream(self._index)
+        if handle not in self._seen:  # a cache dropped with work in flight: its memory waits for that stream too
+            for t in (self._ws, self.status):
+                t.record_stream(stream if stream is not None else torch.cuda.current_stream(self._device))
+            self._seen.add(handle)
+        return handle
+
+    def _new(self, shape, dtype: torch.dtype, stream) -> torch.Tensor:
+        """Memory for kernels on `stream`.  Taken on that stream: what the
+        allocator has for the current one may still be in use by work queued
+        there, which `stream` does not wait for."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self._device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self._device)
 
     @property
     def block_tokens(self) -> int:
@@ -107,10 +123,11 @@ class PagedCache:
         self.status.zero_()
         _check(code, "paged cache (device)")
 
-    def _workspace(self, n: int) -> torch.Tensor:
+    def _workspace(self, n: int, stream, handle: int) -> torch.Tensor:
         if self._ws.numel() < n:
             self._outgrown.append(self._ws)
-            self._ws = torch.empty(n, dtype=torch.uint8, device=self.pool.device)
+            self._ws = self._new(n, torch.uint8, stream)
+            self._seen = {handle}
         return self._ws
 
     def fork(self, parent: torch.Tensor, child: torch.Tensor, reserve: Optional[torch.Tensor] = None,
@@ -136,7 +153,7 @@ class PagedCache:
         block's new number, -1 for a free one (cg_pages_compact)."""
         d = self.pool.device
         if remap is None:
-            remap = torch.empty(self.pool.shape[1], dtype=torch.int32, device=d)
+            remap = self._new(self.pool.shape[1], torch.int32, stream)
         if remap.shape[0] != self.pool.shape[1]:
             raise ValueError("remap has one entry per block of the pool")
         _check(lib().cg_pages_compact(self._ref, _ids(remap, d, "remap"), self._ws.data_ptr(),
@@ -189,7 +206,7 @@ class PagedCache:
                              "contiguous head channels is wanted")
         R, nq, hq, hd = q.shape
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=d)
+            out = self._new(q.shape, q.dtype, stream)
         os_ = out.stride()
         if out.shape != q.shape or out.dtype != q.dtype or out.device != d or os_[3] != 1:
             raise ValueError("out: shape, type and device of q, contiguous head channels")
@@ -212,7 +229,8 @@ class PagedCache:
             n = ct.c_size_t()
             _check(lib().cg_attend_ws_bytes(self._ref, ct.byref(a), ct.byref(n)), "cg_attend_ws_bytes")
             ws_bytes = self._attn[key] = n.value
-        ws = self._workspace(ws_bytes)
-        _check(lib().cg_attend(self._ref, ct.byref(a), ws.data_ptr(), ws.numel(), self._status_ptr,
-                               self._stream(stream)), "cg_attend")
+        handle = self._stream(stream)
+        ws = self._workspace(ws_bytes, stream, handle)
+        _check(lib().cg_attend(self._ref, ct.byref(a), ws.data_ptr(), ws.numel(), self._status_ptr, handle),
+               "cg_attend")
         return out

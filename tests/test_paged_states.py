@@ -1,6 +1,7 @@
 """Paged caches in states and uses off the usual path: rows with gaps, lost
 references, corrupt entries, other streams, reassigned tensors, empty calls."""
-import ctypes as ct
+import contextlib
+import types
 
 import numpy as np
 import pytest
@@ -8,6 +9,7 @@ import torch
 
 from kv_cache_compression_decode_gb300 import codec as C
 from kv_cache_compression_decode_gb300 import paged
+from tests.test_paged_attend import make
 from tests.test_paged_pages import NB, Model, _cache, _ints
 
 needs_gpu = pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")
@@ -174,6 +176,31 @@ def test_the_small_weights_of_a_long_context_count(dtype, D, Hkv, nq, shared):
         assert (lse[:, i].double() - want).abs().max().item() <= es + (seen + 8) * 2.0 ** -23 + want * 2.0 ** -22
 
 
+@pytest.mark.gpu
+@needs_gpu
+def test_a_call_on_another_stream_beside_pending_work():
+    """Memory that the current stream is still to write, freed and asked for
+    again by a call on another stream: the call's results stay its own."""
+    cache, slots = make([40, 300, 70], bt=16, Hkv=2)
+    q = torch.randn((3, 1, 8, 128), device="cuda").to(torch.float16)
+    want = cache.attend(1, q, slots=slots)
+    s = torch.cuda.Stream()
+    caches = [paged.PagedCache(cache.pool, cache.tables, cache.lens, cache.refs, cache.status) for _ in range(5)]
+    torch.cuda.synchronize()
+    for fresh in caches:
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+        dropped = [torch.empty_like(q) for _ in range(8)] + [torch.empty(1 << 22, dtype=torch.uint8, device="cuda")]
+        for t in dropped:
+            t.fill_(255 if t.dtype == torch.uint8 else float("nan"))
+        del dropped, t
+        out = fresh.attend(1, q, slots=slots, stream=s)
+        s.synchronize()
+        got = out.clone()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(out, want)
+        cache.check()
+
+
 # ---------------------------------------------------------------------------
 # The binding, with the library and the GPU replaced (no GPU)
 # ---------------------------------------------------------------------------
@@ -205,6 +232,8 @@ def host_cache(monkeypatch, index=0, current=0):
     monkeypatch.setattr(C, "lib", lambda: fake)
     monkeypatch.setattr(paged, "_raw_stream", lambda device: 0)
     monkeypatch.setattr(paged, "_current_device", lambda: current, raising=False)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "current")
     cache._index = index
     return cache, fake
 
@@ -228,3 +257,50 @@ def test_decode_into_host_memory_is_refused():
                              torch.zeros(3, **i32), torch.zeros(5, **i32))
     with pytest.raises(ValueError, match="not in GPU memory"):
         cache.decode(C.Config(2, 20, 64), None, 0)
+
+
+def test_memory_of_a_call_belongs_to_its_stream(monkeypatch):
+    """out, remap and the workspace are allocated on the stream whose kernels
+    write them, and a workspace that another stream goes on to use is recorded
+    there: the allocator then hands none of it out too early."""
+    cache, fake = host_cache(monkeypatch)
+    at, recorded = [None], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, at[0] = at[0], stream
+        yield
+        at[0] = before
+
+    empty, where = torch.empty, []
+
+    def logged(*args, **kw):
+        where.append(at[0])
+        return empty(*args, **kw)
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch, "empty", logged)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((t.data_ptr(), s)))
+    status = cache.status.data_ptr()
+    s, r = types.SimpleNamespace(cuda_stream=7), types.SimpleNamespace(cuda_stream=8)
+    q = torch.zeros((2, 1, 4, 64), dtype=torch.float16)
+    fake.ws_bytes = 1 << 20
+    cache.attend(0, q, stream=s)
+    assert where == [s, s]  # out and the workspace
+    name, args = fake.launched[-1]
+    assert name == "cg_attend" and args[-1] == 7
+    ws = args[2]
+    where.clear()
+    recorded.clear()
+    cache.attend(0, q, stream=s)
+    assert where == [s] and not recorded
+    cache.attend(0, q, stream=r)
+    cache.attend(0, q, stream=r)
+    assert sorted(recorded, key=str) == sorted([(ws, r), (status, r)], key=str)
+    cache.attend(0, q)
+    assert recorded[2:] == [(ws, "current"), (status, "current")] and where == [s, r, r, None]
+    where.clear()
+    cache.compact(stream=s)
+    assert where == [s]
+    cache.compact()
+    assert where == [s, None]
