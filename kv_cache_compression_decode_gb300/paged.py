@@ -120,7 +120,9 @@ class PagedCache:
         """Wait for the device and raise on any error found there."""
         torch.cuda.synchronize(self.pool.device)
         code = codec.read_status(self.status)
-        self.status.zero_()
+        if code != codec.CG_OK:
+            self.status.zero_()
+            torch.cuda.synchronize(self.pool.device)  # before any stream's next call may find an error
         _check(code, "paged cache (device)")
 
     def _workspace(self, n: int, stream, handle: int) -> torch.Tensor:

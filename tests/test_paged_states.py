@@ -205,6 +205,12 @@ def test_a_call_on_another_stream_beside_pending_work():
 # The binding, with the library and the GPU replaced (no GPU)
 # ---------------------------------------------------------------------------
 
+def cpu_cache():
+    i32 = dict(dtype=torch.int32)
+    return paged.PagedCache(torch.zeros((2, 5, 2, 16, 64), dtype=torch.float16), torch.zeros((3, 4), **i32),
+                            torch.zeros(3, **i32), torch.zeros(5, **i32))
+
+
 class FakeLib:
     """Counts the calls that would have launched something."""
 
@@ -224,9 +230,7 @@ class FakeLib:
 
 def host_cache(monkeypatch, index=0, current=0):
     """A cache of CPU tensors that takes itself for one on GPU `index`."""
-    i32 = dict(dtype=torch.int32)
-    cache = paged.PagedCache(torch.zeros((2, 5, 2, 16, 64), dtype=torch.float16), torch.zeros((3, 4), **i32),
-                             torch.zeros(3, **i32), torch.zeros(5, **i32))
+    cache = cpu_cache()
     fake = FakeLib()
     monkeypatch.setattr(paged, "lib", lambda: fake)
     monkeypatch.setattr(C, "lib", lambda: fake)
@@ -252,9 +256,7 @@ def test_a_pool_on_another_device_is_refused(monkeypatch):
 
 
 def test_decode_into_host_memory_is_refused():
-    i32 = dict(dtype=torch.int32)
-    cache = paged.PagedCache(torch.zeros((2, 5, 2, 16, 64), dtype=torch.float16), torch.zeros((3, 4), **i32),
-                             torch.zeros(3, **i32), torch.zeros(5, **i32))
+    cache = cpu_cache()
     with pytest.raises(ValueError, match="not in GPU memory"):
         cache.decode(C.Config(2, 20, 64), None, 0)
 
@@ -304,3 +306,17 @@ def test_memory_of_a_call_belongs_to_its_stream(monkeypatch):
     assert where == [s]
     cache.compact()
     assert where == [s, None]
+
+
+def test_check_waits_for_its_own_reset(monkeypatch):
+    """After check() the status is zero on the device, not only queued to be:
+    an error that a call on another stream finds next is not wiped out."""
+    cache = cpu_cache()
+    at_sync = []
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: at_sync.append(cache.status.item()))
+    cache.status[0] = 1 << C.CG_ERR_RANGE
+    flagged(cache, C.CG_ERR_RANGE)
+    assert at_sync == [1 << C.CG_ERR_RANGE, 0]
+    at_sync.clear()
+    cache.check()
+    assert set(at_sync) == {0}
