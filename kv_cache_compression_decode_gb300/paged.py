@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes as ct
 import math
+import operator
 from typing import Optional
 
 import torch
@@ -46,11 +47,27 @@ def _ids(t: torch.Tensor, device: torch.device, what: str) -> int:
     return t.data_ptr()
 
 
+def _fixed(name: str) -> property:
+    """A tensor whose address the library has: another one may not take its
+    place (`cache.lens = cache.lens + 1` would leave the calls with the old
+    one).  `cache.lens += 1` assigns the tensor that is there, and may."""
+    get = operator.attrgetter("_" + name)
+
+    def put(self, value):
+        if value is not get(self):
+            raise AttributeError(f"PagedCache.{name} cannot be replaced: write into it, in place")
+
+    return property(get, put)
+
+
 class PagedCache:
     """A pool [L][n_pool][2][block_tokens][C] (fp16 or bf16; any strides with
     the channels contiguous, e.g. a transposed view of [n_pool][L][2][bt][C])
     and its sequences: tables int32 [n_slots][n_blocks] (-1: no block), lens
-    int32 [n_slots], refs int32 [n_pool]."""
+    int32 [n_slots], refs int32 [n_pool].  The calls read and write the tensors
+    given here: change them in place."""
+
+    pool, tables, lens, refs, status = map(_fixed, ("pool", "tables", "lens", "refs", "status"))
 
     def __init__(self, pool: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
                  status: Optional[torch.Tensor] = None):
@@ -62,8 +79,8 @@ class PagedCache:
                 raise ValueError(f"{n}: a contiguous {dim}-D int32 tensor on {pool.device} is wanted")
         if lens.shape[0] != tables.shape[0] or refs.shape[0] != pool.shape[1]:
             raise ValueError("lens has one entry per slot, refs one per block of the pool")
-        self.pool, self.tables, self.lens, self.refs = pool, tables, lens, refs
-        self.status = status if status is not None else codec.new_status(pool.device)
+        self._pool, self._tables, self._lens, self._refs = pool, tables, lens, refs
+        self._status = status if status is not None else codec.new_status(pool.device)
         L, n_pool, _, bt, C = pool.shape
         sl, sb, skv, st, _ = pool.stride()
         self._c = cg_pages(pool.data_ptr(), L, C, n_pool, bt, sl, skv, sb, st, tables.data_ptr(), lens.data_ptr(),
@@ -136,7 +153,7 @@ class PagedCache:
              stream=None) -> None:
         """Start sequence child[i] as a continuation of parent[i] (-1: an
         empty one) with blocks for reserve[i] further tokens (cg_pages_fork)."""
-        d = self.pool.device
+        d = self._device
         n = parent.shape[0]
         if child.shape[0] != n or (reserve is not None and reserve.shape[0] != n):
             raise ValueError("fork: parent, child and reserve have one entry per new sequence")
@@ -147,16 +164,16 @@ class PagedCache:
 
     def free(self, slots: torch.Tensor, stream=None) -> None:
         """End the sequences in `slots` (cg_pages_free)."""
-        _check(lib().cg_pages_free(self._ref, _ids(slots, self.pool.device, "slots"), slots.shape[0],
+        _check(lib().cg_pages_free(self._ref, _ids(slots, self._device, "slots"), slots.shape[0],
                                    self._status_ptr, self._stream(stream)), "cg_pages_free")
 
     def compact(self, remap: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """Move the blocks in use to the front of the pool; returns each
         block's new number, -1 for a free one (cg_pages_compact)."""
-        d = self.pool.device
+        d = self._device
         if remap is None:
-            remap = self._new(self.pool.shape[1], torch.int32, stream)
-        if remap.shape[0] != self.pool.shape[1]:
+            remap = self._new(self._pool.shape[1], torch.int32, stream)
+        if remap.shape[0] != self._pool.shape[1]:
             raise ValueError("remap has one entry per block of the pool")
         _check(lib().cg_pages_compact(self._ref, _ids(remap, d, "remap"), self._ws.data_ptr(),
                                       self._ws.numel(), self._status_ptr, self._stream(stream)),
@@ -166,11 +183,11 @@ class PagedCache:
     def copy(self, src: torch.Tensor, dst: torch.Tensor, source: Optional["PagedCache"] = None, stream=None) -> None:
         """Copy whole blocks src[i] of `source` (default: this cache) to
         blocks dst[i] of this cache (cg_pages_copy)."""
-        d = self.pool.device
+        d = self._device
         other = source if source is not None else self
         if src.shape[0] != dst.shape[0]:
             raise ValueError("copy: src and dst have the same number of blocks")
-        if other.pool.dtype != self.pool.dtype or other.pool.device != d:
+        if other._pool.dtype != self._pool.dtype or other._device != d:
             raise ValueError("copy: both pools have one type and one device")
         _check(lib().cg_pages_copy(self._ref, other._ref, _ids(src, d, "src"), _ids(dst, d, "dst"),
                                    src.shape[0], self._status_ptr, self._stream(stream)), "cg_pages_copy")
@@ -202,7 +219,7 @@ class PagedCache:
         shared_blocks blocks of every sequence are those of shared_slot.
         scale defaults to head_dim ** -0.5.  Returns out (shape and type of
         q); lse, if given, is a fp32 [R][n_queries][n_q_heads]."""
-        d, pool, qs = self._device, self.pool, q.stride()
+        d, pool, qs = self._device, self._pool, q.stride()
         if q.dtype != pool.dtype or len(qs) != 4 or q.device != d or qs[3] != 1:
             raise ValueError("q: a tensor [R][n_queries][n_q_heads][head_dim] of the pool's type and device with "
                              "contiguous head channels is wanted")

@@ -320,3 +320,22 @@ def test_check_waits_for_its_own_reset(monkeypatch):
     at_sync.clear()
     cache.check()
     assert set(at_sync) == {0}
+
+
+@pytest.mark.parametrize("name", ["pool", "tables", "lens", "refs", "status"])
+def test_the_tensors_of_a_cache_are_written_into_not_replaced(name):
+    """The calls go by the addresses of the tensors given at construction: an
+    assignment of another tensor is refused, one in place is not."""
+    cache = cpu_cache()
+    t = getattr(cache, name)
+    with pytest.raises(AttributeError, match="in place"):
+        setattr(cache, name, t + 1)
+    assert getattr(cache, name) is t
+    with pytest.raises(AttributeError, match="in place"):
+        setattr(cache, name, t.clone())
+    if name == "lens":
+        cache.lens += 2  # assigns the same tensor
+    else:
+        setattr(cache, name, t)
+    assert getattr(cache, name) is t
+    assert cache.lens.tolist() == ([2, 2, 2] if name == "lens" else [0, 0, 0])
