@@ -456,7 +456,8 @@ cg_status cg_plan_levels(const cg_level_plan *p, uint32_t *level, cg_chunk_time 
  *                                   0: the block is free
  * An empty slot has length 0 and CG_NO_BLOCK in its whole row.  The calls
  * read the state as it is when the kernel runs, so they can be captured into
- * a CUDA graph; every result is the same from run to run.
+ * a CUDA graph; every result is the same from run to run.  With n == 0 a call
+ * does nothing, and its lists may be null.
  * Pool elements are 16-bit (fp16, or bf16 for cg_attend with CG_BF16):
  * element (layer l, K/V kv, block b, row t, channel c) is
  *     pool[l * layer_stride + kv * kv_stride + b * block_stride + t * token_stride + c]

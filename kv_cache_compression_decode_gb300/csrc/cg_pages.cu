@@ -449,6 +449,9 @@ bool state_ok(const cg_pages *p) {
            !misaligned(p->lens, 4) && !misaligned(p->refs, 4);
 }
 
+// A list of n numbers; an empty one may have no address.
+bool ids_ok(const uint32_t *ids, uint32_t n) { return (ids || n == 0) && !misaligned(ids, 4); }
+
 }  // namespace
 }  // namespace cg
 
@@ -462,8 +465,7 @@ extern "C" cg_status cg_pages_ws_bytes(const cg_pages *p, size_t *ws_bytes) {
 
 extern "C" cg_status cg_pages_copy(const cg_pages *to, const cg_pages *from, const uint32_t *src_ids,
                                    const uint32_t *dst_ids, uint32_t n, uint32_t *dev_status, void *stream) {
-    if (!pool_ok(to) || !pool_ok(from) || !src_ids || !dst_ids || misaligned(src_ids, 4) || misaligned(dst_ids, 4))
-        return CG_ERR_INVALID_ARG;
+    if (!pool_ok(to) || !pool_ok(from) || !ids_ok(src_ids, n) || !ids_ok(dst_ids, n)) return CG_ERR_INVALID_ARG;
     if (to->L != from->L || to->C != from->C || to->block_tokens != from->block_tokens) return CG_ERR_INVALID_ARG;
     if (n == 0) return CG_OK;
     MoveArgs a{};
@@ -483,8 +485,8 @@ extern "C" cg_status cg_pages_copy(const cg_pages *to, const cg_pages *from, con
 extern "C" cg_status cg_pages_fork(const cg_pages *p, const uint32_t *parent, const uint32_t *child,
                                    const uint32_t *reserve, uint32_t n, void *ws, size_t ws_bytes,
                                    uint32_t *dev_status, void *stream) {
-    if (!state_ok(p) || !parent || !child || !ws || misaligned(ws, 256) || misaligned(parent, 4) ||
-        misaligned(child, 4) || misaligned(reserve, 4) || n > p->n_slots)
+    if (!state_ok(p) || !ids_ok(parent, n) || !ids_ok(child, n) || !ws || misaligned(ws, 256) ||
+        misaligned(reserve, 4) || n > p->n_slots)
         return CG_ERR_INVALID_ARG;
     PlanWs w;
     if (ws_bytes < plan_ws(p->n_pool_blocks, p->n_slots, ws, &w)) return CG_ERR_RANGE;
@@ -511,7 +513,7 @@ extern "C" cg_status cg_pages_fork(const cg_pages *p, const uint32_t *parent, co
 
 extern "C" cg_status cg_pages_free(const cg_pages *p, const uint32_t *slots, uint32_t n, uint32_t *dev_status,
                                    void *stream) {
-    if (!state_ok(p) || !slots || misaligned(slots, 4)) return CG_ERR_INVALID_ARG;
+    if (!state_ok(p) || !ids_ok(slots, n)) return CG_ERR_INVALID_ARG;
     if (n == 0) return CG_OK;
     k_free<<<n < 65535u ? n : 65535u, 256, 0, static_cast<cudaStream_t>(stream)>>>(tab_of(p), slots, n, dev_status);
     CG_CUDA_TRY(cudaGetLastError());

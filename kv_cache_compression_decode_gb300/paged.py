@@ -238,6 +238,8 @@ class PagedCache:
             raise ValueError("more requests than slots")
         if min(layer, shared_slot, shared_blocks) < 0:
             raise ValueError("layer, shared_slot and shared_blocks are not negative")
+        if R == 0:
+            return out
         a = cg_attention(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
                          _ids(slots, d, "slots") if slots is not None else None, self._dtype, R, nq, hq,
                          pool.shape[4] // hd if hd else 0, hd, layer, shared_slot, shared_blocks, _Strides(*qs[:3]),

@@ -1,6 +1,7 @@
 """Paged caches in states and uses off the usual path: rows with gaps, lost
 references, corrupt entries, other streams, reassigned tensors, empty calls."""
 import contextlib
+import ctypes as ct
 import types
 
 import numpy as np
@@ -10,7 +11,7 @@ import torch
 from kv_cache_compression_decode_gb300 import codec as C
 from kv_cache_compression_decode_gb300 import paged
 from tests.test_paged_attend import make
-from tests.test_paged_pages import NB, Model, _cache, _ints
+from tests.test_paged_pages import NB, Model, _cache, _ints, fake_pages
 
 needs_gpu = pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")
 
@@ -339,3 +340,40 @@ def test_the_tensors_of_a_cache_are_written_into_not_replaced(name):
         setattr(cache, name, t)
     assert getattr(cache, name) is t
     assert cache.lens.tolist() == ([2, 2, 2] if name == "lens" else [0, 0, 0])
+
+
+def test_no_entries_need_no_addresses():
+    """An empty tensor's address is null; with no entries nothing is done."""
+    L, p = C.lib(), fake_pages()
+    r = ct.byref(p)
+    assert L.cg_pages_copy(r, r, None, None, 0, 0, None) == C.CG_OK
+    assert L.cg_pages_fork(r, None, None, None, 0, 4096, 1 << 30, 0, None) == C.CG_OK
+    assert L.cg_pages_free(r, None, 0, 0, None) == C.CG_OK
+    # what else is wrong is still refused
+    assert L.cg_pages_copy(r, None, None, None, 0, 0, None) == C.CG_ERR_INVALID_ARG
+    assert L.cg_pages_free(ct.byref(fake_pages(L=0)), None, 0, 0, None) == C.CG_ERR_INVALID_ARG
+    assert L.cg_pages_fork(r, None, None, None, 0, None, 1 << 30, 0, None) == C.CG_ERR_INVALID_ARG
+    assert L.cg_pages_fork(r, None, None, None, 0, 4096, 16, 0, None) == C.CG_ERR_RANGE
+
+
+@pytest.mark.gpu
+@needs_gpu
+@pytest.mark.parametrize("nq", [1, 3])
+def test_a_step_with_nothing_to_do(nq):
+    """No request ended, none came, none is left: no error and no change."""
+    cache, slots = make([40, 300], bt=16, Hkv=2)
+    m = Model(cache)
+    none = _ints([])
+    cache.fork(none, none, none)
+    cache.fork(none, none)
+    cache.free(none)
+    cache.copy(none, none)
+    q = torch.empty((0, nq, 8, 128), dtype=torch.float16, device="cuda")
+    lse = torch.empty((0, nq, 8), device="cuda")
+    assert cache.attend(1, q, slots=none, lse=lse).shape == q.shape
+    assert cache.attend(1, q, shared_slot=0, shared_blocks=1, out=q) is q
+    with pytest.raises(ValueError):
+        cache.attend(-1, q)
+    with pytest.raises(ValueError):
+        cache.attend(1, q, slots=slots)
+    m.check(cache)
