@@ -144,8 +144,9 @@ class PagedCache:
 
     def _workspace(self, n: int, stream, handle: int) -> torch.Tensor:
         if self._ws.numel() < n:
+            # at least twice the last one: all that are kept are then at most four times what is needed
             self._outgrown.append(self._ws)
-            self._ws = self._new(n, torch.uint8, stream)
+            self._ws = self._new(max(n, 2 * self._ws.numel()), torch.uint8, stream)
             self._seen = {handle}
         return self._ws
 

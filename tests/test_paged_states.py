@@ -377,3 +377,19 @@ def test_a_step_with_nothing_to_do(nq):
     with pytest.raises(ValueError):
         cache.attend(1, q, slots=slots)
     m.check(cache)
+
+
+def test_a_growing_batch_holds_a_few_times_its_workspace(monkeypatch):
+    """Workspaces that a captured graph may still use are kept; a batch that
+    grows by a request at a time leaves few of them, four times the need in all."""
+    cache, fake = host_cache(monkeypatch)
+    sizes = []
+    for R in range(1, 300):
+        fake.ws_bytes = 1000 + 5000 * R
+        cache.attend(0, torch.zeros((R, 1, 4, 64), dtype=torch.float16), slots=torch.zeros(R, dtype=torch.int32))
+        name, args = fake.launched[-1]
+        assert args[3] >= fake.ws_bytes
+        sizes.append(args[3])
+        held = cache._ws.numel() + sum(t.numel() for t in cache._outgrown)
+        assert held <= 4 * fake.ws_bytes
+    assert len(set(sizes)) <= 10 and sizes == sorted(sizes)
