@@ -245,7 +245,7 @@ class PagedCache:
                          _ids(slots, d, "slots") if slots is not None else None, self._dtype, R, nq, hq,
                          pool.shape[4] // hd if hd else 0, hd, layer, shared_slot, shared_blocks, _Strides(*qs[:3]),
                          _Strides(*os_[:3]), scale if scale is not None else 1.0 / math.sqrt(hd) if hd else 0.0)
-        key = (R, nq, hq, hd, shared_blocks)
+        key = (R, nq, hq, hd, shared_blocks > 0)
         ws_bytes = self._attn.get(key)
         if ws_bytes is None:
             n = ct.c_size_t()

@@ -10,7 +10,7 @@ import torch
 
 from kv_cache_compression_decode_gb300 import codec as C
 from kv_cache_compression_decode_gb300 import paged
-from tests.test_paged_attend import make
+from tests.test_paged_attend import fake_attention, make
 from tests.test_paged_pages import NB, Model, _cache, _ints, fake_pages
 
 needs_gpu = pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")
@@ -393,3 +393,22 @@ def test_a_growing_batch_holds_a_few_times_its_workspace(monkeypatch):
         held = cache._ws.numel() + sum(t.numel() for t in cache._outgrown)
         assert held <= 4 * fake.ws_bytes
     assert len(set(sizes)) <= 10 and sizes == sorted(sizes)
+
+
+def test_the_sizes_kept_by_shape_do_not_grow_with_the_shared_blocks(monkeypatch):
+    cache, fake = host_cache(monkeypatch)
+    q = torch.zeros((2, 1, 4, 64), dtype=torch.float16)
+    for shared in range(5):
+        cache.attend(0, q, shared_blocks=shared)
+    assert len(cache._attn) == 2  # with and without
+
+
+def test_workspace_bytes_depend_on_whether_blocks_are_shared_alone():
+    L, n = C.lib(), ct.c_size_t()
+    for R, nq in ((1, 1), (4, 3), (60, 2)):
+        sizes = set()
+        for shared in (1, 2, 7, 12):
+            a = fake_attention(n_requests=R, n_queries=nq, shared_blocks=shared)
+            assert L.cg_attend_ws_bytes(ct.byref(fake_pages()), ct.byref(a), ct.byref(n)) == C.CG_OK
+            sizes.add(n.value)
+        assert len(sizes) == 1
