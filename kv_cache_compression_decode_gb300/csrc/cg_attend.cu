@@ -1215,8 +1215,11 @@ bool make_plan(const cg_pages *p, const cg_attention *a, Plan *o) {
     // a tensor map's strides have 40 bits, and its rows and blocks may not be empty strides
     if ((p->kv_stride | block | p->token_stride) >> 39 || !p->kv_stride || (p->n_pool_blocks > 1 && !block)) return false;
     o->g = a->n_q_heads / a->n_kv_heads;
-    const uint64_t per = (uint64_t)a->n_queries * o->g, all = per * a->n_requests;
-    if (all * a->n_kv_heads > (1ull << 31)) return false;
+    constexpr uint64_t kMost = 1ull << 31;  // query rows; compared before each product, so that none wraps
+    const uint64_t per = (uint64_t)a->n_queries * o->g;
+    if (per > kMost || per * a->n_requests > kMost) return false;
+    const uint64_t all = per * a->n_requests;
+    if (all * a->n_kv_heads > kMost) return false;
     o->nh = a->n_kv_heads % 4 == 0 ? 4 : a->n_kv_heads % 2 == 0 ? 2 : 1;
     o->ng = a->n_kv_heads / o->nh;
     const bool tc = a->shared_blocks && by_tensor(all, a->n_requests);

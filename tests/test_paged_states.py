@@ -412,3 +412,12 @@ def test_workspace_bytes_depend_on_whether_blocks_are_shared_alone():
             assert L.cg_attend_ws_bytes(ct.byref(fake_pages()), ct.byref(a), ct.byref(n)) == C.CG_OK
             sizes.add(n.value)
         assert len(sizes) == 1
+
+
+def test_a_row_count_past_64_bits_is_refused():
+    """2^31 queries of 2^31 heads for four requests are 2^64 rows: none, where
+    the product wraps."""
+    L, p, n = C.lib(), fake_pages(), ct.c_size_t()
+    for nq, hq, R in ((1 << 31, 1 << 31, 4), (1 << 31, 1 << 31, 5), (1 << 31, 1 << 30, 1 << 3), (0xFFFFFFFF, 1, 1)):
+        a = fake_attention(n_queries=nq, n_q_heads=hq, n_requests=R)
+        assert L.cg_attend_ws_bytes(ct.byref(p), ct.byref(a), ct.byref(n)) == C.CG_ERR_INVALID_ARG, (nq, hq, R)
