@@ -476,8 +476,8 @@ typedef struct {
 
 /* Workspace bytes of the page calls on `p` (cg_pages_fork, cg_pages_compact).
  * Host only.  CG_ERR_INVALID_ARG for zero sizes, block_tokens not a power of
- * two, token_stride < C, or n_blocks * block_tokens above 2^31 (token
- * positions are 32-bit). */
+ * two, token_stride < C, n_slots above 2^31, or n_blocks * block_tokens above
+ * 2^31 (token positions are 32-bit). */
 cg_status cg_pages_ws_bytes(const cg_pages *p, size_t *ws_bytes);
 
 /* Copy n whole blocks, every layer, K and V: block dst_ids[i] of `to` gets
@@ -510,7 +510,7 @@ cg_status cg_pages_fork(const cg_pages *p, const uint32_t *parent, const uint32_
  * reference, the row becomes CG_NO_BLOCK and the length 0.  An empty slot, or
  * one named twice, is ended once.  A slot out of range sets CG_ERR_RANGE and
  * is skipped; a block outside the pool, or one that has no reference left,
- * sets CG_ERR_CORRUPT and its count stays as it is. */
+ * sets CG_ERR_CORRUPT and its count stays as it is.  n is at most 2^31. */
 cg_status cg_pages_free(const cg_pages *p, const uint32_t *slots, uint32_t n, uint32_t *dev_status, void *stream);
 
 /* Move the blocks in use to the front of the pool: with n_live blocks in use,

@@ -444,7 +444,7 @@ bool pool_ok(const cg_pages *p) {
 }
 
 bool state_ok(const cg_pages *p) {
-    return pool_ok(p) && p->tables && p->lens && p->refs && p->n_slots && p->n_blocks &&
+    return pool_ok(p) && p->tables && p->lens && p->refs && p->n_slots && p->n_slots <= (1u << 31) && p->n_blocks &&
            (uint64_t)p->n_blocks * p->block_tokens <= (1ull << 31) && !misaligned(p->tables, 4) &&
            !misaligned(p->lens, 4) && !misaligned(p->refs, 4);
 }
@@ -513,7 +513,7 @@ extern "C" cg_status cg_pages_fork(const cg_pages *p, const uint32_t *parent, co
 
 extern "C" cg_status cg_pages_free(const cg_pages *p, const uint32_t *slots, uint32_t n, uint32_t *dev_status,
                                    void *stream) {
-    if (!state_ok(p) || !ids_ok(slots, n)) return CG_ERR_INVALID_ARG;
+    if (!state_ok(p) || !ids_ok(slots, n) || n > (1u << 31)) return CG_ERR_INVALID_ARG;
     if (n == 0) return CG_OK;
     k_free<<<n < 65535u ? n : 65535u, 256, 0, static_cast<cudaStream_t>(stream)>>>(tab_of(p), slots, n, dev_status);
     CG_CUDA_TRY(cudaGetLastError());

@@ -421,3 +421,16 @@ def test_a_row_count_past_64_bits_is_refused():
     for nq, hq, R in ((1 << 31, 1 << 31, 4), (1 << 31, 1 << 31, 5), (1 << 31, 1 << 30, 1 << 3), (0xFFFFFFFF, 1, 1)):
         a = fake_attention(n_queries=nq, n_q_heads=hq, n_requests=R)
         assert L.cg_attend_ws_bytes(ct.byref(p), ct.byref(a), ct.byref(n)) == C.CG_ERR_INVALID_ARG, (nq, hq, R)
+
+
+def test_numbers_that_the_kernels_cannot_count_to_are_refused():
+    """The kernels step through slots and lists with 32-bit numbers: past 2^31
+    a step could wrap and the loop not end."""
+    L, n = C.lib(), ct.c_size_t()
+    assert L.cg_pages_ws_bytes(ct.byref(fake_pages(n_slots=1 << 31)), ct.byref(n)) == C.CG_OK
+    big = fake_pages(n_slots=(1 << 31) + 1)
+    assert L.cg_pages_ws_bytes(ct.byref(big), ct.byref(n)) == C.CG_ERR_INVALID_ARG
+    assert L.cg_pages_fork(ct.byref(big), 4096, 4096, None, 0, 4096, 1 << 40, 0, None) == C.CG_ERR_INVALID_ARG
+    assert L.cg_pages_free(ct.byref(big), 4096, 0, 0, None) == C.CG_ERR_INVALID_ARG
+    assert L.cg_pages_compact(ct.byref(big), 4096, 4096, 16, 0, None) == C.CG_ERR_INVALID_ARG
+    assert L.cg_pages_free(ct.byref(fake_pages()), 4096, (1 << 31) + 1, 0, None) == C.CG_ERR_INVALID_ARG
