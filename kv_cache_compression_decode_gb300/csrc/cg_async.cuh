@@ -191,12 +191,6 @@ __device__ __forceinline__ void add2(float &x, float &y, float a, float b) {
         : "+f"(x), "+f"(y)
         : "f"(a), "f"(b));
 }
-__device__ __forceinline__ void mul2(float &x, float &y, float f) {
-    asm("{\n\t.reg .b64 s, t, v;\n\tmov.b64 s, {%0, %1};\n\tmov.b64 t, {%2, %2};\n\t"
-        "mul.rn.f32x2 v, s, t;\n\tmov.b64 {%0, %1}, v;\n\t}"
-        : "+f"(x), "+f"(y)
-        : "f"(f));
-}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
