@@ -10,7 +10,7 @@ import torch
 
 from kv_cache_compression_decode_gb300 import codec as C
 from kv_cache_compression_decode_gb300 import paged
-from tests.test_paged_attend import fake_attention, make
+from tests.test_paged_attend import attend, check, fake_attention, make
 from tests.test_paged_pages import NB, Model, _cache, _ints, fake_pages
 
 needs_gpu = pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")
@@ -200,6 +200,21 @@ def test_a_call_on_another_stream_beside_pending_work():
         torch.cuda.synchronize()
         assert torch.equal(got, want) and torch.equal(out, want)
         cache.check()
+
+
+@pytest.mark.gpu
+@needs_gpu
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("nq,Hq,Hkv,D,shared", [(33, 4, 4, 128, 0), (65, 2, 1, 64, 6), (150, 4, 2, 128, 6), (500, 1, 1, 128, 0)])
+def test_a_prompt_of_many_tokens_over_its_context(dtype, nq, Hq, Hkv, D, shared):
+    """The question after a context: each query token sees those before it, row
+    ranges begin and end inside the drafted part, one request has no context."""
+    P = shared * 16
+    lens = [P + nq + 77, P + nq - (shared > 0), 0]
+    cache, slots = make(lens, shared, 16, Hkv, D, dtype, seed=nq)
+    q, out, lse = attend(cache, slots, nq=nq, Hq=Hq, D=D, shared_blocks=shared)
+    cache.check()
+    check(cache, q, out, lse, slots, 1, D ** -0.5)
 
 
 # ---------------------------------------------------------------------------
