@@ -497,6 +497,7 @@ cg_status cg_pages_copy(const cg_pages *to, const cg_pages *from, const uint32_t
  * parent[i] == CG_NO_SLOT it starts empty, with blocks for reserve[i] tokens.
  * Fresh blocks are the lowest-numbered free ones, handed out in the order of
  * i.  parent / child / reserve: device [n] (reserve may be null: 0).
+ * More children than slots are refused on the host (CG_ERR_INVALID_ARG).
  * All or nothing: CG_ERR_RANGE in *dev_status and no change when a slot is
  * out of range, a child is not empty or named twice, a row would need more
  * than n_blocks entries, or too few blocks are free.  A parent's block
@@ -539,14 +540,17 @@ cg_status cg_pages_compact(const cg_pages *p, uint32_t *remap, void *ws, size_t 
  * cg_pages_fork leaves them) and are read through that slot's row.  Rows of
  * the pool at or past a sequence's length are never used, whatever they hold,
  * and a token's infinities and NaNs reach the queries that see it alone.  out
- * may not overlap q or the pool.
+ * may not overlap q or the pool, and no two of its elements may share an
+ * address.
  * Scores, softmax sums and outputs are accumulated in fp32; the weights
- * e^{s_t - max} are rounded to the 16-bit type for the product with V.
+ * e^{s_t - max} are rounded to the 16-bit type for the product with V, fp16
+ * ones scaled by a power of two first: a weight above 2^-31 of the largest is
+ * not lost (2^-40 on the requests' own tokens).
  * Device-side errors: CG_ERR_RANGE for a slot out of range, a length above
- * n_blocks * block_tokens, a non-empty sequence whose first query token lies
- * in the shared blocks (those requests are answered as empty), or a block
- * outside the pool among a sequence's tokens; CG_ERR_TIMEOUT if a wait for a
- * copy gave up.
+ * n_blocks * block_tokens, a non-empty sequence whose first query token does
+ * not see all the shared tokens, n < shared_blocks * block_tokens + n_queries
+ * - 1 (those requests are answered as empty), or a block outside the pool
+ * among a sequence's tokens; CG_ERR_TIMEOUT if a wait for a copy gave up.
  */
 #define CG_FP16 0u
 #define CG_BF16 1u

@@ -66,7 +66,7 @@ __device__ __forceinline__ uint32_t tokens_of(const Args &a, uint32_t r, bool *b
         return 0;
     }
     const uint32_t n = a.lens[s];
-    // the first query token, n - nq, has to lie past the shared tokens
+    // the first query token, which sees n - nq + 1 tokens, has to see all the shared ones
     if (n != 0 && (n > ((uint64_t)a.n_blocks << a.bshift) || (a.P && (uint64_t)n + 1 < (uint64_t)a.P + a.nq))) {
         *bad = true;
         return 0;

@@ -319,10 +319,11 @@ __device__ void compact_tables(const MoveArgs &a) {
 
 // The moves.  A warp takes a unit of 256 vectors of one (move, layer, K/V)
 // and has 8 loads a lane in flight before the first store: 96 KB an SM with
-// the 24 warps that 80 registers allow.  Bound by DRAM: 500 blocks of 80
+// the 24 warps that a copy's 80 registers allow, 64 KB with the 16 warps of a
+// fork (110 registers) or a compaction (104).  Bound by DRAM: 500 blocks of 80
 // layers, 5.24 GB read and written, take 781 us, 6.7 TB/s (99% of a plain
 // copy); 32 tails of one parent, read from L2 and written once each, 671 MB,
-// 143 us, the rate at which memory takes writes (4.7 TB/s).
+// 138 us, 4.9 TB/s of writes (a plain fill of 671 MB takes 168 us, 4.0 TB/s).
 template <int V, Mode kMode>
 __global__ void __launch_bounds__(kMoveThreads) k_move(MoveArgs a) {
     using T = typename Vec<V>::T;
@@ -381,6 +382,9 @@ __global__ void __launch_bounds__(kMoveThreads) k_move(MoveArgs a) {
 // A count may pass below zero for as long as a thread that found no reference
 // takes its step back; read as signed, it counts as none all that time, so as
 // many rows succeed as there were references (fewer than 2^31), in any order.
+// Bound by the chain of two atomics an entry and, where many rows share blocks,
+// by those on one count: 256 rows of 1024 entries, 180 thousand references, take
+// 8.5 us with cold caches, one slot 3 us.
 __global__ void __launch_bounds__(256) k_free(Tab t, const uint32_t *slots, uint32_t n, uint32_t *status) {
     for (uint32_t i = blockIdx.x; i < n; i += gridDim.x) {
         const uint32_t s = slots[i];

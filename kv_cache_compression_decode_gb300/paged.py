@@ -11,8 +11,10 @@ All calls are asynchronous on `stream` (default: the current one), and errors
 found on the device are OR-ed into `status` as in codec.py.  A cache has one
 workspace: calls that use it (fork, compact, attend) belong on one stream, or
 are ordered by the caller, as calls on another stream are after the cache's
-construction.  What a call returns was allocated on the call's stream, as if
-that one were current.  The pool's device has to be the current one.  The pool, tables, lengths and reference counts are plain torch tensors and may be
+construction.  A captured graph uses the cache's workspace: keep the cache for
+as long as the graph.  What a call returns was allocated on the call's stream,
+as if that one were current.  The pool's device has to be the current one.  The
+pool, tables, lengths and reference counts are plain torch tensors and may be
 read and written by the caller's own kernels between calls, e.g. to store a
 new token's K and V and advance `lens`.
 """
