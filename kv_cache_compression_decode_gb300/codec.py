@@ -191,6 +191,14 @@ def _stream_ptr(stream: Optional[torch.cuda.Stream]) -> int:
     return int(s.cuda_stream)
 
 
+def _wait_for_current(stream: Optional[torch.cuda.Stream], dev: torch.device) -> None:
+    """Before a launch on `stream` into memory that the call has just taken on
+    the current stream: zeros are still queued there, and so may be work of
+    the memory's last owner."""
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream(dev))
+
+
 @dataclasses.dataclass
 class Config:
     """Codec configuration (mirrors cg_config); `step` is the per-layer step."""
@@ -517,11 +525,13 @@ def encode(cfg: Config, kv: torch.Tensor, stream=None) -> Encoded:
     on any device status."""
     dev = _cuda_device_of(kv)
     enc = Encoder(cfg, dev)
+    _wait_for_current(stream, dev)
     enc.launch(kv, stream)
     torch.cuda.synchronize(dev)
     st = read_status(enc.status)
     if st == CG_ERR_RANGE and enc.sizes.n_escapes > enc.out.escapes.numel():
         enc = Encoder(cfg, dev, escapes_cap=int(enc.sizes.n_escapes))
+        _wait_for_current(stream, dev)
         enc.launch(kv, stream)
         torch.cuda.synchronize(dev)
         st = read_status(enc.status)
@@ -558,6 +568,7 @@ def encode_levels(cfg: Config, kv: torch.Tensor, mults: Sequence[float], share_a
                 o.anchors, o.scales = outs[0].anchors, outs[0].scales
         arr = (cg_encoded * n)(*[o.c() for o in outs])
         status = new_status(dev)
+        _wait_for_current(stream, dev)
         code = lib().cg_encode_levels(ct.byref(cfg.c()), n, m32.ctypes.data, kv.data_ptr(), ws.data_ptr(), ws.numel(),
                                       arr, ct.addressof(sizes), status.data_ptr(), _stream_ptr(stream))
         _check(code, "cg_encode_levels")
@@ -624,6 +635,7 @@ def ablation(cfg: Config, kv: torch.Tensor, stream=None) -> dict:
     ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
     out = torch.zeros(len(ABLATION_FIELDS), dtype=torch.float64, device=dev)
     status = new_status(dev)
+    _wait_for_current(stream, dev)
     _check(lib().cg_ablation(ct.byref(cfg.c()), kv.data_ptr(), ws.data_ptr(), ws.numel(), out.data_ptr(),
                              status.data_ptr(), _stream_ptr(stream)), "cg_ablation")
     torch.cuda.synchronize(dev)
@@ -645,6 +657,7 @@ def decode(cfg: Config, enc: Encoded, out: Optional[torch.Tensor] = None, stream
     if out is None:
         out = torch.empty((cfg.L, 2, cfg.T, cfg.C), dtype=torch.float16, device=dev)
     status = new_status(dev)
+    _wait_for_current(stream, dev)
     cg_decode(cfg, enc, out, status, stream)
     torch.cuda.synchronize(dev)
     _check(read_status(status), "cg_decode (device)")
