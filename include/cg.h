@@ -582,6 +582,92 @@ cg_status cg_attend_ws_bytes(const cg_pages *p, const cg_attention *a, size_t *w
 cg_status cg_attend(const cg_pages *p, const cg_attention *a, void *ws, size_t ws_bytes, uint32_t *dev_status,
                     void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * A paged pool held in 4 or 8 bits.  Tokens are quantised as they are stored,
+ * read back, and attended to as they lie.  The page calls above work on such
+ * a pool as it is: a token's row of 16-bit words is moved whole.  (The pages
+ * quantize a cache for transfer only; the calls are this library's.)
+ *
+ * A row holds the C = n_kv_heads * head_dim channels of one token's K or V at
+ * one layer, in groups of `group` channels that share a scale and a low value:
+ *   codes   C * bits / 8 bytes, channel 0 first; with 4 bits an even channel
+ *           is the low half of its byte
+ *   pairs   16-bit scale, 16-bit low value for each of the C / group groups
+ *   padding up to a multiple of 16 bytes, never used
+ * A code q stands for low + q * scale.  The row's width in 16-bit words
+ * (cg_quant_row) is the C of the cg_pages that describes the pool.
+ */
+typedef struct {
+    uint32_t dtype;                /* CG_FP16 or CG_BF16: scales and low values, and every tensor of the calls */
+    uint32_t bits;                 /* 4 or 8 */
+    uint32_t group;                /* 32, 64 or 128, at most head_dim */
+    uint32_t n_kv_heads, head_dim; /* head_dim: 64 or 128 */
+} cg_quant;
+
+/* Words of a row.  Host only.  CG_ERR_INVALID_ARG for a format that is not one. */
+cg_status cg_quant_row(const cg_quant *f, uint32_t *row);
+
+/* Rows of K and V beside the pool: row j of layer i is channels
+ *     k[i * k_stride[0] + j * k_stride[1] + c],  c < C
+ * (v likewise).  Sequence r is the one in slot slots[r]; it has the rows
+ * first[r] .. first[r + 1] - 1, or n_rows / n_seqs of them where first is
+ * null.  They are its tokens from start[r] on or, where start is null, its last
+ * ones: lens has been advanced past new tokens already, as for cg_attend.  Rows
+ * before first[0] and from first[n_seqs] on are nobody's: neither read nor
+ * written. */
+typedef struct {
+    uint16_t *k, *v;       /* device */
+    const uint32_t *slots; /* device [n_seqs], or NULL: sequence r is slot r */
+    const uint32_t *first; /* device [n_seqs + 1], ascending, or NULL */
+    const uint32_t *start; /* device [n_seqs], or NULL */
+    uint32_t n_seqs, n_rows;
+    uint32_t layer, n_layers;          /* layers layer .. layer + n_layers - 1 of the pool */
+    uint64_t k_stride[2], v_stride[2]; /* elements: layer, row */
+} cg_token_rows;
+
+/* Quantise the rows of k and v and store them at their tokens' places.  For
+ * each group: low is its smallest value, d its largest less low, rounded to
+ * fp32; scale the smallest number of the 16-bit type with scale * (2^bits - 1)
+ * >= d; a code is (x - low, rounded to fp32) / scale, to the nearest, ties to
+ * even (0 where scale is 0).  So |x - value| is at most scale / 2 and low is
+ * exact.  A group with a NaN or an infinity, or whose d is not finite, is
+ * stored as NaN throughout and sets CG_ERR_NONFINITE in *dev_status.
+ * An empty sequence's rows are not used.  CG_ERR_RANGE in *dev_status, and the
+ * rows are not used, for a slot out of range, a length above n_blocks *
+ * block_tokens, tokens past the sequence's length (or more rows than it has
+ * tokens), or a block outside the pool.  A place that two rows are stored to is
+ * left with unspecified values.  With n_seqs or n_rows == 0 nothing is done.
+ * Host checks (CG_ERR_INVALID_ARG): null pointers, a format that is not one, p->C
+ * other than its row, layers that the pool does not have, n_rows no multiple of
+ * n_seqs where first is null, and a pool, k, v or stride (of a dimension with
+ * more than one element) that is not a multiple of 16 bytes. */
+cg_status cg_quant_write(const cg_pages *p, const cg_quant *f, const cg_token_rows *rows, uint32_t *dev_status,
+                         void *stream);
+
+/* The reverse: rows of k and v get low + code * scale, one fp32 multiply-add
+ * and one rounding to the 16-bit type (a finite value past its range becomes
+ * its largest number).  Rows that cg_quant_write would not use are left as they
+ * are, with the same errors. */
+cg_status cg_quant_read(const cg_pages *p, const cg_quant *f, const cg_token_rows *rows, uint32_t *dev_status,
+                        void *stream);
+
+/*
+ * cg_attend on such a pool: `a` and its meaning, its errors and its guarantees
+ * are those of cg_attend, with K and V the values that the codes stand for and
+ * a->dtype, n_kv_heads and head_dim those of the format.
+ * Codes go into the products as they are, exactly; q is exact but for parts
+ * below 2^-25 of a query's largest channel, and scales, low values, softmax
+ * sums and outputs are applied and accumulated in fp32.  The product of a
+ * weight and a scale is rounded to 11 bits for the product with V's codes (one
+ * above 2^-30 of the largest is not lost).  The shared blocks of more query rows than
+ * a batch of single tokens has (see cg_quant_attend_ws_bytes) are first read into the
+ * workspace as cg_quant_read would read them, and attended to as by cg_attend.
+ */
+cg_status cg_quant_attend_ws_bytes(const cg_pages *p, const cg_quant *f, const cg_attention *a, size_t *ws_bytes);
+cg_status cg_quant_attend(const cg_pages *p, const cg_quant *f, const cg_attention *a, void *ws, size_t ws_bytes,
+                          uint32_t *dev_status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,7 +10,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libcg.so")
-SOURCES = ["cg_encode.cu", "cg_decode.cu", "cg_host.cu", "cg_pages.cu", "cg_attend.cu"]
+SOURCES = ["cg_encode.cu", "cg_decode.cu", "cg_host.cu", "cg_pages.cu", "cg_attend.cu", "cg_quant.cu", "cg_quant_attend.cu",
+           *(f"cg_quant_rows_{bits}_{d}_{t}.cu" for bits in (4, 8) for d in (128, 64) for t in "fb")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 

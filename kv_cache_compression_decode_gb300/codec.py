@@ -97,6 +97,16 @@ class cg_attention(ct.Structure):
                 ("q_stride", ct.c_uint64 * 3), ("out_stride", ct.c_uint64 * 3), ("scale", ct.c_float)]
 
 
+class cg_quant(ct.Structure):
+    _fields_ = [(n, ct.c_uint32) for n in ("dtype", "bits", "group", "n_kv_heads", "head_dim")]
+
+
+class cg_token_rows(ct.Structure):
+    _fields_ = [("k", ct.c_void_p), ("v", ct.c_void_p), ("slots", ct.c_void_p), ("first", ct.c_void_p),
+                ("start", ct.c_void_p), ("n_seqs", ct.c_uint32), ("n_rows", ct.c_uint32), ("layer", ct.c_uint32),
+                ("n_layers", ct.c_uint32), ("k_stride", ct.c_uint64 * 2), ("v_stride", ct.c_uint64 * 2)]
+
+
 ABLATION_FIELDS = ("values", "delta_bits_channel", "delta_bits_slice", "delta_bits_global", "escape_bits",
                    "anchor_bits_raw", "anchor_bits_channel")
 
@@ -118,7 +128,8 @@ EXPORTS = ("cg_status_string", "cg_status_from_flags", "cg_encode_bounds", "cg_e
            "cg_deserialize_header", "cg_deserialize", "cg_plan_levels", "cg_decode_paged",
            "cg_encode_levels_ws_bytes", "cg_encode_levels", "cg_ablation_ws_bytes", "cg_ablation",
            "cg_cache_source", "cg_test_decode_timeout", "cg_pages_ws_bytes", "cg_pages_copy", "cg_pages_fork",
-           "cg_pages_free", "cg_pages_compact", "cg_attend_ws_bytes", "cg_attend")
+           "cg_pages_free", "cg_pages_compact", "cg_attend_ws_bytes", "cg_attend", "cg_quant_row", "cg_quant_write",
+           "cg_quant_read", "cg_quant_attend_ws_bytes", "cg_quant_attend")
 
 _lib = None
 
@@ -159,6 +170,12 @@ def lib() -> ct.CDLL:
         L.cg_pages_compact.argtypes = [PG, P, P, ct.c_size_t, P, P]
         L.cg_attend_ws_bytes.argtypes = [PG, ct.POINTER(cg_attention), SZ]
         L.cg_attend.argtypes = [PG, ct.POINTER(cg_attention), P, ct.c_size_t, P, P]
+        QF, TR = ct.POINTER(cg_quant), ct.POINTER(cg_token_rows)
+        L.cg_quant_row.argtypes = [QF, ct.POINTER(U32)]
+        L.cg_quant_write.argtypes = [PG, QF, TR, P, P]
+        L.cg_quant_read.argtypes = [PG, QF, TR, P, P]
+        L.cg_quant_attend_ws_bytes.argtypes = [PG, QF, ct.POINTER(cg_attention), SZ]
+        L.cg_quant_attend.argtypes = [PG, QF, ct.POINTER(cg_attention), P, ct.c_size_t, P, P]
         L.cg_cache_source.argtypes = [P, ct.POINTER(ct.c_int), ct.POINTER(ct.c_void_p)]
         for name in EXPORTS:
             if name not in ("cg_status_string",):

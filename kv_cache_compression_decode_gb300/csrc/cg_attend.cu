@@ -12,156 +12,12 @@
 // Three kernels, each started while the one before it drains: k_shared (many
 // query rows on the shared part, tcgen05), k_rows (a few query rows on their
 // tokens, bound by memory), k_merge or k_merge_rows.
-#include <cuda.h>
-#include <math.h>
-
-#include "cg_async.cuh"
-#include "cg_launch.cuh"
+#include "cg_attend.cuh"
 
 namespace cg {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr uint32_t kRows = 16;  // query rows of a row tile
 constexpr uint32_t kTileRows = 64;  // K rows of a tile of k_rows: 64 / nh tokens of nh neighbouring heads
-
-struct Args {
-    const uint16_t *q;
-    uint16_t *out;
-    float *lse;
-    const uint32_t *slots, *tables, *lens;
-    uint32_t n_slots, n_blocks, n_pool, bshift;
-    uint32_t R, nq, g, Hkv;  // requests, query tokens, query heads per KV head, KV heads
-    uint32_t P, shared_slot; // shared tokens
-    uint32_t nh, ng;         // k_rows: heads that one block takes together (1, 2 or 4), groups of them
-    uint32_t tlog;           // log2 of the tokens of a tile, 64 / nh
-    uint32_t rt;             // items' row ranges of a request
-    uint32_t npt;            // row ranges of the whole batch over the shared tokens in k_rows (0: k_shared has them)
-    uint32_t pairs;          // k_shared: pairs of 128-row tiles of the whole batch (0: k_rows has the shared part)
-    uint32_t one;            // k_shared: the batch fits one 128-row tile
-    uint32_t n_tc;           // blocks of k_shared
-    uint32_t merge_rows;     // rows of a warp of the joins
-    uint32_t n_cta;          // blocks of k_rows
-    uint64_t qs[3], os[3];
-    float scale2;            // |scale| * log2 e
-    uint32_t flip;           // sign bits to flip in q (scale < 0)
-    uint32_t *status;
-    // workspace
-    uint64_t *cum;           // [R + 1] first tile of request r; [R]: tiles of all requests
-    uint32_t *tokens;        // [R] tokens of request r (tokens_of)
-    // rows of partial results: O [D] and (m, l).  First k_shared's, [piece][2][128];
-    // from row part0 on k_rows', [piece][4][piece_rows], a quarter per warp column
-    float *part_o;
-    float2 *part_ml;
-    uint32_t part0;
-    uint32_t piece_rows, range_rows; // rows of a piece that are stored; rows of an item's range
-};
-
-// Tokens of request r's sequence; 0 for an empty slot and for a request that
-// is refused (*bad).
-__device__ __forceinline__ uint32_t tokens_of(const Args &a, uint32_t r, bool *bad) {
-    const uint32_t s = a.slots ? a.slots[r] : r;
-    if (s >= a.n_slots) {
-        *bad = true;
-        return 0;
-    }
-    const uint32_t n = a.lens[s];
-    // the first query token, which sees n - nq + 1 tokens, has to see all the shared ones
-    if (n != 0 && (n > ((uint64_t)a.n_blocks << a.bshift) || (a.P && (uint64_t)n + 1 < (uint64_t)a.P + a.nq))) {
-        *bad = true;
-        return 0;
-    }
-    return n;
-}
-
-__device__ __forceinline__ uint32_t tiles_of(const Args &a, uint32_t tokens) {
-    return (tokens + (1u << a.tlog) - 1u) >> a.tlog;
-}
-// Blocks that a list of `total` tiles is dealt to: two tiles each at least.
-__device__ __forceinline__ uint64_t shares(const Args &a, uint64_t total) {
-    return min((uint64_t)a.n_cta, (total + 1) / 2);
-}
-
-// Work list: for each request its row ranges x head groups ("items"), each as
-// long as the request's own tokens, then the items of the shared part.  Block
-// c of n takes tiles [c T / n, (c + 1) T / n) of the whole list, so every
-// block has the same share whatever the lengths are (n <= T: no block between
-// two others is left without a tile).  A block's run of tiles of one item is a
-// piece; its slot c + item is unique, since along the list each new piece has
-// a larger block or a larger item.
-struct Piece {
-    uint32_t r;        // request; R: the shared part
-    uint32_t item;     // number of the item
-    uint32_t range, group;
-    uint32_t tile0, n; // tiles of the item
-    uint32_t of;       // tiles the item has
-    uint32_t len;      // tokens in the sequence (request) or P
-};
-
-struct Walk {
-    uint64_t t, end, base;  // position, end of this block's share, first tile of request r
-    uint32_t r;
-    const uint32_t *lens;   // tokens of the requests in shared memory, or null
-};
-
-// floor(x / y): the numbers are small most of the time, and 64-bit division is long.
-__device__ __forceinline__ uint64_t quot(uint64_t x, uint64_t y) {
-    return (x | y) >> 32 ? x / y : (uint32_t)x / (uint32_t)y;
-}
-
-__device__ __forceinline__ bool next_piece(const Args &a, Walk &w, Piece &p) {
-    if (w.t >= w.end) return false;
-    bool bad = false;
-    uint32_t nt = 0, len = 0;
-    while (w.r < a.R) {
-        len = w.lens ? w.lens[w.r] : tokens_of(a, w.r, &bad);
-        nt = len > a.P ? tiles_of(a, len - a.P) : 0;
-        const uint64_t all = (uint64_t)nt * a.rt * a.ng;
-        if (w.t < w.base + all) break;
-        w.base += all;
-        w.r++;
-    }
-    p.r = w.r;
-    if (w.r == a.R) {
-        len = a.P;
-        nt = tiles_of(a, a.P);
-    }
-    if (nt == 0) return false;  // this and the next: lengths that changed under the call leave tiles over
-    const uint64_t at = w.t - w.base;
-    const uint32_t local = (uint32_t)quot(at, nt);
-    if (w.r == a.R && local >= a.npt * a.ng) return false;
-    p.item = w.r * a.rt * a.ng + local;
-    p.range = local / a.ng;
-    p.group = local - p.range * a.ng;
-    p.tile0 = (uint32_t)(at - (uint64_t)local * nt);
-    p.n = (uint32_t)min((uint64_t)(nt - p.tile0), w.end - w.t);
-    p.of = nt;
-    p.len = len;
-    w.t += p.n;
-    return true;
-}
-
-// Query row x of an item (of the request, or of the batch in the shared
-// part): request, query token, query head.
-struct Row {
-    uint32_t r, i, h;
-    bool valid;
-};
-__device__ __forceinline__ Row row_of(const Args &a, const Piece &p, uint32_t x, uint32_t head) {
-    Row o;
-    const uint32_t per = a.nq * a.g;
-    if (p.r == a.R) {
-        o.r = x / per;
-        x -= o.r * per;
-        o.valid = o.r < a.R;
-    } else {
-        o.r = p.r;
-        o.valid = x < per;
-    }
-    o.i = x / a.g;
-    o.h = head * a.g + (x - o.i * a.g);
-    return o;
-}
 
 // kR row tiles of 16 query rows a block.
 template <uint32_t D, uint32_t kR> struct Smem {
@@ -209,54 +65,8 @@ __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __
         }
         fence_bar_init();
     }
-    // This block's share of the work list: every thread sums its own run of requests.
-    const uint32_t per = (a.R + S::kThreads - 1) / S::kThreads;
-    const uint32_t r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
     uint32_t *lens = reinterpret_cast<uint32_t *>(smem + S::oLens);
-    const bool keep = a.R <= S::kLens;
-    uint64_t mine = 0;
-    bool bad = false;
-    for (uint32_t r = r0; r < r1; r++) {
-        const uint32_t n = tokens_of(a, r, &bad);
-        if (keep) lens[r] = n;
-        if (blockIdx.x == 0) a.tokens[r] = n;
-        mine += (uint64_t)(n > a.P ? tiles_of(a, n - a.P) : 0) * a.rt * a.ng;
-    }
-    if (bad && blockIdx.x == 0) flag(a.status, CG_ERR_RANGE);
-    uint64_t inc = mine;
-    for (uint32_t d = 1; d < 32; d <<= 1) {
-        const uint64_t y = __shfl_up_sync(kFull, inc, d);
-        if (lane >= d) inc += y;
-    }
-    if (lane == 31) misc[warp] = inc;
-    __syncthreads();
-    uint64_t before = inc - mine, own = 0;
-    for (uint32_t k = 0; k <= kWarps; k++) {
-        if (k < warp) before += misc[k];
-        own += misc[k];
-    }
-    const uint64_t total = own + (uint64_t)a.npt * a.ng * tiles_of(a, a.P);
-    if (blockIdx.x == 0) {
-        uint64_t at = before;
-        for (uint32_t r = r0; r < r1; r++) {
-            a.cum[r] = at;
-            const uint32_t n = a.tokens[r];  // this thread's own write
-            at += (uint64_t)(n > a.P ? tiles_of(a, n - a.P) : 0) * a.rt * a.ng;
-        }
-        if (tid == 0) a.cum[a.R] = own;
-    }
-    const uint64_t n_cta = shares(a, total);
-    Walk w;
-    w.t = blockIdx.x < n_cta ? quot(blockIdx.x * total, n_cta) : total;
-    w.end = blockIdx.x < n_cta ? quot((blockIdx.x + 1ull) * total, n_cta) : total;
-    if (mine && w.t >= before && w.t < before + mine) {  // one thread at most
-        misc[kWarps + 1] = before;
-        misc[kWarps + 2] = r0;
-    }
-    __syncthreads();
-    w.base = w.t < own ? misc[kWarps + 1] : own;
-    w.r = w.t < own ? (uint32_t)misc[kWarps + 2] : a.R;
-    w.lens = keep ? lens : nullptr;
+    Walk w = take_share<S::kThreads>(a, misc, lens, S::kLens);
 
     const uint32_t tt = 1u << a.tlog;                 // tokens of a tile
     const uint32_t head_bytes = tt * D * 2, half_bytes = tt * 128;
@@ -530,7 +340,6 @@ __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __
 // GFLOP) take 309 us, 1770 TFLOP/s; with 512 rows on 16384 tokens (34 GFLOP,
 // 134 MB) 34 us, of which K and V from DRAM are 20.
 // ---------------------------------------------------------------------------
-constexpr uint32_t kTcTok = 128, kTcSlots = 5;
 // Three warpgroups: two of softmax, one whose first warps fetch tiles and
 // issue MMAs.  The launch gives 168 registers a thread; the last group keeps
 // 72, so that a softmax thread can hold its row of scores: 2 x 216 + 72 = 3 x 168.
@@ -633,7 +442,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 8) {  // fetch: tiles in the order in which the MMA warp uses them
             const uint32_t rows_log = min(a.bshift, 6u), rows = 1u << rows_log, boxes = kTcTok >> rows_log;
-            const uint32_t *row = a.tables + (uint64_t)a.shared_slot * a.n_blocks;
+            const uint32_t *row = a.tables ? a.tables + (uint64_t)a.shared_slot * a.n_blocks : nullptr;
             uint32_t cnt = 0;
             auto fetch = [&](uint32_t tile, uint32_t kv, uint32_t head) {
                 if (!ok) return;
@@ -641,7 +450,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
                 const uint32_t pos = tile * kTcTok + lane * rows;
                 uint32_t id = a.n_pool;  // outside the map: reads zeros
                 if (lane < boxes && pos < a.P) {
-                    id = row[pos >> a.bshift];
+                    id = row ? row[pos >> a.bshift] : pos >> a.bshift;
                     if (id >= a.n_pool) {
                         id = a.n_pool;
                         flag(a.status, CG_ERR_RANGE);
@@ -661,10 +470,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
             };
             while (walk.next(a, p)) {
                 const uint32_t ahead = a.one ? 2 : 1;  // score tiles fetched before the first V
-                for (uint32_t k = 0; k < ahead && k < p.n; k++) fetch(p.tile0 + k, 0, p.head);
+                auto fetch_k = [&](uint32_t tile) {
+                    fetch(tile, 0, p.head);
+                    if (a.split) fetch(tile, 2, p.head);
+                };
+                for (uint32_t k = 0; k < ahead && k < p.n; k++) fetch_k(p.tile0 + k);
                 for (uint32_t k = 0; k < p.n; k++) {
                     fetch(p.tile0 + k, 1, p.head);
-                    if (k + ahead < p.n) fetch(p.tile0 + k + ahead, 0, p.head);
+                    if (k + ahead < p.n) fetch_k(p.tile0 + k + ahead);
                 }
             }
             if (!ok) {
@@ -679,14 +492,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
                 if (ok) ok = __all_sync(kFull, bar_wait(full + 8 * (c % kTcSlots), (c / kTcSlots) & 1u));
                 tc_fence_after();
             };
+            // scores of stream s from the K in slot c (with split, and in the next)
             auto qk = [&](uint32_t s, uint32_t c) {
                 if (!ok) return;
-                const uint32_t q = mma_desc(sm + M::oQ + (a.one ? 0 : s) * M::kTile, true, 0),
-                               k = mma_desc(sm + (c % kTcSlots) * M::kTile, true, 0);
+                const uint32_t q = mma_desc(sm + M::oQ + (a.one ? 0 : s) * M::kTile, true, 0);
+                for (uint32_t y = 0; y <= a.split; y++) {
+                    const uint32_t k = mma_desc(sm + ((c + y) % kTcSlots) * M::kTile, true, 0);
     #pragma unroll
-                for (uint32_t x = 0; x < D / 16; x++) {
-                    const uint32_t o = ((x >> 2) * M::kHalf + (x & 3u) * 32) >> 4;
-                    tc_mma_ss(tm + Tmem<D>::S(s), q + o, k + o, kQk, x != 0);
+                    for (uint32_t x = 0; x < D / 16; x++) {
+                        const uint32_t o = ((x >> 2) * M::kHalf + (x & 3u) * 32) >> 4;
+                        tc_mma_ss(tm + Tmem<D>::S(s), q + o, k + o, kQk, x != 0 || y);
+                    }
                 }
                 tc_commit(s_rdy + 8 * s);
             };
@@ -712,11 +528,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
             while (walk.next(a, p)) {
                 if (ok) ok = __all_sync(kFull, bar_wait(q_rdy, piece++ & 1u));
                 tc_fence_after();
+                // K's slots: cnt, and with split cnt + 1
+                auto k_ready = [&]() {
+                    slot_ready(cnt);
+                    if (a.split) slot_ready(cnt + 1);
+                };
+                auto free_k = [&]() {
+                    free_slot(cnt++);
+                    if (a.split) free_slot(cnt++);
+                };
                 if (a.one) {  // even token tiles: stream 0, odd ones: stream 1
                     for (uint32_t k = 0; k < 2 && k < p.n; k++) {
-                        slot_ready(cnt);
+                        k_ready();
                         qk(k, cnt);
-                        free_slot(cnt++);
+                        free_k();
                     }
                     for (uint32_t k = 0; k < p.n; k++) {
                         const uint32_t s = k & 1u;
@@ -724,30 +549,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
                         pv(s, cnt, k < 2);
                         free_slot(cnt++);
                         if (k + 2 < p.n) {
-                            slot_ready(cnt);
+                            k_ready();
                             qk(s, cnt);
-                            free_slot(cnt++);
+                            free_k();
                         } else {
                             done(s);
                         }
                     }
                 } else {
-                    slot_ready(cnt);
+                    k_ready();
                     qk(0, cnt);
                     qk(1, cnt);
-                    free_slot(cnt++);
+                    free_k();
                     for (uint32_t k = 0; k < p.n; k++) {
                         const uint32_t v = cnt++;
                         const bool more = k + 1 < p.n;
                         slot_ready(v);
-                        if (more) slot_ready(cnt);
+                        if (more) k_ready();
                         for (uint32_t s = 0; s < 2; s++) {
                             pv(s, v, k == 0);
                             if (s) free_slot(v);
                             if (more) qk(s, cnt);
                             else done(s);
                         }
-                        if (more) free_slot(cnt++);
+                        if (more) free_k();
                     }
                 }
             }
@@ -920,9 +745,9 @@ struct Runs {
 // The rows x0.. of request r and KV head `head`, at most up to x_end.
 __device__ __forceinline__ Runs runs_of(const Args &a, uint32_t r, uint32_t head, uint32_t x0, uint32_t x_end, uint32_t len,
                                         uint64_t own, uint64_t first) {
-    const uint32_t hlog = a.nh >> 1, plog = 2u - hlog;  // log2 of nh, and of the parts of a row, 4 / nh
-    const uint32_t group = head >> hlog, hd = head & (a.nh - 1u);
-    const uint32_t rlog = a.range_rows == kRows ? 4u : 5u, rmask = a.range_rows - 1u;
+    const uint32_t plog = a.clog - a.hlog;  // log2 of the parts of a row
+    const uint32_t group = head >> a.hlog, hd = head & (a.nh - 1u);
+    const uint32_t rlog = a.rlog, rmask = (1u << rlog) - 1u;
     const uint32_t nt_sh = a.npt ? tiles_of(a, a.P) : 0, nt_own = len > a.P ? tiles_of(a, len - a.P) : 0;
     const uint64_t total = own + (uint64_t)a.npt * a.ng * nt_sh, n_cta = shares(a, total);
     // tiles [t0, t0 + nt) of an item are spread over blocks c0..c1
@@ -934,7 +759,7 @@ __device__ __forceinline__ Runs runs_of(const Args &a, uint32_t r, uint32_t head
     uint32_t x1 = min(x_end, (x0 | rmask) + 1), c0;
     Runs o{};
     if (a.pairs) x1 = min(x1, x0 + 256u - (xp & 255u));
-    if (a.npt) x1 = min(x1, x0 + a.range_rows - (xp & rmask));
+    if (a.npt) x1 = min(x1, x0 + (rmask + 1u) - (xp & rmask));
     o.rows = x1 - x0;
     if (len && a.pairs) {
         const uint32_t of = (a.P + kTcTok - 1) / kTcTok, item = head * a.pairs + (xp >> 8);
@@ -945,12 +770,12 @@ __device__ __forceinline__ Runs runs_of(const Args &a, uint32_t r, uint32_t head
     if (len && a.npt) {
         const uint32_t item = (xp >> rlog) * a.ng + group;
         o.n_sh = run(own + (uint64_t)item * nt_sh, nt_sh, n_cta, total, c0) << plog;
-        o.sh = a.part0 + ((c0 + a.R * a.rt * a.ng + item) * 4 + hd) * a.piece_rows + (xp & rmask);
+        o.sh = a.part0 + (((c0 + a.R * a.rt * a.ng + item) << a.clog) + hd) * a.piece_rows + (xp & rmask);
     }
     if (nt_own) {
         const uint32_t item = (x0 >> rlog) * a.ng + group;
         o.n_own = run(first + (uint64_t)item * nt_own, nt_own, n_cta, total, c0) << plog;
-        o.own = a.part0 + ((c0 + r * a.rt * a.ng + item) * 4 + hd) * a.piece_rows + (x0 & rmask);
+        o.own = a.part0 + (((c0 + r * a.rt * a.ng + item) << a.clog) + hd) * a.piece_rows + (x0 & rmask);
     }
     o.n = o.n_tc + o.n_sh + o.n_own;
     return o;
@@ -959,10 +784,10 @@ __device__ __forceinline__ Runs runs_of(const Args &a, uint32_t r, uint32_t head
 // Row of piece e of the first row of `o`.
 __device__ __forceinline__ uint32_t place(const Args &a, const Runs &o, uint32_t e) {
     if (e < o.n_tc) return o.tc + (e >> a.one) * 256u + (e & a.one) * 128u;
-    const uint32_t hlog = a.nh >> 1, plog = 2u - hlog;
+    const uint32_t plog = a.clog - a.hlog;
     const bool sh = e - o.n_tc < o.n_sh;
     const uint32_t f = sh ? e - o.n_tc : e - o.n_tc - o.n_sh;
-    return (sh ? o.sh : o.own) + ((f >> plog) * 4u + ((f & ((1u << plog) - 1u)) << hlog)) * a.piece_rows;
+    return (sh ? o.sh : o.own) + (((f >> plog) << a.clog) + ((f & ((1u << plog) - 1u)) << a.hlog)) * a.piece_rows;
 }
 
 __device__ __forceinline__ uint16_t *out_row(const Args &a, uint32_t r, uint32_t head, uint32_t i, uint32_t j) {
@@ -1188,32 +1013,9 @@ struct Plan {
 // on the requests' own tokens (24 requests of one row, 32 heads: 131 us;
 // k_rows 150).  More than 32 rows: k_shared.
 bool by_tensor(uint64_t rows, uint64_t requests) { return rows > 32 || (rows > kRows && requests > 4); }
-constexpr uint32_t kMaxCtas = 304, kMaxTcCtas = 152;  // bounds of the grids that the workspace is sized for: 152 SMs
 
 bool make_plan(const cg_pages *p, const cg_attention *a, Plan *o) {
-    if (!p || !a || !p->pool || !p->tables || !p->lens || !a->q || !a->out) return false;
-    if (!p->L || !p->C || !p->n_pool_blocks || p->n_pool_blocks > (1u << 31) - 1u || !p->n_slots || !p->n_blocks)
-        return false;
-    const uint32_t bt = p->block_tokens;
-    if (bt < 8 || (bt & (bt - 1u)) || (uint64_t)p->n_blocks * bt > (1ull << 31) - 64u || p->token_stride < p->C)
-        return false;
-    if (a->dtype > CG_BF16 || !a->n_requests || !a->n_queries || !a->n_q_heads || !a->n_kv_heads) return false;
-    if (a->head_dim != 64 && a->head_dim != 128) return false;
-    if ((uint64_t)a->n_kv_heads * a->head_dim != p->C || a->n_q_heads % a->n_kv_heads) return false;
-    if (a->layer >= p->L || a->shared_blocks > p->n_blocks) return false;
-    if (a->shared_blocks && a->shared_slot >= p->n_slots) return false;
-    if (!isfinite(a->scale)) return false;
-    // the stride of a dimension with one element is never used
-    const auto used = [](uint64_t n, uint64_t stride) { return n > 1 ? stride : 0; };
-    const uint64_t block = used(p->n_pool_blocks, p->block_stride), layer = used(p->L, p->layer_stride);
-    const uint64_t counts[3] = {a->n_requests, a->n_queries, a->n_q_heads};
-    uint64_t strides = layer | p->kv_stride | block | p->token_stride;
-    for (int k = 0; k < 3; k++) strides |= used(counts[k], a->q_stride[k]) | used(counts[k], a->out_stride[k]);
-    if (strides % 8 || misaligned(p->pool, 16) || misaligned(a->q, 16) || misaligned(a->out, 16)) return false;
-    if (misaligned(p->tables, 4) || misaligned(p->lens, 4) || misaligned(a->lse, 4) || misaligned(a->slots, 4))
-        return false;
-    // a tensor map's strides have 40 bits, and its rows and blocks may not be empty strides
-    if ((p->kv_stride | block | p->token_stride) >> 39 || !p->kv_stride || (p->n_pool_blocks > 1 && !block)) return false;
+    if (!attention_ok(p, a) || (uint64_t)a->n_kv_heads * a->head_dim != p->C) return false;
     o->g = a->n_q_heads / a->n_kv_heads;
     constexpr uint64_t kMost = 1ull << 31;  // query rows; compared before each product, so that none wraps
     const uint64_t per = (uint64_t)a->n_queries * o->g;
@@ -1258,20 +1060,6 @@ EncodeTiled encoder() {
     return fn;
 }
 
-// The layer's K and V as (channel, row, block, K/V), in boxes of 64 channels x `rows` rows.
-bool make_map(const cg_pages *p, const cg_attention *a, uint32_t rows, CUtensorMap *map) {
-    const EncodeTiled enc = encoder();
-    if (!enc) return false;
-    const cuuint64_t dims[4] = {p->C, p->block_tokens, p->n_pool_blocks, 2};
-    const cuuint64_t block = p->n_pool_blocks > 1 ? p->block_stride : p->token_stride;  // unused with one block, but checked
-    const cuuint64_t strides[3] = {2 * p->token_stride, 2 * block, 2 * p->kv_stride};
-    const cuuint32_t box[4] = {64, rows, 1, 1}, step[4] = {1, 1, 1, 1};
-    return enc(map, a->dtype == CG_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-               p->pool + a->layer * p->layer_stride, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <class T, uint32_t D, uint32_t kR>
 cudaError_t launch_rows(const CUtensorMap &map, Args &a, int sms, cudaStream_t s) {
     using S = Smem<D, kR>;
@@ -1283,25 +1071,23 @@ cudaError_t launch_rows(const CUtensorMap &map, Args &a, int sms, cudaStream_t s
 }
 
 template <class T, uint32_t D>
-cudaError_t launch(const CUtensorMap &rows_map, const CUtensorMap &map, Args &a, int sms, cudaStream_t s) {
-    cudaError_t e;
-    if (a.pairs) {
-        e = cudaFuncSetAttribute(k_shared<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<D>::kBytes);
-        if (e != cudaSuccess) return e;
-        // An even deal of all tiles lets a block cross from one item to the
-        // next, which costs about kCross tiles (the streams drain, new
-        // queries come in); where whole blocks per item take no longer than that, deal so.
-        constexpr uint64_t kCross = 4;
-        // A block gets two token tiles a stream at least: a piece less to join saves more than a tile takes.
-        const uint64_t items = (uint64_t)a.pairs * a.Hkv, of = (a.P + kTcTok - 1) / kTcTok, least = a.one ? 4 : 2;
-        const uint64_t most = items * ((of + least - 1) / least), sm = (uint64_t)sms < kMaxTcCtas ? sms : kMaxTcCtas;
-        const uint64_t n = sm < most ? sm : most, k = n / items;
-        a.n_tc = (uint32_t)(k && (of + k - 1) / k <= items * of / n + kCross ? k * items : n);
-        e = launch_next(k_shared<T, D>, a.n_tc, kTcThreads, TcSmem<D>::kBytes, s, false, map, a);
-        if (e != cudaSuccess) return e;
-    }
-    e = a.range_rows == kRows ? launch_rows<T, D, 1>(rows_map, a, sms, s) : launch_rows<T, D, 2>(rows_map, a, sms, s);
+cudaError_t shared(const CUtensorMap &map, Args &a, int sms, cudaStream_t s) {
+    const cudaError_t e = cudaFuncSetAttribute(k_shared<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<D>::kBytes);
     if (e != cudaSuccess) return e;
+    // An even deal of all tiles lets a block cross from one item to the
+    // next, which costs about kCross tiles (the streams drain, new
+    // queries come in); where whole blocks per item take no longer than that, deal so.
+    constexpr uint64_t kCross = 4;
+    // A block gets two token tiles a stream at least: a piece less to join saves more than a tile takes.
+    const uint64_t items = (uint64_t)a.pairs * a.Hkv, of = (a.P + kTcTok - 1) / kTcTok, least = a.one ? 4 : 2;
+    const uint64_t most = items * ((of + least - 1) / least), sm = (uint64_t)sms < kMaxTcCtas ? sms : kMaxTcCtas;
+    const uint64_t n = sm < most ? sm : most, k = n / items;
+    a.n_tc = (uint32_t)(k && (of + k - 1) / k <= items * of / n + kCross ? k * items : n);
+    return launch_next(k_shared<T, D>, a.n_tc, kTcThreads, TcSmem<D>::kBytes, s, false, map, a);
+}
+
+template <class T, uint32_t D>
+cudaError_t joins(Args &a, int sms, cudaStream_t s) {
     // warps for the joins: as many as an SM holds (many rows: twice that), with a few rows each where there are rows enough
     const uint64_t per = (uint64_t)a.nq * a.g, rh = (uint64_t)a.R * a.Hkv;
     const bool wide = rh * per <= (uint64_t)sms * 4, many = rh * per >= (uint64_t)sms * 16;
@@ -1312,7 +1098,64 @@ cudaError_t launch(const CUtensorMap &rows_map, const CUtensorMap &map, Args &a,
     return launch_next(many ? k_merge_rows<T, D> : k_merge<T, D, false>, (unsigned)((warps + 7) / 8), 256, 0, s, true, a);
 }
 
+template <class T, uint32_t D>
+cudaError_t rows(const CUtensorMap &map, uint32_t range_rows, Args &a, int sms, cudaStream_t s) {
+    return range_rows == kRows ? launch_rows<T, D, 1>(map, a, sms, s) : launch_rows<T, D, 2>(map, a, sms, s);
+}
+
 }  // namespace
+
+bool attention_ok(const cg_pages *p, const cg_attention *a) {
+    if (!p || !a || !p->pool || !p->tables || !p->lens || !a->q || !a->out) return false;
+    if (!p->L || !p->C || !p->n_pool_blocks || p->n_pool_blocks > (1u << 31) - 1u || !p->n_slots || !p->n_blocks)
+        return false;
+    const uint32_t bt = p->block_tokens;
+    if (bt < 8 || (bt & (bt - 1u)) || (uint64_t)p->n_blocks * bt > (1ull << 31) - 64u || p->token_stride < p->C)
+        return false;
+    if (a->dtype > CG_BF16 || !a->n_requests || !a->n_queries || !a->n_q_heads || !a->n_kv_heads) return false;
+    if (a->head_dim != 64 && a->head_dim != 128) return false;
+    if (a->n_q_heads % a->n_kv_heads) return false;
+    if (a->layer >= p->L || a->shared_blocks > p->n_blocks) return false;
+    if (a->shared_blocks && a->shared_slot >= p->n_slots) return false;
+    if (!isfinite(a->scale)) return false;
+    // the stride of a dimension with one element is never used
+    const auto used = [](uint64_t n, uint64_t stride) { return n > 1 ? stride : 0; };
+    const uint64_t block = used(p->n_pool_blocks, p->block_stride), layer = used(p->L, p->layer_stride);
+    const uint64_t counts[3] = {a->n_requests, a->n_queries, a->n_q_heads};
+    uint64_t strides = layer | p->kv_stride | block | p->token_stride;
+    for (int k = 0; k < 3; k++) strides |= used(counts[k], a->q_stride[k]) | used(counts[k], a->out_stride[k]);
+    if (strides % 8 || misaligned(p->pool, 16) || misaligned(a->q, 16) || misaligned(a->out, 16)) return false;
+    if (misaligned(p->tables, 4) || misaligned(p->lens, 4) || misaligned(a->lse, 4) || misaligned(a->slots, 4))
+        return false;
+    // a tensor map's strides have 40 bits, and its rows and blocks may not be empty strides
+    if ((p->kv_stride | block | p->token_stride) >> 39 || !p->kv_stride || (p->n_pool_blocks > 1 && !block)) return false;
+    return true;
+}
+
+bool make_token_map(const cg_pages *p, const uint16_t *base, uint32_t channels, uint32_t copies, uint32_t box, uint32_t rows,
+                    CUtensorMapSwizzle swizzle, CUtensorMap *map) {
+    const EncodeTiled enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {channels, p->block_tokens, p->n_pool_blocks, copies};
+    const cuuint64_t block = p->n_pool_blocks > 1 ? p->block_stride : p->token_stride;  // unused with one block, but checked
+    const cuuint64_t strides[3] = {2 * p->token_stride, 2 * block, 2 * p->kv_stride};
+    const cuuint32_t boxes[4] = {box, rows, 1, 1}, step[4] = {1, 1, 1, 1};
+    // words: fp16 and bf16 are moved alike, and what lies outside the matrix is filled with zeros
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<uint16_t *>(base), dims, strides, boxes, step,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_shared(uint32_t dtype, uint32_t head_dim, const CUtensorMap &map, Args &a, int sms, cudaStream_t s) {
+    if (head_dim == 128) return dtype == CG_FP16 ? shared<__half, 128>(map, a, sms, s) : shared<__nv_bfloat16, 128>(map, a, sms, s);
+    return dtype == CG_FP16 ? shared<__half, 64>(map, a, sms, s) : shared<__nv_bfloat16, 64>(map, a, sms, s);
+}
+
+cudaError_t launch_joins(uint32_t dtype, uint32_t head_dim, Args &a, int sms, cudaStream_t s) {
+    if (head_dim == 128) return dtype == CG_FP16 ? joins<__half, 128>(a, sms, s) : joins<__nv_bfloat16, 128>(a, sms, s);
+    return dtype == CG_FP16 ? joins<__half, 64>(a, sms, s) : joins<__nv_bfloat16, 64>(a, sms, s);
+}
+
 }  // namespace cg
 
 using namespace cg;
@@ -1336,7 +1179,10 @@ extern "C" cg_status cg_attend(const cg_pages *p, const cg_attention *at, void *
     // boxes of k_rows are at most a tile high, those of k_shared 64 rows
     const uint32_t tt = kTileRows / pl.nh, bt = p->block_tokens;
     CUtensorMap map, rows_map;
-    if (!make_map(p, at, bt < tt ? bt : tt, &rows_map) || !make_map(p, at, bt < 64 ? bt : 64, &map)) return CG_ERR_CUDA;
+    const uint16_t *layer = p->pool + at->layer * p->layer_stride;
+    if (!make_token_map(p, layer, p->C, 2, 64, bt < tt ? bt : tt, CU_TENSOR_MAP_SWIZZLE_128B, &rows_map) ||
+        !make_token_map(p, layer, p->C, 2, 64, bt < 64 ? bt : 64, CU_TENSOR_MAP_SWIZZLE_128B, &map))
+        return CG_ERR_CUDA;
     Args a{};
     a.q = at->q;
     a.out = at->out;
@@ -1356,8 +1202,10 @@ extern "C" cg_status cg_attend(const cg_pages *p, const cg_attention *at, void *
     a.shared_slot = at->shared_slot;
     a.nh = pl.nh;
     a.ng = pl.ng;
+    a.hlog = (uint32_t)__builtin_ctz(pl.nh);
+    a.clog = 2;
     a.tlog = (uint32_t)__builtin_ctz(tt);
-    a.range_rows = pl.range_rows;
+    a.rlog = (uint32_t)__builtin_ctz(pl.range_rows);
     a.rt = pl.rt;
     a.npt = pl.npt;
     for (int k = 0; k < 3; k++) {
@@ -1378,7 +1226,11 @@ extern "C" cg_status cg_attend(const cg_pages *p, const cg_attention *at, void *
     a.part0 = (uint32_t)pl.tc_rows;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool fp16 = at->dtype == CG_FP16;
-    if (at->head_dim == 128) CG_CUDA_TRY((fp16 ? launch<__half, 128>(rows_map, map, a, sms, s) : launch<__nv_bfloat16, 128>(rows_map, map, a, sms, s)));
-    else CG_CUDA_TRY((fp16 ? launch<__half, 64>(rows_map, map, a, sms, s) : launch<__nv_bfloat16, 64>(rows_map, map, a, sms, s)));
+    if (a.pairs) CG_CUDA_TRY(launch_shared(at->dtype, at->head_dim, map, a, sms, s));
+    if (at->head_dim == 128)
+        CG_CUDA_TRY((fp16 ? rows<__half, 128>(rows_map, pl.range_rows, a, sms, s) : rows<__nv_bfloat16, 128>(rows_map, pl.range_rows, a, sms, s)));
+    else
+        CG_CUDA_TRY((fp16 ? rows<__half, 64>(rows_map, pl.range_rows, a, sms, s) : rows<__nv_bfloat16, 64>(rows_map, pl.range_rows, a, sms, s)));
+    CG_CUDA_TRY(launch_joins(at->dtype, at->head_dim, a, sms, s));
     return CG_OK;
 }

@@ -1,0 +1,9 @@
+// cg_quant_rows_8_64_f.cu -- k_quant_rows for 8-bit codes, heads of 64 channels and fp16 (sm_103a).
+#define CG_QUANT_BITS 8
+#include "cg_quant_rows.cuh"
+
+namespace cg {
+
+CG_QUANT_ROWS(launch_quant_rows_8_64_f) { return launch_rows<__half, 8, 64>(group, n, codes, pairs, a, q, sms, s); }
+
+}  // namespace cg

@@ -1,11 +1,13 @@
-"""Sequences in a paged KV pool: page operations and attention.
+"""Sequences in a paged KV pool of 16, 8 or 4 bits: page operations and attention.
 
 `PagedCache` holds the tensors that libcg's page calls (cg_pages_*) and
 cg_attend work on and marshals their arguments; every step runs in libcg's
 CUDA kernels.  A context is decoded into a slot's blocks (`decode`, over
 cg_decode_paged), continued by other slots that share its full blocks
 (`fork`), attended to by a batch of them (`attend`), and given back (`free`,
-`compact`).
+`compact`).  `QuantCache` is a cache whose pool is held in 4 or 8 bits: tokens
+are quantised as they are stored (`write`, cg_quant_write), read back (`read`)
+and attended to as they lie.
 
 All calls are asynchronous on `stream` (default: the current one), and errors
 found on the device are OR-ed into `status` as in codec.py.  A cache has one
@@ -23,12 +25,12 @@ from __future__ import annotations
 import ctypes as ct
 import math
 import operator
-from typing import Optional
+from typing import Optional, Tuple
 
 import torch
 
 from . import codec
-from .codec import CG_BF16, CG_FP16, Config, _check, cg_attention, cg_pages, lib
+from .codec import CG_BF16, CG_FP16, Config, _check, cg_attention, cg_pages, cg_quant, cg_token_rows, lib
 
 NO_BLOCK = NO_SLOT = -1  # CG_NO_BLOCK / CG_NO_SLOT as int32
 
@@ -36,7 +38,7 @@ _DTYPES = {torch.float16: CG_FP16, torch.bfloat16: CG_BF16}
 
 
 _INT32 = (torch.int32, torch.uint32)
-_Strides = ct.c_uint64 * 3
+_Strides, _Two = ct.c_uint64 * 3, ct.c_uint64 * 2
 # The current stream's handle without building a Stream object around it (3 us of a 7 us call).
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
@@ -69,13 +71,14 @@ class PagedCache:
     int32 [n_slots], refs int32 [n_pool].  The calls read and write the tensors
     given here: change them in place."""
 
+    _POOL = _DTYPES  # types of the pool's elements
     pool, tables, lens, refs, status = map(_fixed, ("pool", "tables", "lens", "refs", "status"))
 
     def __init__(self, pool: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
                  status: Optional[torch.Tensor] = None):
-        if pool.dtype not in _DTYPES or pool.dim() != 5 or pool.shape[2] != 2 or pool.stride(4) != 1:
-            raise ValueError("pool: a fp16 or bf16 tensor [L][n_pool][2][block_tokens][C] with contiguous channels "
-                             "is wanted")
+        if pool.dtype not in self._POOL or pool.dim() != 5 or pool.shape[2] != 2 or pool.stride(4) != 1:
+            raise ValueError(f"pool: a tensor [L][n_pool][2][block_tokens][C] of {' or '.join(map(str, self._POOL))} "
+                             "with contiguous channels is wanted")
         for t, dim, n in ((tables, 2, "tables"), (lens, 1, "lens"), (refs, 1, "refs")):
             if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous() or t.device != pool.device:
                 raise ValueError(f"{n}: a contiguous {dim}-D int32 tensor on {pool.device} is wanted")
@@ -95,7 +98,7 @@ class PagedCache:
         self._status_ptr = self.status.data_ptr()
         self._seen = set()  # streams that status and workspace are recorded on
         self._index = pool.device.index if pool.is_cuda else None
-        self._device, self._dtype = pool.device, _DTYPES[pool.dtype]
+        self._device, self._type, self._dtype = pool.device, pool.dtype, _DTYPES.get(pool.dtype)
         self._attn = {}  # workspace bytes of attend by shape
 
     @classmethod
@@ -190,7 +193,7 @@ class PagedCache:
         other = source if source is not None else self
         if src.shape[0] != dst.shape[0]:
             raise ValueError("copy: src and dst have the same number of blocks")
-        if other._pool.dtype != self._pool.dtype or other._device != d:
+        if other._form() != self._form() or other._device != d:
             raise ValueError("copy: both pools have one type and one device")
         _check(lib().cg_pages_copy(self._ref, other._ref, _ids(src, d, "src"), _ids(dst, d, "dst"),
                                    src.shape[0], self._status_ptr, self._stream(stream)), "cg_pages_copy")
@@ -222,9 +225,9 @@ class PagedCache:
         shared_blocks blocks of every sequence are those of shared_slot.
         scale defaults to head_dim ** -0.5.  Returns out (shape and type of
         q); lse, if given, is a fp32 [R][n_queries][n_q_heads]."""
-        d, pool, qs = self._device, self._pool, q.stride()
-        if q.dtype != pool.dtype or len(qs) != 4 or q.device != d or qs[3] != 1:
-            raise ValueError("q: a tensor [R][n_queries][n_q_heads][head_dim] of the pool's type and device with "
+        d, qs = self._device, q.stride()
+        if q.dtype != self._type or len(qs) != 4 or q.device != d or qs[3] != 1:
+            raise ValueError("q: a tensor [R][n_queries][n_q_heads][head_dim] of the cache's type and device with "
                              "contiguous head channels is wanted")
         R, nq, hq, hd = q.shape
         if out is None:
@@ -245,16 +248,182 @@ class PagedCache:
             return out
         a = cg_attention(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
                          _ids(slots, d, "slots") if slots is not None else None, self._dtype, R, nq, hq,
-                         pool.shape[4] // hd if hd else 0, hd, layer, shared_slot, shared_blocks, _Strides(*qs[:3]),
+                         self._kv_heads(hd), hd, layer, shared_slot, shared_blocks, _Strides(*qs[:3]),
                          _Strides(*os_[:3]), scale if scale is not None else 1.0 / math.sqrt(hd) if hd else 0.0)
-        key = (R, nq, hq, hd, shared_blocks > 0)
+        key = (R, nq, hq, hd, self._shared_key(shared_blocks))
         ws_bytes = self._attn.get(key)
         if ws_bytes is None:
             n = ct.c_size_t()
-            _check(lib().cg_attend_ws_bytes(self._ref, ct.byref(a), ct.byref(n)), "cg_attend_ws_bytes")
+            _check(self._attend_ws_bytes(a, n), "attend (workspace)")
             ws_bytes = self._attn[key] = n.value
         handle = self._stream(stream)
         ws = self._workspace(ws_bytes, stream, handle)
-        _check(lib().cg_attend(self._ref, ct.byref(a), ws.data_ptr(), ws.numel(), self._status_ptr, handle),
-               "cg_attend")
+        _check(self._attend(a, ws, handle), "attend")
         return out
+
+    # what a pool of another format does otherwise
+
+    def _form(self) -> tuple:
+        return (self._type,)
+
+    def _kv_heads(self, head_dim: int) -> int:
+        return self._pool.shape[4] // head_dim if head_dim else 0
+
+    def _shared_key(self, shared_blocks: int):
+        return shared_blocks > 0  # the workspace does not depend on how many
+
+    def _attend_ws_bytes(self, a, n) -> int:
+        return lib().cg_attend_ws_bytes(self._ref, ct.byref(a), ct.byref(n))
+
+    def _attend(self, a, ws, handle) -> int:
+        return lib().cg_attend(self._ref, ct.byref(a), ws.data_ptr(), ws.numel(), self._status_ptr, handle)
+
+
+class QuantCache(PagedCache):
+    """A cache whose pool holds K and V in 4 or 8 bits: an int16 tensor
+    [L][n_pool][2][block_tokens][row], each row the codes of a token's channels
+    and a scale and a low value of `dtype` for each `group` of them (cg_quant in
+    cg.h; `row_width` gives the row's length).  Tables, lengths, references and
+    the page calls are those of PagedCache; `dtype` (fp16 or bf16) is the type of
+    what is written, read and attended with.  group defaults to head_dim."""
+
+    _POOL = (torch.int16,)
+
+    def __init__(self, pool: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
+                 status: Optional[torch.Tensor] = None, *, n_kv_heads: int, head_dim: int, bits: int = 4,
+                 group: Optional[int] = None, dtype: torch.dtype = torch.float16):
+        row = self.row_width(n_kv_heads, head_dim, bits, group, dtype)
+        if pool.dim() == 5 and pool.shape[4] != row:
+            raise ValueError(f"pool: rows of {row} words hold {n_kv_heads} x {head_dim} channels in {bits} bits, "
+                             f"not {pool.shape[4]}")
+        super().__init__(pool, tables, lens, refs, status)
+        self._format = self._format_of(n_kv_heads, head_dim, bits, group, dtype)
+        self._fref = ct.byref(self._format)
+        self._type, self._dtype, self._heads, self._hd = dtype, _DTYPES[dtype], n_kv_heads, head_dim
+
+    @staticmethod
+    def _format_of(n_kv_heads, head_dim, bits, group, dtype) -> cg_quant:
+        if dtype not in _DTYPES:
+            raise ValueError("dtype: fp16 or bf16 is wanted")
+        return cg_quant(_DTYPES[dtype], bits, group if group is not None else head_dim, n_kv_heads, head_dim)
+
+    @classmethod
+    def row_width(cls, n_kv_heads: int, head_dim: int, bits: int = 4, group: Optional[int] = None,
+                  dtype: torch.dtype = torch.float16) -> int:
+        """Words of a row of the pool (cg_quant_row)."""
+        n = ct.c_uint32()
+        _check(lib().cg_quant_row(ct.byref(cls._format_of(n_kv_heads, head_dim, bits, group, dtype)), ct.byref(n)),
+               "cg_quant_row")
+        return n.value
+
+    @classmethod
+    def empty(cls, L: int, n_pool: int, block_tokens: int, n_kv_heads: int, head_dim: int, n_slots: int, n_blocks: int,
+              bits: int = 4, group: Optional[int] = None, dtype: torch.dtype = torch.float16,
+              device="cuda") -> "QuantCache":
+        """A cache of free blocks and empty slots."""
+        i32 = dict(dtype=torch.int32, device=device)
+        row = cls.row_width(n_kv_heads, head_dim, bits, group, dtype)
+        return cls(torch.zeros((L, n_pool, 2, block_tokens, row), dtype=torch.int16, device=device),
+                   torch.full((n_slots, n_blocks), NO_BLOCK, **i32), torch.zeros(n_slots, **i32),
+                   torch.zeros(n_pool, **i32), n_kv_heads=n_kv_heads, head_dim=head_dim, bits=bits, group=group,
+                   dtype=dtype)
+
+    @property
+    def channels(self) -> int:
+        return self._heads * self._hd
+
+    def _rows(self, k, v, layer, slots, offsets, start) -> cg_token_rows:
+        C, d = self._heads * self._hd, self._device
+        for t in (k, v):
+            if t.dtype != self._type or t.device != d or t.dim() != 3 or t.shape[2] != C or (C > 1 and t.stride(2) != 1):
+                raise ValueError(f"k and v: tensors [layers][rows][{C}] of {self._type} on {d} with contiguous channels "
+                                 "are wanted")
+        if v.shape != k.shape:
+            raise ValueError("k and v have one shape")
+        if layer < 0:
+            raise ValueError("layer is not negative")
+        n_layers, n_rows, _ = k.shape
+        if offsets is not None:
+            n = offsets.shape[0] - 1
+            if n < 0:
+                raise ValueError("offsets has an entry per sequence and one more")
+        else:
+            n = slots.shape[0] if slots is not None else start.shape[0] if start is not None else self._tables.shape[0]
+        if (slots is not None and slots.shape[0] != n) or (start is not None and start.shape[0] != n):
+            raise ValueError("slots and start have one entry per sequence, offsets one more")
+        if slots is None and n > self._tables.shape[0]:
+            raise ValueError("more sequences than slots")
+        ks, vs = k.stride(), v.stride()
+        return cg_token_rows(k.data_ptr(), v.data_ptr(), _ids(slots, d, "slots") if slots is not None else None,
+                             _ids(offsets, d, "offsets") if offsets is not None else None,
+                             _ids(start, d, "start") if start is not None else None, n, n_rows, layer, n_layers,
+                             _Two(ks[0], ks[1]), _Two(vs[0], vs[1]))
+
+    def write(self, k: torch.Tensor, v: torch.Tensor, layer: int = 0, slots: Optional[torch.Tensor] = None,
+              offsets: Optional[torch.Tensor] = None, start: Optional[torch.Tensor] = None, stream=None) -> None:
+        """Quantise the rows of k and v, [layers][rows][C], and store them in
+        the pool's layers from `layer` on (cg_quant_write).  The sequence in
+        slots[r] (default: slot r) has the rows offsets[r] .. offsets[r + 1] - 1
+        (default: an even share); they are its last tokens (advance `lens` first)
+        or those from start[r] on."""
+        rows = self._rows(k, v, layer, slots, offsets, start)
+        _check(lib().cg_quant_write(self._ref, self._fref, ct.byref(rows), self._status_ptr, self._stream(stream)),
+               "cg_quant_write")
+
+    def read(self, layer: int = 0, n_layers: Optional[int] = None, rows: Optional[int] = None,
+             slots: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None,
+             start: Optional[torch.Tensor] = None, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+             stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """The values of tokens as k and v, [layers][rows][C], the reverse of
+        `write` (cg_quant_read).  Without out, n_layers (default: 1) and `rows`
+        give the shape, and rows that belong to no token are zeros."""
+        if out is None:
+            if rows is None or rows < 0:
+                raise ValueError("read: rows or out is wanted")
+            shape = (n_layers if n_layers is not None else 1, rows, self._heads * self._hd)
+            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self._device)):
+                out = tuple(torch.zeros(shape, dtype=self._type, device=self._device) for _ in range(2))
+        k, v = out
+        if (n_layers is not None and k.shape[0] != n_layers) or (rows is not None and k.shape[1] != rows):
+            raise ValueError("read: n_layers and rows are those of out")
+        r = self._rows(k, v, layer, slots, offsets, start)
+        _check(lib().cg_quant_read(self._ref, self._fref, ct.byref(r), self._status_ptr, self._stream(stream)),
+               "cg_quant_read")
+        return k, v
+
+    def decode(self, cfg: Config, enc, slot: int, stream=None) -> None:
+        """Decode a context and quantise it into the blocks that a slot holds,
+        and set its length.  The slot needs blocks for all cfg.T tokens (fork
+        with parent -1 and reserve T).  The decoded context, fp16, is held until
+        the stream has written it."""
+        self._stream(stream)
+        if self._type != torch.float16:
+            raise ValueError("decode writes fp16: the cache is another type")
+        L, C = self._pool.shape[0], self._heads * self._hd
+        if (cfg.L, cfg.C) != (L, C):
+            raise ValueError(f"the context has {cfg.L} layers x {cfg.C} channels, the pool {L} x {C}")
+        if not 0 <= slot < self._tables.shape[0] or cfg.T > self._tables.shape[1] * self.block_tokens:
+            raise ValueError("decode: no such slot, or its row is shorter than the context")
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self._device)):
+            i32 = dict(dtype=torch.int32, device=self._device)
+            kv = torch.empty((L, 2, cfg.T, C), dtype=torch.float16, device=self._device)
+            codec.cg_decode(cfg, enc, kv, self.status, stream)
+            self.lens[slot] = cfg.T
+            self.write(kv[:, 0], kv[:, 1], slots=torch.full((1,), slot, **i32), stream=stream)
+
+    def _kv_heads(self, head_dim: int) -> int:
+        return self._heads
+
+    def _form(self) -> tuple:
+        f = self._format
+        return (self._type, f.bits, f.group, f.n_kv_heads, f.head_dim)
+
+    def _shared_key(self, shared_blocks: int):
+        return shared_blocks
+
+    def _attend_ws_bytes(self, a, n) -> int:
+        return lib().cg_quant_attend_ws_bytes(self._ref, self._fref, ct.byref(a), ct.byref(n))
+
+    def _attend(self, a, ws, handle) -> int:
+        return lib().cg_quant_attend(self._ref, self._fref, ct.byref(a), ws.data_ptr(), ws.numel(), self._status_ptr,
+                                     handle)
