@@ -88,23 +88,19 @@ extern "C" cg_status cg_quant_attend(const cg_pages *p, const cg_quant *f, const
     const uint32_t head_bytes = f->head_dim * f->bits / 8, n_groups = f->head_dim / f->group;
 
     QuantArgs q{};
-    const uint32_t across = pl.nh * head_bytes, width = across < 128 ? across : 128;  // 32, 64 or 128 bytes: a swizzle each
-    q.wlog = (uint32_t)__builtin_ctz(width);
-    q.cols = across / width;
+    q.cols = (pl.nh * head_bytes + 127) / 128;
     q.pw = pl.nh * n_groups * 4 < 16 ? 16 : pl.nh * n_groups * 4;
-    q.tile = pl.tt * across;
+    q.tile = pl.tt * q.cols * 128;
     q.ptile = pl.tt * q.pw;
     q.stage = (uint32_t)round_up(2 * (q.tile + q.ptile), 1024);
     const uint32_t room = kStageBytes / q.stage;
     q.n_stages = room < kQuantMaxStages ? room : kQuantMaxStages;
-    q.scale2 = at->scale * 1.4426950408889634f;
+    q.scale2 = fmaxf(fabsf(at->scale) * 1.4426950408889634f, 1e-35f);  // not 0: masked scores are -inf before the product
 
     const uint16_t *layer = p->pool + at->layer * p->layer_stride;
     const uint32_t box = bt < pl.tt ? bt : pl.tt, codes = quant_codes(f);
     CUtensorMap code_map, pair_map, map;
-    const CUtensorMapSwizzle swizzle = width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
-                                       : width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
-    if (!make_token_map(p, layer, codes, 2, width / 2, box, swizzle, &code_map) ||
+    if (!make_token_map(p, layer, codes, 2, 64, box, CU_TENSOR_MAP_SWIZZLE_128B, &code_map) ||
         !make_token_map(p, layer + codes, p->C - codes, 2, q.pw / 2, box, CU_TENSOR_MAP_SWIZZLE_NONE, &pair_map))
         return CG_ERR_CUDA;
 
@@ -139,7 +135,7 @@ extern "C" cg_status cg_quant_attend(const cg_pages *p, const cg_quant *f, const
         a.qs[k] = at->q_stride[k];
         a.os[k] = at->out_stride[k];
     }
-    a.scale2 = fmaxf(fabsf(q.scale2), 1e-35f);  // k_shared's, see cg_attend
+    a.scale2 = q.scale2;
     a.flip = at->scale < 0.f ? 0x80008000u : 0u;
     a.status = dev_status;
     uint8_t *w = static_cast<uint8_t *>(ws);

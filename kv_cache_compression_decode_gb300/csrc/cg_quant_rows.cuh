@@ -25,11 +25,10 @@
 namespace cg {
 
 struct QuantArgs {
-    uint32_t wlog;       // log2 of the bytes of a code box's rows: 5, 6 or 7
-    uint32_t cols;       // code boxes side by side in a tile
+    uint32_t cols;       // code boxes of 128 bytes side by side in a tile
     uint32_t pw;         // bytes of a tile's pairs for one token
     uint32_t n_stages, stage, tile, ptile;  // tiles in flight; bytes of a stage, of a tile's codes of K, of its pairs of K
-    float scale2;        // scale * log2 e
+    float scale2;        // |scale| * log2 e, not 0
 };
 
 // Three warpgroups: two compute, one warp of the third fetches.  The launch gives 168 registers a thread, of which the
@@ -72,17 +71,17 @@ template <uint32_t kBits> __device__ __forceinline__ uint32_t take(uint32_t w, u
     return (i ? w >> 8 : w) & 0x00FF00FFu;
 }
 
-// N words from shared memory at an address that is a multiple of their size (at most 16 bytes).
-template <uint32_t kN> __device__ __forceinline__ void load_words(uint32_t (&w)[kN], const uint8_t *at) {
-    if constexpr (kN == 1) w[0] = *reinterpret_cast<const uint32_t *>(at);
-    if constexpr (kN == 2) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(at);
-        w[0] = v.x, w[1] = v.y;
-    }
-    if constexpr (kN == 4) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(at);
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    }
+// kN words from shared memory at an address that is a multiple of their size (at most 16 bytes).
+template <uint32_t kN> __device__ __forceinline__ void load_words(uint32_t (&w)[kN], uint32_t at) {
+    if constexpr (kN == 1) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at));
+    if constexpr (kN == 2) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+    if constexpr (kN == 4)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+}
+__device__ __forceinline__ uint32_t load_half(uint32_t at) {
+    uint16_t x;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at));
+    return x;
 }
 
 // Numbers of a pair, of type T.
@@ -104,12 +103,12 @@ __device__ __forceinline__ void mul2(float &x, float &y, float a, float b, float
         : "=f"(x), "=f"(y)
         : "f"(a), "f"(b), "f"(m), "f"(n));
 }
-// (x, y) += (a, b) m
-__device__ __forceinline__ void axpy2(float &x, float &y, float a, float b, float m) {
-    asm("{\n\t.reg .b64 s, t, u, v;\n\tmov.b64 s, {%2, %3};\n\tmov.b64 t, {%4, %4};\n\tmov.b64 u, {%0, %1};\n\t"
+// (x, y) += (a m, b n)
+__device__ __forceinline__ void vfma2(float &x, float &y, float a, float b, float m, float n) {
+    asm("{\n\t.reg .b64 s, t, u, v;\n\tmov.b64 s, {%2, %3};\n\tmov.b64 t, {%4, %5};\n\tmov.b64 u, {%0, %1};\n\t"
         "fma.rn.f32x2 v, s, t, u;\n\tmov.b64 {%0, %1}, v;\n\t}"
         : "+f"(x), "+f"(y)
-        : "f"(a), "f"(b), "f"(m));
+        : "f"(a), "f"(b), "f"(m), "f"(n));
 }
 // The power of two 2^e, e within -120 .. 120.
 __device__ __forceinline__ float power2(int e) { return __uint_as_float((uint32_t)(127 + max(-120, min(120, e))) << 23); }
@@ -125,6 +124,7 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
     constexpr uint32_t kQuarter = kGroup / 4, kEighth = kGroup / 8;
     constexpr uint32_t kKWords = kQuarter / 4;             // words of a lane's quarter of a group
     constexpr bool kHalf = __is_same(T, __half);
+    constexpr float kMiddle = kBits == 4 ? 8.f : 128.f;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (s_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t sm = s_addr(smem);
@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                     const uint32_t bid = __shfl_sync(kFull, id, sub), bin = __shfl_sync(kFull, in, sub);
                     if (b >= boxes) continue;
                     if (col < qa.cols)
-                        tma_box(base + kv * qa.tile + (((col << a.tlog) + (sub << rlog)) << qa.wlog), &codes,
-                                x + (int)(col << (qa.wlog - 1)), (int)bin, (int)bid, (int)kv, full + 8 * st);
+                        tma_box(base + kv * qa.tile + ((col << a.tlog) + (sub << rlog)) * 128, &codes, x + (int)col * 64, (int)bin,
+                                (int)bid, (int)kv, full + 8 * st);
                     else
                         tma_box(base + 2 * qa.tile + kv * qa.ptile + (sub << rlog) * qa.pw, &pairs, xp, (int)bin, (int)bid,
                                 (int)kv, full + 8 * st);
@@ -216,17 +216,19 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
     const uint32_t hd = warp & (a.nh - 1u), part = warp >> a.hlog;  // head of the group, kTok tokens of the tile
     // This lane's places in a tile: rows pi(r) and on for K, tokens 2c, pi(2c + 1) and on for V; bits 4..6 of an
     // address are swizzled by its bits 7..9
-    const uint32_t wl = qa.wlog, mask = wl == 7 ? 0x70u : wl == 6 ? 0x30u : 0x10u;
-    const uint32_t col = (hd * kHead) >> wl, inner = (hd * kHead) & ((1u << wl) - 1u);
-    const uint32_t tile0 = ((col << a.tlog) + part * kTok) << wl;
+    const uint32_t col = hd * kHead / 128, inner = hd * kHead % 128;
     const uint32_t tk = pi(r), t0 = 2 * c, t1 = pi(2 * c + 1);
-    const uint32_t xk = ((tk << wl) >> 3) & mask, x0 = ((t0 << wl) >> 3) & mask, x1 = ((t1 << wl) >> 3) & mask;
+    const uint32_t tile0 = sm + ((col << a.tlog) + part * kTok) * 128;
+    // of the first group; the next group's address differs in bits 4..6 alone
+    const uint32_t at_k = tile0 + tk * 128 + ((inner + c * kQuarter) ^ (tk << 4));
+    const uint32_t at_v0 = tile0 + qa.tile + t0 * 128 + ((inner + r * kEighth) ^ (t0 << 4));
+    const uint32_t at_v1 = tile0 + qa.tile + t1 * 128 + ((inner + r * kEighth) ^ (t1 << 4));
     bool ok = true, more = next_piece(a, w, p);
     while (more) {
         const bool shared = p.r == a.R, active = p.group * a.nh + hd < a.Hkv;
         const uint32_t head = p.group * a.nh + hd, row0 = p.range << a.rlog;
         const uint32_t own_tokens = shared ? a.P : p.len - a.P;
-        const uint32_t pair0 = 2 * qa.tile + ((p.group * a.nh * NG * 4) & 15u) + hd * NG * 4 + (part * kTok + tk) * qa.pw;
+        const uint32_t pair0 = sm + 2 * qa.tile + ((p.group * a.nh * NG * 4) & 15u) + hd * NG * 4 + (part * kTok + tk) * qa.pw;
         uint32_t least = own_tokens;
         if (!shared) least = min(least, p.len + 1 > a.nq + a.P ? p.len + 1 - a.nq - a.P : 0u);
         // The queries, each scaled by a power of two so that its largest channel lies in [2^14, 2^15): bf16 ones then
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
             const int up = mx == 0.f || mx == INFINITY ? 0 : max(-100, min(100, 14 - exponent(mx)));
-            const float high = power2(up);
+            const float high = a.flip ? -power2(up) : power2(up);  // a negative scale turns q
 #pragma unroll
             for (uint32_t e = 0; e < D / 4; e++) x[e] *= high;
             float sum = 0.f;
@@ -305,7 +307,12 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
 
         // Running maximum m and sum l of the weights, their products with the low values, and the power of two F that a
         // group's weights times scales are multiplied by before they become operands.
-        float o[kN][D / 16][4], m[kN][2], l[kN][2], lows[kN][NG][2], F[kN][NG][2];
+        // Codes are taken about their middle: the operands' rounding then meets half the codes' size, and with one column
+        // tile the middle's part is a product of its own (mid), taken away again at the end.
+        constexpr bool kMid = kN == 1;
+        float o[kN][D / 16][4], m[kN][2], l[kN][2][2], lows[kN][NG][2][2], F[kN][NG][2][2], mid[kN][NG][4], most[NG];
+#pragma unroll
+        for (uint32_t g = 0; g < NG; g++) most[g] = 1.f;  // the larger F of the columns
 #pragma unroll
         for (uint32_t n = 0; n < kN; n++) {
 #pragma unroll
@@ -315,11 +322,12 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
 #pragma unroll
             for (uint32_t j = 0; j < 2; j++) {
                 m[n][j] = -INFINITY;
-                l[n][j] = 0.f;
+                l[n][j][0] = l[n][j][1] = 0.f;
 #pragma unroll
                 for (uint32_t g = 0; g < NG; g++) {
-                    lows[n][g][j] = 0.f;
-                    F[n][g][j] = 1.f;
+                    lows[n][g][j][0] = lows[n][g][j][1] = 0.f;
+                    F[n][g][j][0] = F[n][g][j][1] = 1.f;
+                    mid[n][g][j] = mid[n][g][2 + j] = 0.f;
                 }
             }
         }
@@ -331,14 +339,14 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                 continue;
             }
             const uint32_t tok = ((p.tile0 + k) << a.tlog) + kTok * part;  // this warp's first token of the item
-            const uint8_t *base = smem + st * qa.stage;
+            const uint32_t base = st * qa.stage;
             // 16 tokens at a time; not unrolled: the loop's body alone fills the instruction cache
 #pragma unroll 1
             for (uint32_t t = 0; active && t < kTok && tok + t < own_tokens; t += 16) {
-                const uint8_t *kp = base + pair0 + t * qa.pw, *vp = kp + qa.ptile;
-                const uint8_t *kc = base + tile0 + ((t + tk) << wl);
+                const uint32_t kp = base + pair0 + t * qa.pw, vp = kp + qa.ptile;
+                const uint32_t kc = base + at_k + t * 128, vc0 = base + at_v0 + t * 128, vc1 = base + at_v1 + t * 128;
                 const bool hidden = tok + t + 16 > least;  // some rows do not see some of the tokens, or there are none
-                float s[kN][4];
+                float s[kN][4], x[kN][2][2];  // scores; weights by column and row
                 {
                     uint32_t pw[2][NG];
 #pragma unroll
@@ -346,8 +354,11 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                     // low values: words (scale, low) times (0, part of the sum of q)
                     uint32_t lo[2];
 #pragma unroll
-                    for (uint32_t h = 0; h < 2; h++)
-                        lo[h] = NG == 1 ? pw[h][0] : *reinterpret_cast<const uint32_t *>(kp + 8 * h * qa.pw + 4 * (c & (NG - 1)));
+                    for (uint32_t h = 0; h < 2; h++) {
+                        uint32_t y[1] = {pw[h][0]};
+                        if constexpr (NG > 1) load_words<1>(y, kp + 8 * h * qa.pw + 4 * (c & (NG - 1)));
+                        lo[h] = y[0];
+                    }
                     const uint32_t lw[4] = {lo[0] & 0xFFFF0000u, lo[1] & 0xFFFF0000u, lo[0] & 0xFFFF0000u, lo[1] & 0xFFFF0000u};
 #pragma unroll
                     for (uint32_t n = 0; n < kN; n++) {
@@ -363,16 +374,15 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                         uint32_t wk[2][kKWords];
 #pragma unroll
                         for (uint32_t h = 0; h < 2; h++) {
-                            const uint8_t *row = kc + ((8 * h) << wl);
-                            const uint32_t at = inner + g * kGroup + c * kQuarter;
+                            const uint32_t row = (kc ^ (g * kGroup)) + 8 * 128 * h;
                             if constexpr (kKWords == 8) {
                                 uint32_t y[4], z[4];
-                                load_words<4>(y, row + (at ^ xk));
-                                load_words<4>(z, row + ((at + 16) ^ xk));
+                                load_words<4>(y, row);
+                                load_words<4>(z, row ^ 16);
 #pragma unroll
                                 for (uint32_t e = 0; e < 4; e++) wk[h][e] = y[e], wk[h][4 + e] = z[e];
                             } else {
-                                load_words<kKWords>(wk[h], row + (at ^ xk));
+                                load_words<kKWords>(wk[h], row);
                             }
                         }
                         float acc[kN][kChains][4];
@@ -397,10 +407,6 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                                 s[n][e] = fmaf(y, sc[e >> 1], s[n][e]);
                             }
                     }
-#pragma unroll
-                    for (uint32_t n = 0; n < kN; n++)
-#pragma unroll
-                        for (uint32_t e = 0; e < 4; e++) s[n][e] *= fq[n][e & 1u];
                 }
                 uint32_t pv[2][NG];  // the pairs of V
 #pragma unroll
@@ -417,63 +423,73 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
 #pragma unroll
                             for (uint32_t g = 0; g < NG; g++) pv[h][g] = 0;
                 }
-                // Weights are e^{s - m}.  m and F stay while weights are at most 2^8 and operands at most 2^15, which a
-                // lane's largest score and scale bound.  Beyond that m becomes the column's maximum and F such that the
-                // largest operand of column and group lies in [2^6, 2^7); O is scaled along.
-                bool grow[kN][2], any = false;
-                float widest[NG];
+                // Weights are 2^{s fq - m}.  m and F stay while no operand can exceed 2^15, by a lane's largest weight, scale
+                // and F.  Otherwise m becomes the maximum of a column that did exceed it and F such that its largest
+                // operand lies in [2^4, 2^5), and O is scaled along: eleven octaves go by before the next time.
+                float widest = 0.f, x_most = -INFINITY;
 #pragma unroll
-                for (uint32_t g = 0; g < NG; g++) widest[g] = scale_of<T>(__vmaxu2(pv[0][g], pv[1][g]));
+                for (uint32_t g = 0; g < NG; g++) widest = fmaxf(widest, scale_of<T>(__vmaxu2(pv[0][g], pv[1][g])) * most[g]);
 #pragma unroll
                 for (uint32_t n = 0; n < kN; n++)
 #pragma unroll
-                    for (uint32_t j = 0; j < 2; j++) {
-                        const float d = fmaxf(s[n][j], s[n][2 + j]) - m[n][j], x = ex2(d);
-                        float y = 0.f;  // (in this order: a weight of 0 times a scale is not lost in an overflow)
+                    for (uint32_t j = 0; j < 2; j++) x_most = fmaxf(x_most, fmaf(fmaxf(s[n][j], s[n][2 + j]), fq[n][j], -m[n][j]));
+                if (__builtin_expect(__any_sync(kFull, !(ex2(x_most) * widest <= 32768.f)), 0)) {
 #pragma unroll
-                        for (uint32_t g = 0; g < NG; g++) y = fmaxf(y, x * widest[g] * F[n][g][j]);
-                        grow[n][j] = d > 8.f || y > 32768.f;
-                        any |= grow[n][j];
-                    }
-                if (__builtin_expect(__any_sync(kFull, any), 0)) {
+                    for (uint32_t g = 0; g < NG; g++) most[g] = 0.f;
 #pragma unroll
                     for (uint32_t n = 0; n < kN; n++)
 #pragma unroll
                         for (uint32_t j = 0; j < 2; j++) {
-                            // (a column moves for its own sake only: no query's rounding depends on the others)
-                            const bool move = __ballot_sync(kFull, grow[n][j]) & (0x11111111u << c);
-                            float mx = move ? fmaxf(s[n][j], s[n][2 + j]) : -INFINITY;
+                            const float y[2] = {s[n][j] * fq[n][j], s[n][2 + j] * fq[n][j]};
+                            float mx = fmaxf(y[0], y[1]);
 #pragma unroll
                             for (uint32_t d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
-                            const float nm = fmaxf(m[n][j], mx), f = nm == m[n][j] ? 1.f : ex2(m[n][j] - nm);
-                            m[n][j] = nm;
-                            l[n][j] *= f;
-                            const float z = nm == -INFINITY ? 0.f : nm, x[2] = {ex2(s[n][j] - z), ex2(s[n][2 + j] - z)};
+                            const bool first = m[n][j] == -INFINITY;
+                            const float z = !first ? m[n][j] : mx == -INFINITY ? 0.f : mx, wt[2] = {ex2(y[0] - z), ex2(y[1] - z)};
+                            float v[NG];  // the largest weights times scales
+                            bool move = first && mx != -INFINITY;
 #pragma unroll
                             for (uint32_t g = 0; g < NG; g++) {
-                                // the largest weight times scale, those that F was chosen by included
-                                float v = x[0] == 0.f ? 0.f : x[0] * scale_of<T>(pv[0][g]);
-                                v = x[1] == 0.f ? v : fmaxf(v, x[1] * scale_of<T>(pv[1][g]));
+                                v[g] = 0.f;
 #pragma unroll
-                                for (uint32_t d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, d));
-                                const float old = f / F[n][g][j];
-                                v = fmaxf(v, 128.f * old);
-                                if (move) F[n][g][j] = power2(6 - exponent(v));
-                                lows[n][g][j] *= f;
+                                for (uint32_t h = 0; h < 2; h++)
+                                    if (wt[h] != 0.f) v[g] = fmaxf(v[g], wt[h] * scale_of<T>(pv[h][g]));
+#pragma unroll
+                                for (uint32_t d = 4; d < 32; d <<= 1) v[g] = fmaxf(v[g], __shfl_xor_sync(kFull, v[g], d));
+                                move |= v[g] * F[n][g][j][0] > 32768.f;
+                            }
+                            // (a column moves for its own sake only: no query's rounding depends on the others)
+                            const float nm = move ? fmaxf(m[n][j], mx) : m[n][j], f = nm == m[n][j] ? 1.f : ex2(m[n][j] - nm);
+                            const float by_new = first ? 1.f : f;
+                            m[n][j] = nm;
+                            l[n][j][0] *= f;
+                            l[n][j][1] *= f;
+#pragma unroll
+                            for (uint32_t g = 0; g < NG; g++) {
+                                float *F_ = F[n][g][j];
+                                const float old = f / F_[0], nf = move ? power2(4 - exponent(fmaxf(v[g] * by_new, 32.f * old))) : F_[0];
+                                const float by = old * nf;
+                                F_[0] = F_[1] = nf;
+                                most[g] = fmaxf(most[g], nf);
+                                lows[n][g][j][0] *= f;
+                                lows[n][g][j][1] *= f;
 #pragma unroll
                                 for (uint32_t d = 0; d < G / 16; d++) {
-                                    o[n][g * (G / 16) + d][j] *= old * F[n][g][j];
-                                    o[n][g * (G / 16) + d][2 + j] *= old * F[n][g][j];
+                                    o[n][g * (G / 16) + d][j] *= by;
+                                    o[n][g * (G / 16) + d][2 + j] *= by;
                                 }
+                                if constexpr (kMid) mid[n][g][j] *= by;
                             }
                         }
                 }
 #pragma unroll
                 for (uint32_t n = 0; n < kN; n++)
 #pragma unroll
-                    for (uint32_t e = 0; e < 4; e++) {
-                        s[n][e] = ex2(s[n][e] - (m[n][e & 1u] == -INFINITY ? 0.f : m[n][e & 1u]));
-                        l[n][e & 1u] += s[n][e];
+                    for (uint32_t j = 0; j < 2; j++) {
+                        const float z = m[n][j] == -INFINITY ? 0.f : m[n][j];
+#pragma unroll
+                        for (uint32_t h = 0; h < 2; h++) x[n][j][h] = ex2(fmaf(s[n][2 * h + j], fq[n][j], -z));
+                        add2(l[n][j][0], l[n][j][1], x[n][j][0], x[n][j][1]);
                     }
                 // A pair that is not finite must stay out of the rows that do not see its token, whose weight is 0: the rows
                 // that do get it (infinite or NaN, as it is) here, and the products a zero.
@@ -487,32 +503,43 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                                 for (uint32_t n = 0; n < kN; n++)
 #pragma unroll
                                     for (uint32_t j = 0; j < 2; j++)
-                                        if (s[n][2 * h + j] != 0.f) lows[n][g][j] += scale_of<T>(pv[h][g]) + low_of<T>(pv[h][g]);
+                                        if (x[n][j][h] != 0.f) lows[n][g][j][h] += scale_of<T>(pv[h][g]) + low_of<T>(pv[h][g]);
                                 pv[h][g] = 0;
                             }
                 // O += operands times codes of V
-                const uint8_t *vc = base + qa.tile + tile0 + (t << wl);
 #pragma unroll
                 for (uint32_t g = 0; g < NG; g++) {
                     uint32_t b[kN][2];
+                    const float sc[2] = {scale_of<T>(pv[0][g]), scale_of<T>(pv[1][g])};
+                    float low[2] = {low_of<T>(pv[0][g]), low_of<T>(pv[1][g])};
+                    if constexpr (kMid) {
+                        low[0] = fmaf(sc[0], kMiddle, low[0]);
+                        low[1] = fmaf(sc[1], kMiddle, low[1]);
+                    }
 #pragma unroll
-                    for (uint32_t h = 0; h < 2; h++) {
-                        const float low = low_of<T>(pv[h][g]), sc = scale_of<T>(pv[h][g]);
+                    for (uint32_t n = 0; n < kN; n++) {
+                        float y[2][2];
 #pragma unroll
-                        for (uint32_t n = 0; n < kN; n++) {
-#pragma unroll
-                            for (uint32_t j = 0; j < 2; j++) lows[n][g][j] = fmaf(s[n][2 * h + j], low, lows[n][g][j]);
-                            b[n][h] = transpose8(Half<__half>::pack(s[n][2 * h] * sc * F[n][g][0], s[n][2 * h + 1] * sc * F[n][g][1]));
+                        for (uint32_t j = 0; j < 2; j++) {
+                            // (in this order: a weight of 0 times a scale is not lost in an overflow)
+                            mul2(y[j][0], y[j][1], x[n][j][0], x[n][j][1], sc[0], sc[1]);
+                            mul2(y[j][0], y[j][1], y[j][0], y[j][1], F[n][g][j][0], F[n][g][j][1]);
+                            vfma2(lows[n][g][j][0], lows[n][g][j][1], x[n][j][0], x[n][j][1], low[0], low[1]);
+                        }
+                        b[n][0] = transpose8(Half<__half>::pack(y[0][0], y[1][0]));
+                        b[n][1] = transpose8(Half<__half>::pack(y[0][1], y[1][1]));
+                        if constexpr (kMid) {
+                            constexpr uint32_t k2 = (uint32_t)kMiddle * 0x10001u;
+                            const uint32_t middles[4] = {k2, k2, k2, k2};
+                            Half<__half>::mma(mid[n][g], middles, b[n][0], b[n][1]);
                         }
                     }
-                    const uint32_t at = inner + g * kGroup + r * kEighth;
-                    const uint8_t *from[4] = {vc + (t0 << wl) + (at ^ x0), vc + (t1 << wl) + (at ^ x1),
-                                              vc + ((t0 + 8) << wl) + (at ^ x0), vc + ((t1 + 8) << wl) + (at ^ x1)};
+                    const uint32_t v0 = vc0 ^ (g * kGroup), v1 = vc1 ^ (g * kGroup), from[4] = {v0, v1, v0 + 8 * 128, v1 + 8 * 128};
                     constexpr uint32_t kWords = kEighth < 4 ? 1 : kEighth / 4;
                     uint32_t wv[4][kWords];
 #pragma unroll
                     for (uint32_t e = 0; e < 4; e++) {
-                        if constexpr (kEighth == 2) wv[e][0] = *reinterpret_cast<const uint16_t *>(from[e]);
+                        if constexpr (kEighth == 2) wv[e][0] = load_half(from[e]);
                         else load_words<kWords>(wv[e], from[e]);
                     }
                     // words of two tokens' codes side by side: channel by channel, operands along the tokens
@@ -523,11 +550,11 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                         const uint32_t y0 = __byte_perm(wv[0][e / 2], wv[1][e / 2], sel), y1 = __byte_perm(wv[2][e / 2], wv[3][e / 2], sel);
 #pragma unroll
                         for (uint32_t d = 0; d < kTiles; d++) {
-                            const uint32_t x[4] = {take<kBits>(y0, 2 * d), take<kBits>(y0, 2 * d + 1), take<kBits>(y1, 2 * d),
+                            const uint32_t v[4] = {take<kBits>(y0, 2 * d), take<kBits>(y0, 2 * d + 1), take<kBits>(y1, 2 * d),
                                                    take<kBits>(y1, 2 * d + 1)};
 #pragma unroll
                             for (uint32_t n = 0; n < kN; n++)
-                                Half<__half>::mma(o[n][g * (G / 16) + e * kTiles + d], x, b[n][0], b[n][1]);
+                                Half<__half>::mma(o[n][g * (G / 16) + e * kTiles + d], v, b[n][0], b[n][1]);
                         }
                     }
                 }
@@ -544,27 +571,30 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
             for (uint32_t n = 0; n < kN; n++)
 #pragma unroll
                 for (uint32_t j = 0; j < 2; j++) {
+                    float sum = l[n][j][0] + l[n][j][1], low[NG];
+#pragma unroll
+                    for (uint32_t g = 0; g < NG; g++) low[g] = lows[n][g][j][0] + lows[n][g][j][1];
 #pragma unroll
                     for (uint32_t d = 4; d < 32; d <<= 1) {
-                        l[n][j] += __shfl_xor_sync(kFull, l[n][j], d);
+                        sum += __shfl_xor_sync(kFull, sum, d);
 #pragma unroll
-                        for (uint32_t g = 0; g < NG; g++) lows[n][g][j] += __shfl_xor_sync(kFull, lows[n][g][j], d);
+                        for (uint32_t g = 0; g < NG; g++) low[g] += __shfl_xor_sync(kFull, low[g], d);
                     }
                     const uint32_t x = 8 * n + 2 * c + j;
                     const Row row = row_of(a, p, row0 + x, head);
                     if (!row.valid) continue;
-                    const float inv = !answer ? 1.f : l[n][j] == 0.f ? 0.f : 1.f / l[n][j];
+                    const float inv = !answer ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
                     float *part_o = a.part_o + (slot + x) * D;
                     uint16_t *dst = a.out + row.r * a.os[0] + row.i * a.os[1] + row.h * a.os[2];
                     constexpr uint32_t kPer = G / 8;  // channels of a group that this lane has
 #pragma unroll
                     for (uint32_t g = 0; g < NG; g++) {
-                        const float even = 0x1p24f / F[n][g][j], odd = kBits == 4 ? even * 0.0625f : even, low = lows[n][g][j];
+                        const float unit = 0x1p24f / F[n][g][j][0], centre = kMid ? mid[n][g][j] : 0.f;
                         float y[kPer];
 #pragma unroll
                         for (uint32_t d = 0; d < kPer / 2; d++) {
-                            y[2 * d] = fmaf(o[n][g * (G / 16) + d][j], even, low) * inv;
-                            y[2 * d + 1] = fmaf(o[n][g * (G / 16) + d][2 + j], odd, low) * inv;
+                            y[2 * d] = fmaf(o[n][g * (G / 16) + d][j] - centre, unit, low[g]) * inv;
+                            y[2 * d + 1] = fmaf(o[n][g * (G / 16) + d][2 + j] * (kBits == 4 ? 0.0625f : 1.f) - centre, unit, low[g]) * inv;
                         }
                         const uint32_t ch = g * G + r * kPer;
                         if (answer) {
@@ -579,10 +609,10 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                         }
                     }
                     if (r == 0) {
-                        if (!answer) a.part_ml[slot + x] = make_float2(m[n][j], l[n][j]);
+                        if (!answer) a.part_ml[slot + x] = make_float2(m[n][j], sum);
                         else if (a.lse)
                             a.lse[((uint64_t)row.r * a.nq + row.i) * (a.g * a.Hkv) + row.h] =
-                                l[n][j] == 0.f ? -INFINITY : (m[n][j] + log2f(l[n][j])) * 0.6931471805599453f;
+                                sum == 0.f ? -INFINITY : (m[n][j] + log2f(sum)) * 0.6931471805599453f;
                     }
                 }
         }
