@@ -1,10 +1,10 @@
 // cg_quant.cu -- tokens written into, and read back from, a paged pool held in
 // 4 or 8 bits (sm_103a).
 //
-// A thread takes eight channels at a time: 16 bytes of the 16-bit tensor, 4
-// or 8 of codes.  The 4, 8 or 16 threads of a group find its smallest and
-// largest value by exchange, so that a row is read once and its codes go out
-// in runs of 128 or 256 bytes a warp.
+// A lane takes eight channels at a time: 16 bytes of the 16-bit tensor, 4 or 8
+// of codes.  The 4, 8 or 16 lanes of a group find its smallest and largest
+// value by exchange, so that a row is read once and its codes go out in runs of
+// 128 or 256 bytes a warp.
 #include "cg_async.cuh"
 #include "cg_quant.cuh"
 
@@ -12,7 +12,6 @@ namespace cg {
 namespace {
 
 constexpr uint32_t kThreads = 256;
-constexpr uint32_t kKeep = 1024;  // sequences whose first rows a block keeps in shared memory
 
 template <class T> struct Type;
 template <> struct Type<__half> {
@@ -22,6 +21,7 @@ template <> struct Type<__half> {
     static __device__ __forceinline__ T2 two(__half a, __half b) { return __halves2half2(a, b); }
     static __device__ __forceinline__ float of(uint32_t bits) { return __half2float(__ushort_as_half((uint16_t)bits)); }
     static __device__ __forceinline__ uint32_t bits(float x) { return __half_as_ushort(__float2half_rn(x)); }
+    static __device__ __forceinline__ uint32_t bits_up(float x) { return __half_as_ushort(__float2half_ru(x)); }
     static constexpr uint32_t kNan = 0x7E00u;
     static constexpr float kMost = 65504.f;
 };
@@ -32,6 +32,7 @@ template <> struct Type<__nv_bfloat16> {
     static __device__ __forceinline__ T2 two(__nv_bfloat16 a, __nv_bfloat16 b) { return __halves2bfloat162(a, b); }
     static __device__ __forceinline__ float of(uint32_t bits) { return __uint_as_float(bits << 16); }
     static __device__ __forceinline__ uint32_t bits(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+    static __device__ __forceinline__ uint32_t bits_up(float x) { return (__float_as_uint(x) + 0xFFFFu) >> 16; }  // x >= 0
     static constexpr uint32_t kNan = 0x7FC0u;
     static constexpr float kMost = 3.3895313892515355e38f;  // (2 - 2^-7) 2^127
 };
@@ -93,214 +94,240 @@ __device__ __noinline__ float code_at_border(float y, float s) {
     return n + ((int)n & 1);
 }
 
-// A block takes a run of kU x 256 eight-channel units of the flattened rows,
-// finds their tokens' places once, and then goes over `slices` layers of K and
-// V, in which the places are the same.
+// A warp, or an eighth to a half of one where rows are short, takes a row: its
+// lanes find the token's place and go over the row's eight-channel units side
+// by side, kBatch of them in flight, in K and V of some layers, in which the
+// place is the same.
+constexpr uint32_t kBatch = 4;
 struct Job {
     QuantPool p;
     TokenRows t;
     uint32_t *status;
+    uint32_t llog;             // log2 of the lanes of a row
     uint32_t units;            // of a row
-    uint32_t runs;             // of a layer's K
-    uint32_t slices, n_slices; // of a block; all of them: layers x 2
+    uint32_t steps, chunks;    // steps of a warp along a row; how many warps share a row
+    uint32_t slices, n_slices; // of a warp; all of them: layers x (K, V)
 };
 
-constexpr uint32_t kMaxRows = 4 * kThreads / 8 + 1;  // rows that a run touches: C is 64 at least
-
-template <uint32_t kU> struct Run {
-    uint64_t at[kU];    // word offset of the row in a layer's K, or kNone / kOutside
-    uint32_t row[kU], unit[kU];
-    uint32_t slice, end;
+struct Run {
+    uint32_t j, unit, end;  // row; this lane's first unit, end of the warp's units
+    uint64_t at;            // place, or kNone / kOutside
+    uint32_t slice, last;
+    bool some;              // some lane of the warp has a row
     __device__ __forceinline__ Run(const Job &b) {
-        __shared__ uint32_t sh_first[kKeep + 1];
-        __shared__ uint64_t sh_at[kMaxRows];
-        const uint32_t *first = b.t.first;
-        if (first && b.t.n_seqs <= kKeep) {
-            for (uint32_t k = threadIdx.x; k <= b.t.n_seqs; k += kThreads) sh_first[k] = first[k];
-            first = sh_first;
-            __syncthreads();
-        }
-        const uint32_t part = blockIdx.x / b.runs, run = blockIdx.x - part * b.runs;
-        const uint64_t from = (uint64_t)run * (kU * kThreads);
-        const uint32_t j0 = from >> 32 ? (uint32_t)(from / b.units) : (uint32_t)from / b.units;
-        const uint32_t x0 = (uint32_t)(from - (uint64_t)j0 * b.units), rows = (x0 + kU * kThreads - 1) / b.units + 1;
-        for (uint32_t k = threadIdx.x; k < rows; k += kThreads)
-            sh_at[k] = j0 + k < b.t.n_rows ? place(b.p, b.t, first, j0 + k, b.status) : kNone;
-        __syncthreads();
-#pragma unroll
-        for (uint32_t u = 0; u < kU; u++) {
-            const uint32_t x = x0 + u * kThreads + threadIdx.x, k = x / b.units;
-            row[u] = j0 + k;
-            unit[u] = x - k * b.units;
-            at[u] = sh_at[k];
-        }
-        slice = part * b.slices;
-        end = min(slice + b.slices, b.n_slices);
+        const uint32_t lane = threadIdx.x & 31u, id = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+        const uint32_t group = b.chunks == 1 ? id : id / b.chunks, chunk = b.chunks == 1 ? 0u : id - group * b.chunks;
+        const uint64_t row = ((uint64_t)group << (5u - b.llog)) + (lane >> b.llog);
+        j = (uint32_t)row;
+        unit = ((chunk * b.steps) << b.llog) + (lane & ((1u << b.llog) - 1u));
+        end = min(b.units, ((chunk + 1u) * b.steps) << b.llog);
+        at = row < b.t.n_rows ? place(b.p, b.t, b.t.first, j, b.status) : kNone;
+        slice = blockIdx.y * b.slices;
+        last = min(slice + b.slices, b.n_slices);
+        some = __any_sync(kFull, at != kNone);
     }
 };
 
-template <class T, uint32_t kBits, uint32_t kU>
-__global__ void __launch_bounds__(kThreads) k_quant_write(const Job b) {
+// Codes and pair of a unit; its group's `lanes` threads call together.
+template <class T, uint32_t kBits>
+__device__ __forceinline__ bool quantise(const uint4 &in, uint32_t lanes, uint2 &codes, uint32_t &pair) {
     using Y = Type<T>;
     constexpr float kTop = (1u << kBits) - 1u, kMagic = 12582912.f;  // 1.5 2^23: adding it rounds to an integer
-    const Run<kU> r(b);
-    const uint32_t lanes = b.p.group / 8;
-    for (uint32_t slice = r.slice; slice < r.end; slice++) {
+    const typename Y::T2 *h = reinterpret_cast<const typename Y::T2 *>(&in);
+    typename Y::T2 mn = __hmin2_nan(__hmin2_nan(h[0], h[1]), __hmin2_nan(h[2], h[3]));
+    typename Y::T2 mx = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+    // both in one word: the larger of x and -x's
+    typename Y::T2 mm = Y::two(__hmax_nan(mx.x, mx.y), __hneg(__hmin_nan(mn.x, mn.y)));
+    mm = __hmax2_nan(mm, __shfl_xor_sync(kFull, mm, 1));
+    mm = __hmax2_nan(mm, __shfl_xor_sync(kFull, mm, 2));
+    if (lanes > 4) mm = __hmax2_nan(mm, __shfl_xor_sync(kFull, mm, 4));
+    if (lanes > 8) mm = __hmax2_nan(mm, __shfl_xor_sync(kFull, mm, 8));
+    const float2 hl = Y::wide(mm);
+    const float low = -hl.y, d = hl.x - low;
+    // The smallest scale of the type with scale * kTop >= d.  d (1 - 2^-21) / kTop, rounded up to the type, is that or
+    // the number before it; the products are exact.
+    uint32_t sb = Y::bits_up(d * ((1.f - 0x1p-21f) / kTop));
+    if (Y::of(sb) * kTop < d) sb++;
+    const float s = Y::of(sb);
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    if (!sb) inv = 0.f;
+    // Codes are the nearest integers to (x - low) / s.  The quotients are off by 2^-22 of themselves at most: a code
+    // that is not near a border is right (and where 1 / s may not be finite, none is trusted).
+    float y[8], c[8], far = s < 0x1p-90f && sb ? 1.f : 0.f;
+    constexpr float kNear = 0.5f - kTop * 0x1p-20f;
+#pragma unroll
+    for (uint32_t k = 0; k < 4; k++) {
+        const float2 x = Y::wide(h[k]);
+        y[2 * k] = x.x, y[2 * k + 1] = x.y;
+        add2(y[2 * k], y[2 * k + 1], -low, -low);
+        fma2(c[2 * k], c[2 * k + 1], y[2 * k], y[2 * k + 1], inv, kMagic);
+        add2(c[2 * k], c[2 * k + 1], -kMagic, -kMagic);
+        far = fmaxf(far, fmaxf(fabsf(fmaf(y[2 * k], inv, -c[2 * k])), fabsf(fmaf(y[2 * k + 1], inv, -c[2 * k + 1]))));
+    }
+    const bool finite = d - d == 0.f;
+    if (far > kNear && finite)
+#pragma unroll
+        for (uint32_t k = 0; k < 8; k++)
+            if (far >= 1.f || fabsf(fmaf(y[k], inv, -c[k])) > kNear) c[k] = code_at_border(y[k], s);
+    // codes side by side, as integers
+    uint32_t w[2];
+    if constexpr (kBits == 4) {
+#pragma unroll
+        for (uint32_t k = 0; k < 2; k++)
+            w[k] = __float_as_uint(fmaf(c[4 * k + 3], 4096.f, fmaf(c[4 * k + 2], 256.f, fmaf(c[4 * k + 1], 16.f, c[4 * k]))) + 8388608.f);
+        codes.x = __byte_perm(w[0], w[1], 0x5410);
+    } else {
+#pragma unroll
+        for (uint32_t k = 0; k < 2; k++)
+            w[k] = __byte_perm(__float_as_uint(fmaf(c[4 * k + 1], 256.f, c[4 * k]) + 8388608.f),
+                               __float_as_uint(fmaf(c[4 * k + 3], 256.f, c[4 * k + 2]) + 8388608.f), 0x5410);
+        codes = make_uint2(w[0], w[1]);
+    }
+    pair = sb | Y::bits(low) << 16;
+    if (!finite) {
+        codes = make_uint2(0, 0);
+        pair = Y::kNan << 16;
+    }
+    return finite;
+}
+
+template <class T, uint32_t kBits>
+__global__ void __launch_bounds__(kThreads) k_quant_write(const Job b) {
+    const Run r(b);
+    if (!r.some) return;
+    const uint32_t lanes = b.p.group / 8, glog = 31u - __clz(lanes), step = 1u << b.llog;
+    const bool here = r.at < kOutside, first = here && (threadIdx.x & (lanes - 1u)) == 0;
+    for (uint32_t slice = r.slice; slice < r.last; slice++) {
         const uint32_t layer = slice >> 1, kv = slice & 1u;
-        const uint16_t *src = kv ? b.t.v + layer * b.t.vs[0] : b.t.k + layer * b.t.ks[0];
-        const uint64_t stride = kv ? b.t.vs[1] : b.t.ks[1];
-        uint16_t *pool = b.p.pool + layer * b.p.layer + kv * b.p.kv;
-        uint4 in[kU];
+        const uint16_t *src = kv ? b.t.v + layer * b.t.vs[0] + r.j * b.t.vs[1] : b.t.k + layer * b.t.ks[0] + r.j * b.t.ks[1];
+        uint32_t *row = reinterpret_cast<uint32_t *>(b.p.pool + layer * b.p.layer + kv * b.p.kv + (here ? r.at : 0));
+        uint32_t *pairs = row + b.p.codes / 2;
+        for (uint32_t u0 = r.unit; __any_sync(kFull, u0 < r.end); u0 += kBatch * step) {
+            uint4 in[kBatch];
 #pragma unroll
-        for (uint32_t u = 0; u < kU; u++)
-            in[u] = r.at[u] < kOutside ? *reinterpret_cast<const uint4 *>(src + r.row[u] * stride + 8 * r.unit[u]) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (uint32_t u = 0; u < kU; u++) {
-            const typename Y::T2 *h = reinterpret_cast<const typename Y::T2 *>(&in[u]);
-            typename Y::T2 mn = __hmin2_nan(__hmin2_nan(h[0], h[1]), __hmin2_nan(h[2], h[3]));
-            typename Y::T2 mx = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
-            // both in one word: the larger of x and -x's
-            typename Y::T2 mm = Y::two(__hmax_nan(mx.x, mx.y), __hneg(__hmin_nan(mn.x, mn.y)));
-            mm = __hmax2_nan(mm, __shfl_xor_sync(kFull, mm, 1));
-            mm = __hmax2_nan(mm, __shfl_xor_sync(kFull, mm, 2));
-            if (lanes > 4) mm = __hmax2_nan(mm, __shfl_xor_sync(kFull, mm, 4));
-            if (lanes > 8) mm = __hmax2_nan(mm, __shfl_xor_sync(kFull, mm, 8));
-            if (r.at[u] >= kOutside) continue;
-            const float2 hl = Y::wide(mm);
-            const float low = -hl.y, d = hl.x - low;
-            const bool finite = d - d == 0.f;
-            // the smallest scale of the type with scale * kTop >= d: the products are exact, the first guess is at
-            // most one step off
-            uint32_t sb = Y::bits(d * (1.f / kTop));
-            if (sb && Y::of(sb - 1) * kTop >= d) sb--;
-            if (Y::of(sb) * kTop < d) sb++;
-            const float s = Y::of(sb);
-            float inv;
-            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-            if (!sb) inv = 0.f;
-            // codes: the nearest integers to (x - low) / s, unless one is near a border (or 1 / s too large)
-            float y[8], c[8], far = s < 0x1p-90f && sb ? 1.f : 0.f;
-#pragma unroll
-            for (uint32_t k = 0; k < 4; k++) {
-                const float2 x = Y::wide(h[k]);
-                float q[2], e[2];
-                y[2 * k] = x.x, y[2 * k + 1] = x.y;
-                add2(y[2 * k], y[2 * k + 1], -low, -low);
-                fma2(q[0], q[1], y[2 * k], y[2 * k + 1], inv, kMagic);
-                c[2 * k] = q[0], c[2 * k + 1] = q[1];
-                add2(c[2 * k], c[2 * k + 1], -kMagic, -kMagic);
-                e[0] = fmaf(y[2 * k], inv, -c[2 * k]), e[1] = fmaf(y[2 * k + 1], inv, -c[2 * k + 1]);
-                far = fmaxf(far, fmaxf(fabsf(e[0]), fabsf(e[1])));
+            for (uint32_t u = 0; u < kBatch; u++) {
+                const uint32_t unit = u0 + u * step;
+                in[u] = here && unit < r.end ? *reinterpret_cast<const uint4 *>(src + 8 * unit) : make_uint4(0, 0, 0, 0);
             }
-            if (far > 0.4995f && finite)
 #pragma unroll
-                for (uint32_t k = 0; k < 8; k++)
-                    if (far >= 1.f || fabsf(fmaf(y[k], inv, -c[k])) > 0.4995f) c[k] = code_at_border(y[k], s);
-            uint16_t *row = pool + r.at[u];
-            if constexpr (kBits == 4) {
-                uint32_t w[2];
-#pragma unroll
-                for (uint32_t k = 0; k < 2; k++)
-                    w[k] = __float_as_uint(fmaf(c[4 * k + 3], 4096.f, fmaf(c[4 * k + 2], 256.f, fmaf(c[4 * k + 1], 16.f, c[4 * k]))) + 8388608.f);
-                reinterpret_cast<uint32_t *>(row)[r.unit[u]] = finite ? __byte_perm(w[0], w[1], 0x5410) : 0u;
-            } else {
-                uint32_t w[2];
-#pragma unroll
-                for (uint32_t k = 0; k < 2; k++)
-                    w[k] = __byte_perm(__float_as_uint(fmaf(c[4 * k + 1], 256.f, c[4 * k]) + 8388608.f),
-                                       __float_as_uint(fmaf(c[4 * k + 3], 256.f, c[4 * k + 2]) + 8388608.f), 0x5410);
-                reinterpret_cast<uint2 *>(row)[r.unit[u]] = finite ? make_uint2(w[0], w[1]) : make_uint2(0, 0);
-            }
-            if ((threadIdx.x & (lanes - 1)) == 0) {
-                reinterpret_cast<uint32_t *>(row + b.p.codes)[r.unit[u] / lanes] = finite ? sb | Y::bits(low) << 16 : Y::kNan << 16;
+            for (uint32_t u = 0; u < kBatch; u++) {
+                const uint32_t unit = u0 + u * step;
+                if (u && !__any_sync(kFull, unit < r.end)) break;
+                uint2 codes;
+                uint32_t pair;
+                const bool finite = quantise<T, kBits>(in[u], lanes, codes, pair);
+                if (!here || unit >= r.end) continue;
+                if constexpr (kBits == 4) row[unit] = codes.x;
+                else reinterpret_cast<uint2 *>(row)[unit] = codes;
+                if (first) pairs[unit >> glog] = pair;
                 if (!finite) flag(b.status, CG_ERR_NONFINITE);
             }
         }
     }
 }
 
-template <class T, uint32_t kBits, uint32_t kU>
+template <class T, uint32_t kBits>
 __global__ void __launch_bounds__(kThreads) k_quant_read(const Job b) {
     using Y = Type<T>;
-    const Run<kU> r(b);
-    const uint32_t glog = 31 - __clz(b.p.group / 8);
-    for (uint32_t slice = r.slice; slice < r.end; slice++) {
+    constexpr float kTop = (1u << kBits) - 1u;
+    const Run r(b);
+    const bool here = r.at < kOutside, use = here || (b.t.zero && r.at == kOutside);
+    if (!use) return;
+    const uint32_t glog = 31u - __clz(b.p.group / 8), step = 1u << b.llog;
+    for (uint32_t slice = r.slice; slice < r.last; slice++) {
         const uint32_t layer = slice >> 1, kv = slice & 1u;
-        uint16_t *dst = kv ? b.t.v + layer * b.t.vs[0] : b.t.k + layer * b.t.ks[0];
-        const uint64_t stride = kv ? b.t.vs[1] : b.t.ks[1];
-        const uint16_t *pool = b.p.pool + layer * b.p.layer + kv * b.p.kv;
-        uint2 w[kU];
-        uint32_t pair[kU];
+        uint16_t *dst = kv ? b.t.v + layer * b.t.vs[0] + r.j * b.t.vs[1] : b.t.k + layer * b.t.ks[0] + r.j * b.t.ks[1];
+        uint16_t *rest = !kv && b.t.k_rest ? b.t.k_rest + (dst - b.t.k) : nullptr;
+        const uint32_t *row = reinterpret_cast<const uint32_t *>(b.p.pool + layer * b.p.layer + kv * b.p.kv + (here ? r.at : 0));
+        const uint32_t *pairs = row + b.p.codes / 2;
+        for (uint32_t u0 = r.unit; u0 < r.end; u0 += kBatch * step) {
+            uint2 w[kBatch];
+            uint32_t pair[kBatch];
 #pragma unroll
-        for (uint32_t u = 0; u < kU; u++) {
-            w[u] = make_uint2(0, 0);
-            pair[u] = 0;
-            if (r.at[u] < kOutside) {
-                const uint16_t *row = pool + r.at[u];
-                if constexpr (kBits == 4) w[u].x = reinterpret_cast<const uint32_t *>(row)[r.unit[u]];
-                else w[u] = reinterpret_cast<const uint2 *>(row)[r.unit[u]];
-                pair[u] = reinterpret_cast<const uint32_t *>(row + b.p.codes)[r.unit[u] >> glog];
-            }
-        }
-#pragma unroll
-        for (uint32_t u = 0; u < kU; u++) {
-            if (r.at[u] >= kOutside && !(r.at[u] == kOutside && b.t.zero)) continue;
-            const float s = Y::of(pair[u] & 0xFFFFu), low = Y::of(pair[u] >> 16);
-            float x[8], most = -INFINITY;
-#pragma unroll
-            for (uint32_t k = 0; k < 8; k += 2) {
-                uint32_t c[2];
-#pragma unroll
-                for (uint32_t e = 0; e < 2; e++) {  // 2^23 + code
-                    if constexpr (kBits == 4) c[e] = ((w[u].x >> (4 * (k + e))) & 15u) | 0x4B000000u;
-                    else c[e] = __byte_perm(k < 4 ? w[u].x : w[u].y, 0x4B000000u, 0x7440u | ((k + e) & 3u));
-                    x[k + e] = __uint_as_float(c[e]);
+            for (uint32_t u = 0; u < kBatch; u++) {
+                const uint32_t unit = u0 + u * step;
+                w[u] = make_uint2(0, 0);
+                pair[u] = 0;
+                if (here && unit < r.end) {
+                    if constexpr (kBits == 4) w[u].x = row[unit];
+                    else w[u] = reinterpret_cast<const uint2 *>(row)[unit];
+                    pair[u] = pairs[unit >> glog];
                 }
-                add2(x[k], x[k + 1], -8388608.f, -8388608.f);
-                x[k] = fmaf(x[k], s, low), x[k + 1] = fmaf(x[k + 1], s, low);
-                most = fmaxf(most, fmaxf(x[k], x[k + 1]));
             }
-            if (most > Y::kMost)  // past the type's range
 #pragma unroll
-                for (uint32_t k = 0; k < 8; k++) x[k] = x[k] > Y::kMost && x[k] < INFINITY ? Y::kMost : x[k];
-            uint4 o;
-            typename Y::T2 *h = reinterpret_cast<typename Y::T2 *>(&o);
+            for (uint32_t u = 0; u < kBatch; u++) {
+                const uint32_t unit = u0 + u * step;
+                if (unit >= r.end) break;
+                const float s = Y::of(pair[u] & 0xFFFFu), low = Y::of(pair[u] >> 16);
+                float x[8];
+                if constexpr (kBits == 4) {
+                    // codes k and k + 4 in place: 2^23 + code 16^k, less 2^23, times s / 16^k
+                    const uint32_t y[2] = {w[u].x, w[u].x >> 16};
+                    float f = s;
 #pragma unroll
-            for (uint32_t k = 0; k < 4; k++) h[k] = Y::pack(x[2 * k], x[2 * k + 1]);
-            const uint64_t at = r.row[u] * stride + 8 * r.unit[u];
-            *reinterpret_cast<uint4 *>(dst + at) = o;
-            if (b.t.k_rest && !kv) {
+                    for (uint32_t k = 0; k < 4; k++) {
+                        x[k] = __uint_as_float((y[0] & (15u << 4 * k)) | 0x4B000000u);
+                        x[k + 4] = __uint_as_float((y[1] & (15u << 4 * k)) | 0x4B000000u);
+                        add2(x[k], x[k + 4], -8388608.f, -8388608.f);
+                        fma2(x[k], x[k + 4], x[k], x[k + 4], f, low);
+                        f *= 0.0625f;
+                    }
+                } else {
 #pragma unroll
-                for (uint32_t k = 0; k < 4; k++) {
-                    const float2 y = Y::wide(h[k]);
-                    h[k] = Y::pack(x[2 * k] - y.x, x[2 * k + 1] - y.y);
+                    for (uint32_t k = 0; k < 8; k += 2) {
+#pragma unroll
+                        for (uint32_t e = 0; e < 2; e++)
+                            x[k + e] = __uint_as_float(__byte_perm(k < 4 ? w[u].x : w[u].y, 0x4B000000u, 0x7440u | ((k + e) & 3u)));
+                        add2(x[k], x[k + 1], -8388608.f, -8388608.f);
+                        fma2(x[k], x[k + 1], x[k], x[k + 1], s, low);
+                    }
                 }
-                *reinterpret_cast<uint4 *>(b.t.k_rest + at) = o;
+                if (fmaf(kTop, s, low) > Y::kMost)  // some may lie past the type's range
+#pragma unroll
+                    for (uint32_t k = 0; k < 8; k++) x[k] = x[k] > Y::kMost && x[k] < INFINITY ? Y::kMost : x[k];
+                uint4 o;
+                typename Y::T2 *h = reinterpret_cast<typename Y::T2 *>(&o);
+#pragma unroll
+                for (uint32_t k = 0; k < 4; k++) h[k] = Y::pack(x[2 * k], x[2 * k + 1]);
+                *reinterpret_cast<uint4 *>(dst + 8 * unit) = o;
+                if (rest) {
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; k++) {
+                        const float2 y = Y::wide(h[k]);
+                        h[k] = Y::pack(x[2 * k] - y.x, x[2 * k + 1] - y.y);
+                    }
+                    *reinterpret_cast<uint4 *>(rest + 8 * unit) = o;
+                }
             }
         }
     }
 }
 
+// Where the call is short, a warp takes 32 units of K or of V of one layer;
+// otherwise whole rows, in up to eight layers as long as there are warps
+// enough.
 template <class T, uint32_t kBits>
 cudaError_t launch(Job &b, uint32_t n_layers, bool write, cudaStream_t s) {
     b.units = b.p.C / 8;
     b.n_slices = 2 * n_layers;
-    const uint64_t n = (uint64_t)b.t.n_rows * b.units;  // of a layer's K
-    // one unit a thread where the call is short, four where that leaves every SM full; and eight slices a block
-    const bool wide = n * b.n_slices >= 4ull * 152 * 2048;
-    const uint64_t per = (wide ? 4u : 1u) * kThreads, runs = (n + per - 1) / per, full = 152 * 8;
-    b.slices = 8;
-    while (b.slices > 1 && runs * ((b.n_slices + b.slices - 1) / b.slices) < 4 * full) b.slices >>= 1;
-    const uint64_t grid = runs * ((b.n_slices + b.slices - 1) / b.slices);
-    if (grid > 0x7FFFFFFFull) return cudaErrorInvalidValue;
-    b.runs = (uint32_t)runs;
-    if (write) {
-        if (wide) k_quant_write<T, kBits, 4><<<(unsigned)grid, kThreads, 0, s>>>(b);
-        else k_quant_write<T, kBits, 1><<<(unsigned)grid, kThreads, 0, s>>>(b);
-    } else {
-        if (wide) k_quant_read<T, kBits, 4><<<(unsigned)grid, kThreads, 0, s>>>(b);
-        else k_quant_read<T, kBits, 1><<<(unsigned)grid, kThreads, 0, s>>>(b);
-    }
+    b.llog = b.units >= 32 ? 5 : b.units >= 16 ? 4 : 3;
+    const uint64_t groups = ((uint64_t)b.t.n_rows + (32u >> b.llog) - 1) >> (5 - b.llog);
+    const uint32_t steps = (b.units + (1u << b.llog) - 1) >> b.llog;
+    const uint64_t full = 152 * 32;  // warps that fill the SMs
+    b.steps = steps;
+    b.slices = 16;
+    const auto warps = [&] { return groups * ((steps + b.steps - 1) / b.steps) * ((b.n_slices + b.slices - 1) / b.slices); };
+    while (b.slices > 2 && warps() < 2 * full) b.slices >>= 1;
+    if (warps() < full) b.slices = 1;
+    while (b.steps > 1 && warps() < full) b.steps = (b.steps + 1) / 2;
+    while ((b.n_slices + b.slices - 1) / b.slices > 65535u) b.slices <<= 1;
+    b.chunks = (steps + b.steps - 1) / b.steps;
+    const uint64_t runs = (groups * b.chunks + kThreads / 32 - 1) / (kThreads / 32);
+    if (runs > 0x7FFFFFFFull / (kThreads / 32)) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)runs, (b.n_slices + b.slices - 1) / b.slices);
+    if (write) k_quant_write<T, kBits><<<grid, kThreads, 0, s>>>(b);
+    else k_quant_read<T, kBits><<<grid, kThreads, 0, s>>>(b);
     return cudaGetLastError();
 }
 
@@ -347,8 +374,8 @@ cg_status tokens(const cg_pages *p, const cg_quant *f, const cg_token_rows *r, b
         t.ks[k] = r->k_stride[k];
         t.vs[k] = r->v_stride[k];
     }
-    // blocks of at least 256 eight-channel units: the grid must fit
-    if ((uint64_t)r->n_rows * (quant_channels(f) / 8) / kThreads * 2 * r->n_layers > 0x7FFF0000ull) return CG_ERR_INVALID_ARG;
+    // the number of warps must fit: one takes 32 eight-channel units of a row at least
+    if ((uint64_t)r->n_rows * ((quant_channels(f) / 8 + 31) / 32) > 0x7FFF0000ull) return CG_ERR_INVALID_ARG;
     CG_CUDA_TRY(run(quant_pool(p, f, r->layer), t, r->n_layers, f->dtype, f->bits, write, dev_status,
                     static_cast<cudaStream_t>(stream)));
     return CG_OK;
