@@ -168,14 +168,14 @@ def lib() -> ct.CDLL:
         L.cg_pages_fork.argtypes = [PG, P, P, P, U32, P, ct.c_size_t, P, P]
         L.cg_pages_free.argtypes = [PG, P, U32, P, P]
         L.cg_pages_compact.argtypes = [PG, P, P, ct.c_size_t, P, P]
-        L.cg_attend_ws_bytes.argtypes = [PG, ct.POINTER(cg_attention), SZ]
-        L.cg_attend.argtypes = [PG, ct.POINTER(cg_attention), P, ct.c_size_t, P, P]
-        QF, TR = ct.POINTER(cg_quant), ct.POINTER(cg_token_rows)
+        L.cg_attend_ws_bytes.argtypes = [PG, P, SZ]  # a cg_attention, or its bytes
+        L.cg_attend.argtypes = [PG, P, P, ct.c_size_t, P, P]
+        QF = ct.POINTER(cg_quant)
         L.cg_quant_row.argtypes = [QF, ct.POINTER(U32)]
-        L.cg_quant_write.argtypes = [PG, QF, TR, P, P]
-        L.cg_quant_read.argtypes = [PG, QF, TR, P, P]
-        L.cg_quant_attend_ws_bytes.argtypes = [PG, QF, ct.POINTER(cg_attention), SZ]
-        L.cg_quant_attend.argtypes = [PG, QF, ct.POINTER(cg_attention), P, ct.c_size_t, P, P]
+        L.cg_quant_write.argtypes = [PG, QF, P, P, P]  # a cg_token_rows, or its bytes
+        L.cg_quant_read.argtypes = [PG, QF, P, P, P]
+        L.cg_quant_attend_ws_bytes.argtypes = [PG, QF, P, SZ]
+        L.cg_quant_attend.argtypes = [PG, QF, P, P, ct.c_size_t, P, P]
         L.cg_cache_source.argtypes = [P, ct.POINTER(ct.c_int), ct.POINTER(ct.c_void_p)]
         for name in EXPORTS:
             if name not in ("cg_status_string",):

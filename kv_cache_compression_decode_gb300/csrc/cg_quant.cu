@@ -22,6 +22,12 @@ template <> struct Type<__half> {
     static __device__ __forceinline__ float of(uint32_t bits) { return __half2float(__ushort_as_half((uint16_t)bits)); }
     static __device__ __forceinline__ uint32_t bits(float x) { return __half_as_ushort(__float2half_rn(x)); }
     static __device__ __forceinline__ uint32_t bits_up(float x) { return __half_as_ushort(__float2half_ru(x)); }
+    // the two of a word plus z, in fp32
+    static __device__ __forceinline__ void add(float &x, float &y, uint32_t w, float z) {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.rn.f32.f16 %0, a, %3;\n\tadd.rn.f32.f16 %1, b, %3;\n\t}"
+            : "=f"(x), "=f"(y)
+            : "r"(w), "f"(z));
+    }
     static constexpr uint32_t kNan = 0x7E00u;
     static constexpr float kMost = 65504.f;
 };
@@ -33,6 +39,12 @@ template <> struct Type<__nv_bfloat16> {
     static __device__ __forceinline__ float of(uint32_t bits) { return __uint_as_float(bits << 16); }
     static __device__ __forceinline__ uint32_t bits(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
     static __device__ __forceinline__ uint32_t bits_up(float x) { return (__float_as_uint(x) + 0xFFFFu) >> 16; }  // x >= 0
+    // the two of a word plus z, in fp32
+    static __device__ __forceinline__ void add(float &x, float &y, uint32_t w, float z) {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.rn.f32.bf16 %0, a, %3;\n\tadd.rn.f32.bf16 %1, b, %3;\n\t}"
+            : "=f"(x), "=f"(y)
+            : "r"(w), "f"(z));
+    }
     static constexpr uint32_t kNan = 0x7FC0u;
     static constexpr float kMost = 3.3895313892515355e38f;  // (2 - 2^-7) 2^127
 };
@@ -149,18 +161,17 @@ __device__ __forceinline__ bool quantise(const uint4 &in, uint32_t lanes, uint2 
     uint32_t sb = Y::bits_up(d * ((1.f - 0x1p-21f) / kTop));
     if (Y::of(sb) * kTop < d) sb++;
     const float s = Y::of(sb);
-    float inv;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-    if (!sb) inv = 0.f;
+    float inv;  // of 2^-126 at least: with a scale of 0 every x - low is 0, too
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaxf(s, 0x1p-126f)));
     // Codes are the nearest integers to (x - low) / s.  The quotients are off by 2^-22 of themselves at most: a code
-    // that is not near a border is right (and where 1 / s may not be finite, none is trusted).
-    float y[8], c[8], far = s < 0x1p-90f && sb ? 1.f : 0.f;
+    // that is not near a border is right (and with bf16's smallest scales, whose inverse is not, none is trusted).
+    float y[8], c[8], far = 0.f;
+    if constexpr (!__is_same(T, __half)) far = sb && s < 0x1p-90f ? 1.f : 0.f;
+    const uint32_t words[4] = {in.x, in.y, in.z, in.w};
     constexpr float kNear = 0.5f - kTop * 0x1p-20f;
 #pragma unroll
     for (uint32_t k = 0; k < 4; k++) {
-        const float2 x = Y::wide(h[k]);
-        y[2 * k] = x.x, y[2 * k + 1] = x.y;
-        add2(y[2 * k], y[2 * k + 1], -low, -low);
+        Y::add(y[2 * k], y[2 * k + 1], words[k], -low);
         fma2(c[2 * k], c[2 * k + 1], y[2 * k], y[2 * k + 1], inv, kMagic);
         add2(c[2 * k], c[2 * k + 1], -kMagic, -kMagic);
         far = fmaxf(far, fmaxf(fabsf(fmaf(y[2 * k], inv, -c[2 * k])), fabsf(fmaf(y[2 * k + 1], inv, -c[2 * k + 1]))));
@@ -184,7 +195,9 @@ __device__ __forceinline__ bool quantise(const uint4 &in, uint32_t lanes, uint2 
                                __float_as_uint(fmaf(c[4 * k + 3], 256.f, c[4 * k + 2]) + 8388608.f), 0x5410);
         codes = make_uint2(w[0], w[1]);
     }
-    pair = sb | Y::bits(low) << 16;
+    // low as it came: mm holds -low above the largest value
+    const uint32_t both = *reinterpret_cast<const uint32_t *>(&mm);
+    pair = __byte_perm(sb, both ^ 0x80000000u, 0x7610);
     if (!finite) {
         codes = make_uint2(0, 0);
         pair = Y::kNan << 16;
@@ -193,7 +206,7 @@ __device__ __forceinline__ bool quantise(const uint4 &in, uint32_t lanes, uint2 
 }
 
 template <class T, uint32_t kBits>
-__global__ void __launch_bounds__(kThreads) k_quant_write(const Job b) {
+__global__ void __launch_bounds__(kThreads, 4) k_quant_write(const Job b) {
     const Run r(b);
     if (!r.some) return;
     const uint32_t lanes = b.p.group / 8, glog = 31u - __clz(lanes), step = 1u << b.llog;

@@ -25,12 +25,13 @@ from __future__ import annotations
 import ctypes as ct
 import math
 import operator
+import struct
 from typing import Optional, Tuple
 
 import torch
 
 from . import codec
-from .codec import CG_BF16, CG_FP16, Config, _check, cg_attention, cg_pages, cg_quant, cg_token_rows, lib
+from .codec import CG_BF16, CG_FP16, Config, _check, cg_pages, cg_quant, lib
 
 NO_BLOCK = NO_SLOT = -1  # CG_NO_BLOCK / CG_NO_SLOT as int32
 
@@ -38,7 +39,10 @@ _DTYPES = {torch.float16: CG_FP16, torch.bfloat16: CG_BF16}
 
 
 _INT32 = (torch.int32, torch.uint32)
-_Strides, _Two = ct.c_uint64 * 3, ct.c_uint64 * 2
+# The fields of cg_attention and cg_token_rows as the C compiler lays them out: building the ctypes structures took a
+# quarter of a call.
+_pack_attention = struct.Struct("4P9I6Qf4x").pack
+_pack_rows = struct.Struct("5P4I4Q").pack
 # The current stream's handle without building a Stream object around it (3 us of a 7 us call).
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
@@ -246,10 +250,10 @@ class PagedCache:
             raise ValueError("layer, shared_slot and shared_blocks are not negative")
         if R == 0:
             return out
-        a = cg_attention(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
-                         _ids(slots, d, "slots") if slots is not None else None, self._dtype, R, nq, hq,
-                         self._kv_heads(hd), hd, layer, shared_slot, shared_blocks, _Strides(*qs[:3]),
-                         _Strides(*os_[:3]), scale if scale is not None else 1.0 / math.sqrt(hd) if hd else 0.0)
+        a = _pack_attention(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else 0,
+                            _ids(slots, d, "slots") if slots is not None else 0, self._dtype, R, nq, hq,
+                            self._kv_heads(hd), hd, layer, shared_slot, shared_blocks, *qs[:3], *os_[:3],
+                            scale if scale is not None else 1.0 / math.sqrt(hd) if hd else 0.0)
         key = (R, nq, hq, hd, self._shared_key(shared_blocks))
         ws_bytes = self._attn.get(key)
         if ws_bytes is None:
@@ -273,10 +277,10 @@ class PagedCache:
         return shared_blocks > 0  # the workspace does not depend on how many
 
     def _attend_ws_bytes(self, a, n) -> int:
-        return lib().cg_attend_ws_bytes(self._ref, ct.byref(a), ct.byref(n))
+        return lib().cg_attend_ws_bytes(self._ref, a, ct.byref(n))
 
     def _attend(self, a, ws, handle) -> int:
-        return lib().cg_attend(self._ref, ct.byref(a), ws.data_ptr(), ws.numel(), self._status_ptr, handle)
+        return lib().cg_attend(self._ref, a, ws.data_ptr(), ws.numel(), self._status_ptr, handle)
 
 
 class QuantCache(PagedCache):
@@ -300,6 +304,7 @@ class QuantCache(PagedCache):
         self._format = self._format_of(n_kv_heads, head_dim, bits, group, dtype)
         self._fref = ct.byref(self._format)
         self._type, self._dtype, self._heads, self._hd = dtype, _DTYPES[dtype], n_kv_heads, head_dim
+        self._channels, self._n_slots, self._lib = n_kv_heads * head_dim, tables.shape[0], lib()
 
     @staticmethod
     def _format_of(n_kv_heads, head_dim, bits, group, dtype) -> cg_quant:
@@ -330,34 +335,29 @@ class QuantCache(PagedCache):
 
     @property
     def channels(self) -> int:
-        return self._heads * self._hd
+        return self._channels
 
-    def _rows(self, k, v, layer, slots, offsets, start) -> cg_token_rows:
-        C, d = self._heads * self._hd, self._device
-        for t in (k, v):
-            if t.dtype != self._type or t.device != d or t.dim() != 3 or t.shape[2] != C or (C > 1 and t.stride(2) != 1):
-                raise ValueError(f"k and v: tensors [layers][rows][{C}] of {self._type} on {d} with contiguous channels "
-                                 "are wanted")
-        if v.shape != k.shape:
-            raise ValueError("k and v have one shape")
-        if layer < 0:
-            raise ValueError("layer is not negative")
-        n_layers, n_rows, _ = k.shape
+    def _rows(self, k, v, layer, slots, offsets, start) -> bytes:
+        """A cg_token_rows."""
+        d, shape, ks, vs = self._device, k.shape, k.stride(), v.stride()
+        if (k.dtype is not self._type or v.dtype is not self._type or len(shape) != 3 or shape != v.shape
+                or shape[2] != self._channels or ks[2] != 1 or vs[2] != 1 or k.device != d or v.device != d):
+            raise ValueError(f"k and v: two tensors [layers][rows][{self._channels}] of {self._type} on {d} with contiguous "
+                             "channels are wanted")
+        n_slots = self._n_slots
+        n = len(slots) if slots is not None else len(start) if start is not None else n_slots
         if offsets is not None:
-            n = offsets.shape[0] - 1
-            if n < 0:
-                raise ValueError("offsets has an entry per sequence and one more")
-        else:
-            n = slots.shape[0] if slots is not None else start.shape[0] if start is not None else self._tables.shape[0]
-        if (slots is not None and slots.shape[0] != n) or (start is not None and start.shape[0] != n):
-            raise ValueError("slots and start have one entry per sequence, offsets one more")
-        if slots is None and n > self._tables.shape[0]:
-            raise ValueError("more sequences than slots")
-        ks, vs = k.stride(), v.stride()
-        return cg_token_rows(k.data_ptr(), v.data_ptr(), _ids(slots, d, "slots") if slots is not None else None,
-                             _ids(offsets, d, "offsets") if offsets is not None else None,
-                             _ids(start, d, "start") if start is not None else None, n, n_rows, layer, n_layers,
-                             _Two(ks[0], ks[1]), _Two(vs[0], vs[1]))
+            m = len(offsets) - 1
+            if m < 0 or ((slots is not None or start is not None) and n != m):
+                raise ValueError("slots and start have one entry per sequence, offsets one more")
+            n = m
+        if (start is not None and len(start) != n) or (slots is None and n > n_slots) or layer < 0:
+            raise ValueError("slots and start have one entry per sequence, of which there are no more than slots; layer is "
+                             "not negative")
+        return _pack_rows(k.data_ptr(), v.data_ptr(), _ids(slots, d, "slots") if slots is not None else 0,
+                          _ids(offsets, d, "offsets") if offsets is not None else 0,
+                          _ids(start, d, "start") if start is not None else 0, n, shape[1], layer, shape[0], ks[0], ks[1],
+                          vs[0], vs[1])
 
     def write(self, k: torch.Tensor, v: torch.Tensor, layer: int = 0, slots: Optional[torch.Tensor] = None,
               offsets: Optional[torch.Tensor] = None, start: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -367,7 +367,7 @@ class QuantCache(PagedCache):
         (default: an even share); they are its last tokens (advance `lens` first)
         or those from start[r] on."""
         rows = self._rows(k, v, layer, slots, offsets, start)
-        _check(lib().cg_quant_write(self._ref, self._fref, ct.byref(rows), self._status_ptr, self._stream(stream)),
+        _check(self._lib.cg_quant_write(self._ref, self._fref, rows, self._status_ptr, self._stream(stream)),
                "cg_quant_write")
 
     def read(self, layer: int = 0, n_layers: Optional[int] = None, rows: Optional[int] = None,
@@ -380,14 +380,14 @@ class QuantCache(PagedCache):
         if out is None:
             if rows is None or rows < 0:
                 raise ValueError("read: rows or out is wanted")
-            shape = (n_layers if n_layers is not None else 1, rows, self._heads * self._hd)
+            shape = (n_layers if n_layers is not None else 1, rows, self._channels)
             with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self._device)):
                 out = tuple(torch.zeros(shape, dtype=self._type, device=self._device) for _ in range(2))
         k, v = out
         if (n_layers is not None and k.shape[0] != n_layers) or (rows is not None and k.shape[1] != rows):
             raise ValueError("read: n_layers and rows are those of out")
         r = self._rows(k, v, layer, slots, offsets, start)
-        _check(lib().cg_quant_read(self._ref, self._fref, ct.byref(r), self._status_ptr, self._stream(stream)),
+        _check(self._lib.cg_quant_read(self._ref, self._fref, r, self._status_ptr, self._stream(stream)),
                "cg_quant_read")
         return k, v
 
@@ -399,7 +399,7 @@ class QuantCache(PagedCache):
         self._stream(stream)
         if self._type != torch.float16:
             raise ValueError("decode writes fp16: the cache is another type")
-        L, C = self._pool.shape[0], self._heads * self._hd
+        L, C = self._pool.shape[0], self._channels
         if (cfg.L, cfg.C) != (L, C):
             raise ValueError(f"the context has {cfg.L} layers x {cfg.C} channels, the pool {L} x {C}")
         if not 0 <= slot < self._tables.shape[0] or cfg.T > self._tables.shape[1] * self.block_tokens:
@@ -422,8 +422,8 @@ class QuantCache(PagedCache):
         return shared_blocks
 
     def _attend_ws_bytes(self, a, n) -> int:
-        return lib().cg_quant_attend_ws_bytes(self._ref, self._fref, ct.byref(a), ct.byref(n))
+        return lib().cg_quant_attend_ws_bytes(self._ref, self._fref, a, ct.byref(n))
 
     def _attend(self, a, ws, handle) -> int:
-        return lib().cg_quant_attend(self._ref, self._fref, ct.byref(a), ws.data_ptr(), ws.numel(), self._status_ptr,
+        return lib().cg_quant_attend(self._ref, self._fref, a, ws.data_ptr(), ws.numel(), self._status_ptr,
                                      handle)

@@ -865,3 +865,11 @@ def test_python_checks():
         cache.write(x, x, slots=ids(0))
     with pytest.raises(ValueError):
         cache.attend(0, torch.zeros((1, 1, 4, 64), dtype=BF16))
+
+
+def test_packed_arguments_are_laid_out_as_the_structures():
+    want = [C.cg_token_rows(1, 2, 3, 4, 5, 6, 7, 8, 9, (ct.c_uint64 * 2)(10, 11), (ct.c_uint64 * 2)(12, 13)),
+            C.cg_attention(*range(1, 14), (ct.c_uint64 * 3)(14, 15, 16), (ct.c_uint64 * 3)(17, 18, 19), 0.5)]
+    got = [paged._pack_rows(*range(1, 14)), paged._pack_attention(*range(1, 20), 0.5)]
+    for a, b in zip(want, got):
+        assert bytes(a) == b
