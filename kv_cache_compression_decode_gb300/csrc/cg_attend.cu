@@ -748,9 +748,9 @@ __device__ __forceinline__ Runs runs_of(const Args &a, uint32_t r, uint32_t head
     const uint32_t plog = a.clog - a.hlog;  // log2 of the parts of a row
     const uint32_t group = head >> a.hlog, hd = head & (a.nh - 1u);
     const uint32_t rlog = a.rlog, rmask = (1u << rlog) - 1u;
-    const uint32_t nt_sh = a.npt ? tiles_of(a, a.P) : 0, nt_own = len > a.P ? tiles_of(a, len - a.P) : 0;
+    const uint32_t nt_sh = a.npt ? places_of(a, a.P) : 0, nt_own = len > a.P ? places_of(a, len - a.P) : 0;
     const uint64_t total = own + (uint64_t)a.npt * a.ng * nt_sh, n_cta = shares(a, total);
-    // tiles [t0, t0 + nt) of an item are spread over blocks c0..c1
+    // places [t0, t0 + nt) of the list, an item's tiles, are spread over blocks c0..c1
     auto run = [](uint64_t t0, uint32_t nt, uint64_t n, uint64_t all, uint32_t &c0) {
         c0 = (uint32_t)quot((t0 + 1) * n - 1, all);
         return (uint32_t)quot((t0 + nt) * n - 1, all) - c0 + 1;
@@ -769,12 +769,12 @@ __device__ __forceinline__ Runs runs_of(const Args &a, uint32_t r, uint32_t head
     }
     if (len && a.npt) {
         const uint32_t item = (xp >> rlog) * a.ng + group;
-        o.n_sh = run(own + (uint64_t)item * nt_sh, nt_sh, n_cta, total, c0) << plog;
+        o.n_sh = run(own + (uint64_t)item * nt_sh + a.over, nt_sh - a.over, n_cta, total, c0) << plog;
         o.sh = a.part0 + (((c0 + a.R * a.rt * a.ng + item) << a.clog) + hd) * a.piece_rows + (xp & rmask);
     }
     if (nt_own) {
         const uint32_t item = (x0 >> rlog) * a.ng + group;
-        o.n_own = run(first + (uint64_t)item * nt_own, nt_own, n_cta, total, c0) << plog;
+        o.n_own = run(first + (uint64_t)item * nt_own + a.over, nt_own - a.over, n_cta, total, c0) << plog;
         o.own = a.part0 + (((c0 + r * a.rt * a.ng + item) << a.clog) + hd) * a.piece_rows + (x0 & rmask);
     }
     o.n = o.n_tc + o.n_sh + o.n_own;

@@ -26,6 +26,7 @@ struct Args {
     uint32_t hlog, clog;     // log2 of nh, and of the warp columns of a block: a column has a head, or part of its tokens
     uint32_t tlog;           // log2 of the tokens of a tile
     uint32_t rlog;           // log2 of an item's rows
+    uint32_t over;           // what a piece's beginning and end cost, in tiles: an item is dealt as that many tiles more
     uint32_t rt;             // items' row ranges of a request
     uint32_t npt;            // row ranges of the whole batch over the shared tokens in the row kernel (0: k_shared has them)
     uint32_t pairs;          // k_shared: pairs of 128-row tiles of the whole batch (0: the row kernel has the shared part)
@@ -69,18 +70,22 @@ __device__ __forceinline__ uint32_t tokens_of(const Args &a, uint32_t r, bool *b
 __device__ __forceinline__ uint32_t tiles_of(const Args &a, uint32_t tokens) {
     return (tokens + (1u << a.tlog) - 1u) >> a.tlog;
 }
+// Places on the work list that an item of `tokens` tokens takes.
+__device__ __forceinline__ uint32_t places_of(const Args &a, uint32_t tokens) {
+    return tokens ? tiles_of(a, tokens) + a.over : 0u;
+}
 // Blocks that a list of `total` tiles is dealt to: two tiles each at least.
 __device__ __forceinline__ uint64_t shares(const Args &a, uint64_t total) {
     return min((uint64_t)a.n_cta, (total + 1) / 2);
 }
 
 // Work list: for each request its row ranges x head groups ("items"), each as
-// long as the request's own tokens, then the items of the shared part.  Block
-// c of n takes tiles [c T / n, (c + 1) T / n) of the whole list, so every
-// block has the same share whatever the lengths are (n <= T: no block between
-// two others is left without a tile).  A block's run of tiles of one item is a
-// piece; its slot c + item is unique, since along the list each new piece has
-// a larger block or a larger item.
+// long as the request's own tokens, then the items of the shared part.  An item
+// has a.over places before those of its tiles.  Block c of n takes places
+// [c T / n, (c + 1) T / n) of the whole list, so every block has the same share
+// whatever the lengths are.  A block's run of tiles of one item is a piece; its
+// slot c + item is unique, since along the list each new piece has a larger
+// block or a larger item.
 struct Piece {
     uint32_t r;        // request; R: the shared part
     uint32_t item;     // number of the item
@@ -102,35 +107,40 @@ __device__ __forceinline__ uint64_t quot(uint64_t x, uint64_t y) {
 }
 
 __device__ __forceinline__ bool next_piece(const Args &a, Walk &w, Piece &p) {
-    if (w.t >= w.end) return false;
-    bool bad = false;
-    uint32_t nt = 0, len = 0;
-    while (w.r < a.R) {
-        len = w.lens ? w.lens[w.r] : tokens_of(a, w.r, &bad);
-        nt = len > a.P ? tiles_of(a, len - a.P) : 0;
-        const uint64_t all = (uint64_t)nt * a.rt * a.ng;
-        if (w.t < w.base + all) break;
-        w.base += all;
-        w.r++;
+    for (;;) {
+        if (w.t >= w.end) return false;
+        bool bad = false;
+        uint32_t nt = 0, len = 0;  // places of an item of request r
+        while (w.r < a.R) {
+            len = w.lens ? w.lens[w.r] : tokens_of(a, w.r, &bad);
+            nt = len > a.P ? places_of(a, len - a.P) : 0;
+            const uint64_t all = (uint64_t)nt * a.rt * a.ng;
+            if (w.t < w.base + all) break;
+            w.base += all;
+            w.r++;
+        }
+        p.r = w.r;
+        if (w.r == a.R) {
+            len = a.P;
+            nt = places_of(a, a.P);
+        }
+        if (nt == 0) return false;  // this and the next: lengths that changed under the call leave places over
+        const uint64_t at = w.t - w.base;
+        const uint32_t local = (uint32_t)quot(at, nt);
+        if (w.r == a.R && local >= a.npt * a.ng) return false;
+        p.item = w.r * a.rt * a.ng + local;
+        p.range = local / a.ng;
+        p.group = local - p.range * a.ng;
+        const uint32_t from = (uint32_t)(at - (uint64_t)local * nt);
+        const uint32_t to = from + (uint32_t)min((uint64_t)(nt - from), w.end - w.t);
+        w.t += to - from;
+        if (to <= a.over) continue;  // none of the item's tiles
+        p.tile0 = max(from, a.over) - a.over;
+        p.n = to - a.over - p.tile0;
+        p.of = nt - a.over;
+        p.len = len;
+        return true;
     }
-    p.r = w.r;
-    if (w.r == a.R) {
-        len = a.P;
-        nt = tiles_of(a, a.P);
-    }
-    if (nt == 0) return false;  // this and the next: lengths that changed under the call leave tiles over
-    const uint64_t at = w.t - w.base;
-    const uint32_t local = (uint32_t)quot(at, nt);
-    if (w.r == a.R && local >= a.npt * a.ng) return false;
-    p.item = w.r * a.rt * a.ng + local;
-    p.range = local / a.ng;
-    p.group = local - p.range * a.ng;
-    p.tile0 = (uint32_t)(at - (uint64_t)local * nt);
-    p.n = (uint32_t)min((uint64_t)(nt - p.tile0), w.end - w.t);
-    p.of = nt;
-    p.len = len;
-    w.t += p.n;
-    return true;
 }
 
 // This block's share of the work list, found by all of its kThreads threads:
@@ -150,7 +160,7 @@ __device__ __forceinline__ Walk take_share(const Args &a, uint64_t *misc, uint32
         const uint32_t n = tokens_of(a, r, &bad);
         if (keep) lens[r] = n;
         if (blockIdx.x == 0) a.tokens[r] = n;
-        mine += (uint64_t)(n > a.P ? tiles_of(a, n - a.P) : 0) * a.rt * a.ng;
+        mine += (uint64_t)(n > a.P ? places_of(a, n - a.P) : 0) * a.rt * a.ng;
     }
     if (bad && blockIdx.x == 0) flag(a.status, CG_ERR_RANGE);
     uint64_t inc = mine;
@@ -165,13 +175,13 @@ __device__ __forceinline__ Walk take_share(const Args &a, uint64_t *misc, uint32
         if (k < warp) before += misc[k];
         own += misc[k];
     }
-    const uint64_t total = own + (uint64_t)a.npt * a.ng * tiles_of(a, a.P);
+    const uint64_t total = own + (uint64_t)a.npt * a.ng * places_of(a, a.P);
     if (blockIdx.x == 0) {
         uint64_t at = before;
         for (uint32_t r = r0; r < r1; r++) {
             a.cum[r] = at;
             const uint32_t n = a.tokens[r];  // this thread's own write
-            at += (uint64_t)(n > a.P ? tiles_of(a, n - a.P) : 0) * a.rt * a.ng;
+            at += (uint64_t)(n > a.P ? places_of(a, n - a.P) : 0) * a.rt * a.ng;
         }
         if (tid == 0) a.cum[a.R] = own;
     }

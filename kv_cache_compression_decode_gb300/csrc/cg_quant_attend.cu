@@ -127,6 +127,7 @@ extern "C" cg_status cg_quant_attend(const cg_pages *p, const cg_quant *f, const
     a.clog = 3;
     a.tlog = (uint32_t)__builtin_ctz(pl.tt);
     a.rlog = pl.kN == 1 ? 3 : 4;
+    a.over = 3;
     a.rt = pl.rt;
     a.npt = pl.npt;
     a.pairs = pl.pairs;

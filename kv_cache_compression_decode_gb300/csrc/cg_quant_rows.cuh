@@ -223,10 +223,32 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
     const uint32_t at_k = tile0 + tk * 128 + ((inner + c * kQuarter) ^ (tk << 4));
     const uint32_t at_v0 = tile0 + qa.tile + t0 * 128 + ((inner + r * kEighth) ^ (t0 << 4));
     const uint32_t at_v1 = tile0 + qa.tile + t1 * 128 + ((inner + r * kEighth) ^ (t1 << 4));
+    // The queries of a piece, as they lie in memory, and how many of the item's tokens this lane's rows see.  They are
+    // fetched before the results of the piece before it go out.
+    uint4 raw[kN][D / 32];
+    uint32_t sees[kN];
+    auto fetch_queries = [&]() {
+        const uint32_t head = p.group * a.nh + hd, own = p.r == a.R ? a.P : p.len - a.P;
+#pragma unroll
+        for (uint32_t n = 0; n < kN; n++) {
+            const Row o = row_of(a, p, (p.range << a.rlog) + 8 * n + r, head < a.Hkv ? head : 0u);
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + o.r * a.qs[0] + o.i * a.qs[1] + o.h * a.qs[2]);
+#pragma unroll
+            for (uint32_t g = 0; g < NG; g++)
+#pragma unroll
+                for (uint32_t e = 0; e < G / 32; e++)
+                    raw[n][g * (G / 32) + e] = o.valid ? src[g * (G / 8) + c * (G / 32) + e] : make_uint4(0, 0, 0, 0);
+            sees[n] = own;
+            if (p.r != a.R) {
+                const uint32_t y = p.len + 1 + o.i;
+                sees[n] = y > a.nq + a.P ? min(y - a.nq - a.P, own) : 0u;
+            }
+        }
+    };
     bool ok = true, more = next_piece(a, w, p);
+    if (more) fetch_queries();
     while (more) {
         const bool shared = p.r == a.R, active = p.group * a.nh + hd < a.Hkv;
-        const uint32_t head = p.group * a.nh + hd, row0 = p.range << a.rlog;
         const uint32_t own_tokens = shared ? a.P : p.len - a.P;
         const uint32_t pair0 = sm + 2 * qa.tile + ((p.group * a.nh * NG * 4) & 15u) + hd * NG * 4 + (part * kTok + tk) * qa.pw;
         uint32_t least = own_tokens;
@@ -239,18 +261,10 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
         float fq[kN][2];
 #pragma unroll
         for (uint32_t n = 0; n < kN; n++) {
-            const Row o = row_of(a, p, row0 + 8 * n + r, active ? head : 0u);
-            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + o.r * a.qs[0] + o.i * a.qs[1] + o.h * a.qs[2]);
-            uint4 raw[D / 32];
-#pragma unroll
-            for (uint32_t g = 0; g < NG; g++)
-#pragma unroll
-                for (uint32_t e = 0; e < G / 32; e++)
-                    raw[g * (G / 32) + e] = o.valid ? src[g * (G / 8) + c * (G / 32) + e] : make_uint4(0, 0, 0, 0);
             float x[D / 4], mx = 0.f;
 #pragma unroll
             for (uint32_t e = 0; e < D / 32; e++) {
-                const uint32_t v[4] = {raw[e].x, raw[e].y, raw[e].z, raw[e].w};
+                const uint32_t v[4] = {raw[n][e].x, raw[n][e].y, raw[n][e].z, raw[n][e].w};
 #pragma unroll
                 for (uint32_t k = 0; k < 4; k++) {
                     const float2 y = Half<T>::unpack(v[k]);
@@ -292,16 +306,11 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
             }
             // what this lane's columns need, from the lanes that have the row
             const float f = qa.scale2 * power2(24 - up);
-            uint32_t l = own_tokens;
-            if (!shared) {
-                const uint32_t sees = p.len + 1 + o.i;
-                l = sees > a.nq + a.P ? min(sees - a.nq - a.P, own_tokens) : 0u;
-            }
 #pragma unroll
             for (uint32_t j = 0; j < 2; j++) {
                 const uint32_t from = (2 * c + j) * 4;
                 fq[n][j] = __shfl_sync(kFull, f, from);
-                lim[n][j] = __shfl_sync(kFull, l, from);
+                lim[n][j] = __shfl_sync(kFull, sees[n], from);
             }
         }
 
@@ -564,9 +573,13 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
             step();
         }
 
+        const Piece done = p;
+        more = next_piece(a, w, p);
+        if (more) fetch_queries();
         if (active) {
-            const bool answer = a.P == 0 && a.hlog == a.clog && p.n == p.of;  // the whole sequence
-            const uint64_t slot = a.part0 + ((((uint64_t)blockIdx.x + p.item) << a.clog) + warp) * a.piece_rows;
+            const bool answer = a.P == 0 && a.hlog == a.clog && done.n == done.of;  // the whole sequence
+            const uint64_t slot = a.part0 + ((((uint64_t)blockIdx.x + done.item) << a.clog) + warp) * a.piece_rows;
+            const uint32_t head = done.group * a.nh + hd, row0 = done.range << a.rlog;
 #pragma unroll
             for (uint32_t n = 0; n < kN; n++)
 #pragma unroll
@@ -581,7 +594,7 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                         for (uint32_t g = 0; g < NG; g++) low[g] += __shfl_xor_sync(kFull, low[g], d);
                     }
                     const uint32_t x = 8 * n + 2 * c + j;
-                    const Row row = row_of(a, p, row0 + x, head);
+                    const Row row = row_of(a, done, row0 + x, head);
                     if (!row.valid) continue;
                     const float inv = !answer ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
                     float *part_o = a.part_o + (slot + x) * D;
@@ -616,7 +629,6 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                     }
                 }
         }
-        more = next_piece(a, w, p);
     }
     if (!ok && lane == 0) flag_why(a.status, CG_ERR_TIMEOUT, kWhyWait);
 }
