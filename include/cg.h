@@ -660,9 +660,12 @@ cg_status cg_quant_read(const cg_pages *p, const cg_quant *f, const cg_token_row
  * below 2^-25 of a query's largest channel, and scales, low values, softmax
  * sums and outputs are applied and accumulated in fp32.  The product of a
  * weight and a scale is rounded to 11 bits for the product with V's codes (one
- * above 2^-30 of the largest is not lost).  The shared blocks of more query rows than
- * a batch of single tokens has (see cg_quant_attend_ws_bytes) are first read into the
- * workspace as cg_quant_read would read them, and attended to as by cg_attend.
+ * above 2^-28 of the largest is not lost).  The shared blocks of many query
+ * rows (more than 64 to a KV head, and a few thousand tokens) are first read
+ * into the workspace, as cg_quant_read would read them, with bf16 in two parts
+ * for K, and attended to as by cg_attend.
+ * ws: device, 256-byte aligned, cg_quant_attend_ws_bytes bytes, which depend
+ * on shared_blocks too.
  */
 cg_status cg_quant_attend_ws_bytes(const cg_pages *p, const cg_quant *f, const cg_attention *a, size_t *ws_bytes);
 cg_status cg_quant_attend(const cg_pages *p, const cg_quant *f, const cg_attention *a, void *ws, size_t ws_bytes,

@@ -172,10 +172,10 @@ def lib() -> ct.CDLL:
         L.cg_attend.argtypes = [PG, P, P, ct.c_size_t, P, P]
         QF = ct.POINTER(cg_quant)
         L.cg_quant_row.argtypes = [QF, ct.POINTER(U32)]
-        L.cg_quant_write.argtypes = [PG, QF, P, P, P]  # a cg_token_rows, or its bytes
-        L.cg_quant_read.argtypes = [PG, QF, P, P, P]
-        L.cg_quant_attend_ws_bytes.argtypes = [PG, QF, P, SZ]
-        L.cg_quant_attend.argtypes = [PG, QF, P, P, ct.c_size_t, P, P]
+        # cg_pages, cg_quant, then cg_token_rows or cg_attention: references, addresses or bytes
+        L.cg_quant_write.argtypes = L.cg_quant_read.argtypes = [P, P, P, P, P]
+        L.cg_quant_attend_ws_bytes.argtypes = [P, P, P, SZ]
+        L.cg_quant_attend.argtypes = [P, P, P, P, ct.c_size_t, P, P]
         L.cg_cache_source.argtypes = [P, ct.POINTER(ct.c_int), ct.POINTER(ct.c_void_p)]
         for name in EXPORTS:
             if name not in ("cg_status_string",):

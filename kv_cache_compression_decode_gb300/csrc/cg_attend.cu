@@ -444,6 +444,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
             const uint32_t rows_log = min(a.bshift, 6u), rows = 1u << rows_log, boxes = kTcTok >> rows_log;
             const uint32_t *row = a.tables ? a.tables + (uint64_t)a.shared_slot * a.n_blocks : nullptr;
             uint32_t cnt = 0;
+            if (a.after) {  // the kernel before this one makes what is fetched
+                wait_for_previous();
+                asm volatile("fence.proxy.async.global;" ::: "memory");
+            }
             auto fetch = [&](uint32_t tile, uint32_t kv, uint32_t head) {
                 if (!ok) return;
                 const uint32_t st = cnt % kTcSlots;
@@ -1083,7 +1087,7 @@ cudaError_t shared(const CUtensorMap &map, Args &a, int sms, cudaStream_t s) {
     const uint64_t most = items * ((of + least - 1) / least), sm = (uint64_t)sms < kMaxTcCtas ? sms : kMaxTcCtas;
     const uint64_t n = sm < most ? sm : most, k = n / items;
     a.n_tc = (uint32_t)(k && (of + k - 1) / k <= items * of / n + kCross ? k * items : n);
-    return launch_next(k_shared<T, D>, a.n_tc, kTcThreads, TcSmem<D>::kBytes, s, false, map, a);
+    return launch_next(k_shared<T, D>, a.n_tc, kTcThreads, TcSmem<D>::kBytes, s, a.after != 0, map, a);
 }
 
 template <class T, uint32_t D>

@@ -32,6 +32,7 @@ struct Args {
     uint32_t pairs;          // k_shared: pairs of 128-row tiles of the whole batch (0: the row kernel has the shared part)
     uint32_t one;            // k_shared: the batch fits one 128-row tile
     uint32_t n_tc;           // blocks of k_shared
+    uint32_t after;          // k_shared: its K and V are made by the kernel before it, which lets it start early
     uint32_t split;          // k_shared: K is the sum of the map's matrices 0 and 2
     uint32_t merge_rows;     // rows of a warp of the joins
     uint32_t n_cta;          // blocks of the row kernel

@@ -6,6 +6,7 @@
 // value by exchange, so that a row is read once and its codes go out in runs of
 // 128 or 256 bytes a warp.
 #include "cg_async.cuh"
+#include "cg_launch.cuh"
 #include "cg_quant.cuh"
 
 namespace cg {
@@ -244,6 +245,7 @@ template <class T, uint32_t kBits>
 __global__ void __launch_bounds__(kThreads) k_quant_read(const Job b) {
     using Y = Type<T>;
     constexpr float kTop = (1u << kBits) - 1u;
+    let_next_start();
     const Run r(b);
     const bool here = r.at < kOutside, use = here || (b.t.zero && r.at == kOutside);
     if (!use) return;

@@ -12,8 +12,15 @@ namespace {
 
 bool misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1u)) != 0; }
 
-// Query rows per KV head from which the shared blocks go through the workspace.
-constexpr uint64_t kWorkspaceRows = 65;
+// Whether the shared blocks go through the workspace, by the row ranges that k_quant_rows would take over them (of 8 query
+// rows of a KV head, or of 16, which cost half as much again) and the tokens.  Microseconds a call, through the workspace /
+// in k_quant_rows, fp16, 8 KV heads: 2048 shared tokens, 64 rows 29 / 25, 128 rows 26 / 25; 8192 tokens, 64 rows 36 / 38,
+// 96 rows 33 / 43; 32768 tokens, 48 rows 87 / 70, 64 rows 90 / 93, 128 rows 86 / 160.  The workspace costs two launches
+// and about the time of eight ranges.
+bool by_workspace(uint64_t ranges, uint32_t kN, uint64_t tokens, uint32_t heads) {
+    const uint64_t half = ranges * (kN == 1 ? 2 : 3);
+    return half > 16 && (half - 16) * tokens * heads > 160000;
+}
 constexpr uint32_t kStageBytes = 214u << 10;  // shared memory for an SM's tiles in flight
 
 struct Plan {
@@ -38,13 +45,13 @@ bool make_plan(const cg_pages *p, const cg_quant *f, const cg_attention *a, Plan
     o->nh = 1u << o->hlog;
     o->ng = (Hkv + o->nh - 1) / o->nh;
     o->tt = quant_tok(f->bits, f->head_dim) * (kQuantWarps >> o->hlog);
-    const bool tc = a->shared_blocks && all >= kWorkspaceRows;
+    o->kN = per > 8 ? 2 : 1;
+    const uint32_t range = 8 * o->kN;
+    const bool tc = a->shared_blocks && by_workspace((all + range - 1) / range, o->kN, (uint64_t)a->shared_blocks * p->block_tokens, Hkv);
     o->pairs = tc ? (uint32_t)((all + 255) / 256) : 0;
     o->one = all <= 128;
     const bool here = a->shared_blocks && !tc;  // the shared part goes through k_quant_rows too
     const uint64_t most = here ? all : per;
-    o->kN = per > 8 ? 2 : 1;
-    const uint32_t range = 8 * o->kN;
     o->rt = (uint32_t)((per + range - 1) / range);
     o->npt = here ? (uint32_t)((all + range - 1) / range) : 0;
     o->piece_rows = (uint32_t)(most < range ? most : range);
@@ -173,6 +180,7 @@ extern "C" cg_status cg_quant_attend(const cg_pages *p, const cg_quant *f, const
         b.tables = nullptr;
         b.n_pool = at->shared_blocks;
         b.split = pl.copies == 3;
+        b.after = 1;
         CG_CUDA_TRY(launch_shared(at->dtype, at->head_dim, map, b, sms, s));
         a.n_tc = b.n_tc;
     }

@@ -55,6 +55,11 @@ def _ids(t: torch.Tensor, device: torch.device, what: str) -> int:
     return t.data_ptr()
 
 
+def _stride3(t: torch.Tensor) -> tuple:
+    s = t.stride()
+    return s if len(s) == 3 else (0, 0, 0)
+
+
 def _fixed(name: str) -> property:
     """A tensor whose address the library has: another one may not take its
     place (`cache.lens = cache.lens + 1` would leave the calls with the old
@@ -302,7 +307,7 @@ class QuantCache(PagedCache):
                              f"not {pool.shape[4]}")
         super().__init__(pool, tables, lens, refs, status)
         self._format = self._format_of(n_kv_heads, head_dim, bits, group, dtype)
-        self._fref = ct.byref(self._format)
+        self._at, self._format_at = ct.addressof(self._c), ct.addressof(self._format)
         self._type, self._dtype, self._heads, self._hd = dtype, _DTYPES[dtype], n_kv_heads, head_dim
         self._channels, self._n_slots, self._lib = n_kv_heads * head_dim, tables.shape[0], lib()
 
@@ -339,25 +344,28 @@ class QuantCache(PagedCache):
 
     def _rows(self, k, v, layer, slots, offsets, start) -> bytes:
         """A cg_token_rows."""
-        d, shape, ks, vs = self._device, k.shape, k.stride(), v.stride()
-        if (k.dtype is not self._type or v.dtype is not self._type or len(shape) != 3 or shape != v.shape
-                or shape[2] != self._channels or ks[2] != 1 or vs[2] != 1 or k.device != d or v.device != d):
+        d, shape, (k0, k1, k2), (v0, v1, v2) = self._device, k.shape, _stride3(k), _stride3(v)
+        n_layers, n_rows, C = shape if len(shape) == 3 else (0, 0, 0)
+        if (k.dtype is not self._type or v.dtype is not self._type or shape != v.shape or C != self._channels
+                or k2 != 1 or v2 != 1 or k.device != d or v.device != d):
             raise ValueError(f"k and v: two tensors [layers][rows][{self._channels}] of {self._type} on {d} with contiguous "
                              "channels are wanted")
-        n_slots = self._n_slots
-        n = len(slots) if slots is not None else len(start) if start is not None else n_slots
+        n, s, o, b = self._n_slots, 0, 0, 0
+        if slots is not None:
+            n, s = slots.shape[0], _ids(slots, d, "slots")
         if offsets is not None:
-            m = len(offsets) - 1
-            if m < 0 or ((slots is not None or start is not None) and n != m):
-                raise ValueError("slots and start have one entry per sequence, offsets one more")
+            m, o = offsets.shape[0] - 1, _ids(offsets, d, "offsets")
+            if m < 0 or (slots is not None and n != m):
+                raise ValueError("slots has one entry per sequence, offsets one more")
             n = m
-        if (start is not None and len(start) != n) or (slots is None and n > n_slots) or layer < 0:
-            raise ValueError("slots and start have one entry per sequence, of which there are no more than slots; layer is "
-                             "not negative")
-        return _pack_rows(k.data_ptr(), v.data_ptr(), _ids(slots, d, "slots") if slots is not None else 0,
-                          _ids(offsets, d, "offsets") if offsets is not None else 0,
-                          _ids(start, d, "start") if start is not None else 0, n, shape[1], layer, shape[0], ks[0], ks[1],
-                          vs[0], vs[1])
+        if start is not None:
+            m, b = start.shape[0], _ids(start, d, "start")
+            if (slots is not None or offsets is not None) and n != m:
+                raise ValueError("start has one entry per sequence")
+            n = m
+        if layer < 0 or (slots is None and n > self._n_slots):
+            raise ValueError("layer is negative, or there are more sequences than slots")
+        return _pack_rows(k.data_ptr(), v.data_ptr(), s, o, b, n, n_rows, layer, n_layers, k0, k1, v0, v1)
 
     def write(self, k: torch.Tensor, v: torch.Tensor, layer: int = 0, slots: Optional[torch.Tensor] = None,
               offsets: Optional[torch.Tensor] = None, start: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -367,7 +375,7 @@ class QuantCache(PagedCache):
         (default: an even share); they are its last tokens (advance `lens` first)
         or those from start[r] on."""
         rows = self._rows(k, v, layer, slots, offsets, start)
-        _check(self._lib.cg_quant_write(self._ref, self._fref, rows, self._status_ptr, self._stream(stream)),
+        _check(self._lib.cg_quant_write(self._at, self._format_at, rows, self._status_ptr, self._stream(stream)),
                "cg_quant_write")
 
     def read(self, layer: int = 0, n_layers: Optional[int] = None, rows: Optional[int] = None,
@@ -387,7 +395,7 @@ class QuantCache(PagedCache):
         if (n_layers is not None and k.shape[0] != n_layers) or (rows is not None and k.shape[1] != rows):
             raise ValueError("read: n_layers and rows are those of out")
         r = self._rows(k, v, layer, slots, offsets, start)
-        _check(self._lib.cg_quant_read(self._ref, self._fref, r, self._status_ptr, self._stream(stream)),
+        _check(self._lib.cg_quant_read(self._at, self._format_at, r, self._status_ptr, self._stream(stream)),
                "cg_quant_read")
         return k, v
 
@@ -422,8 +430,8 @@ class QuantCache(PagedCache):
         return shared_blocks
 
     def _attend_ws_bytes(self, a, n) -> int:
-        return lib().cg_quant_attend_ws_bytes(self._ref, self._fref, a, ct.byref(n))
+        return lib().cg_quant_attend_ws_bytes(self._at, self._format_at, a, ct.byref(n))
 
     def _attend(self, a, ws, handle) -> int:
-        return lib().cg_quant_attend(self._ref, self._fref, a, ws.data_ptr(), ws.numel(), self._status_ptr,
+        return lib().cg_quant_attend(self._at, self._format_at, a, ws.data_ptr(), ws.numel(), self._status_ptr,
                                      handle)

@@ -492,6 +492,18 @@ def test_batches_over_a_long_context(R, nq, Hq, D, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [FP16, BF16])
+@pytest.mark.parametrize("R,g,bits,group", [(8, 8, 4, 128), (16, 8, 4, 32), (30, 4, 8, 64), (40, 8, 4, 64)])
+def test_query_rows_around_one_tile_over_thousands_of_shared_tokens(dtype, R, g, bits, group):
+    """64 to 320 rows of two KV heads on 6000 tokens: k_quant_rows, and through the workspace in one and in two tiles."""
+    lens = [6016 + 1 + 3 * r for r in range(R)]
+    cache, slots = make(lens, 6016 // 32, 32, 2, 128, bits, group, dtype, seed=R)
+    q, out, lse = attend(cache, slots, Hq=2 * g, shared_blocks=6016 // 32)
+    cache.check()
+    check(cache, q, out, lse, slots, 1, 128 ** -0.5, 6016 // 32)
+
+
+@gpu
 @pytest.mark.parametrize("Hkv,g,nq", [(4, 8, 1), (8, 8, 4), (12, 1, 1), (5, 5, 2), (6, 5, 2), (32, 1, 1), (9, 3, 7)])
 @pytest.mark.parametrize("D,shared", [(128, 0), (128, 9), (64, 0), (64, 9)])
 def test_groups_of_heads(Hkv, g, nq, D, shared):
