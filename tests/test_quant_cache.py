@@ -757,6 +757,21 @@ def test_a_decoded_context_is_forked_and_continued(bits, group):
         other.copy(_ints([0]), _ints([0]), source=paged.QuantCache.empty(L, 10, bt, Hkv, D, 1, 5, bits, group, dtype=BF16))
 
 
+@gpu
+@pytest.mark.parametrize("bits", [4, 8])
+def test_the_example_on_a_quantised_pool(bits):
+    """After 2 x 5 steps, a free and a compaction, the last step's outputs are the formula's over the codes as they are."""
+    from examples import shared_prefix
+
+    cache, slots, q, out = shared_prefix.run(layers=2, context=333, kv_heads=2, q_heads=8, head_dim=64, block_tokens=16,
+                                             requests=6, steps=5, bits=bits, log=lambda s: None)
+    assert [cache.lens.tolist()[s] for s in slots.tolist()] == [343] * 3 and cache._format.bits == bits
+    for layer in range(2):
+        _, again, lse = attend(cache, slots, q=q[layer], layer=layer, shared_blocks=333 // 16)
+        assert torch.equal(again, out[layer])
+        check(cache, q[layer], out[layer], lse, slots, layer, 0.125, 333 // 16)
+
+
 # ---------------------------------------------------------------------------
 # Refusals on the host
 # ---------------------------------------------------------------------------
