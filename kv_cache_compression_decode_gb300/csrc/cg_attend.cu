@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __
         fence_bar_init();
     }
     uint32_t *lens = reinterpret_cast<uint32_t *>(smem + S::oLens);
-    Walk w = take_share<S::kThreads>(a, misc, lens, S::kLens);
+    Walk w = take_share<S::kThreads, false>(a, misc, lens, S::kLens);
 
     const uint32_t tt = 1u << a.tlog;                 // tokens of a tile
     const uint32_t head_bytes = tt * D * 2, half_bytes = tt * 128;
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __
         const bool mine_box = kv < 2;
         const uint32_t dst0 = sm + kv * S::kTile + head * head_bytes + half * half_bytes + (sub << rlog) * 128;
         bool ok = true;
-        while (ok && next_piece(a, w, p)) {
+        while (ok && next_piece<false>(a, w, p)) {
             const bool shared = p.r == a.R;
             const uint32_t slot = shared ? a.shared_slot : a.slots ? a.slots[p.r] : p.r;
             const uint32_t *row = a.tables + (uint64_t)slot * a.n_blocks;
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __
             }
         }
     };
-    bool more = next_piece(a, w, p);
+    bool more = next_piece<false>(a, w, p);
     if (more) begin();
     while (more) {
         if (a.flip)
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(Smem<D, kR>::kThreads, 3 - kR) k_rows(const __
                 if (qd == 0) a.part_ml[at] = make_float2(m[e], l[e]);
             }
         }
-        more = next_piece(a, w, p);
+        more = next_piece<false>(a, w, p);
         if (more) begin();
     }
     if (!ok && lane == 0) flag_why(a.status, CG_ERR_TIMEOUT, kWhyWait);
@@ -395,7 +395,8 @@ struct TcWalk {
     }
 };
 
-template <class T, uint32_t D>
+// kSplit: K is the sum of the map's matrices 0 and 2, a tile of each in turn.
+template <class T, uint32_t D, bool kSplit>
 __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant__ CUtensorMap map, const Args a) {
     using M = TcSmem<D>;
     constexpr bool kBf16 = sizeof(T) == 2 && !__is_same(T, __half);
@@ -476,7 +477,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
                 const uint32_t ahead = a.one ? 2 : 1;  // score tiles fetched before the first V
                 auto fetch_k = [&](uint32_t tile) {
                     fetch(tile, 0, p.head);
-                    if (a.split) fetch(tile, 2, p.head);
+                    if constexpr (kSplit) fetch(tile, 2, p.head);
                 };
                 for (uint32_t k = 0; k < ahead && k < p.n; k++) fetch_k(p.tile0 + k);
                 for (uint32_t k = 0; k < p.n; k++) {
@@ -496,13 +497,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
                 if (ok) ok = __all_sync(kFull, bar_wait(full + 8 * (c % kTcSlots), (c / kTcSlots) & 1u));
                 tc_fence_after();
             };
-            // scores of stream s from the K in slot c (with split, and in the next)
+            // scores of stream s from the K in slot c (kSplit: and in the next)
             auto qk = [&](uint32_t s, uint32_t c) {
                 if (!ok) return;
                 const uint32_t q = mma_desc(sm + M::oQ + (a.one ? 0 : s) * M::kTile, true, 0);
-                for (uint32_t y = 0; y <= a.split; y++) {
+#pragma unroll
+                for (uint32_t y = 0; y <= (kSplit ? 1u : 0u); y++) {
                     const uint32_t k = mma_desc(sm + ((c + y) % kTcSlots) * M::kTile, true, 0);
-    #pragma unroll
+#pragma unroll
                     for (uint32_t x = 0; x < D / 16; x++) {
                         const uint32_t o = ((x >> 2) * M::kHalf + (x & 3u) * 32) >> 4;
                         tc_mma_ss(tm + Tmem<D>::S(s), q + o, k + o, kQk, x != 0 || y);
@@ -532,14 +534,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_shared(const __grid_constant_
             while (walk.next(a, p)) {
                 if (ok) ok = __all_sync(kFull, bar_wait(q_rdy, piece++ & 1u));
                 tc_fence_after();
-                // K's slots: cnt, and with split cnt + 1
+                // K's slots: cnt, with kSplit cnt + 1 too
                 auto k_ready = [&]() {
                     slot_ready(cnt);
-                    if (a.split) slot_ready(cnt + 1);
+                    if constexpr (kSplit) slot_ready(cnt + 1);
                 };
                 auto free_k = [&]() {
                     free_slot(cnt++);
-                    if (a.split) free_slot(cnt++);
+                    if constexpr (kSplit) free_slot(cnt++);
                 };
                 if (a.one) {  // even token tiles: stream 0, odd ones: stream 1
                     for (uint32_t k = 0; k < 2 && k < p.n; k++) {
@@ -747,12 +749,15 @@ struct Runs {
 };
 
 // The rows x0.. of request r and KV head `head`, at most up to x_end.
+template <bool kQuant>
 __device__ __forceinline__ Runs runs_of(const Args &a, uint32_t r, uint32_t head, uint32_t x0, uint32_t x_end, uint32_t len,
                                         uint64_t own, uint64_t first) {
-    const uint32_t plog = a.clog - a.hlog;  // log2 of the parts of a row
+    constexpr uint32_t clog = columns_log<kQuant>();
+    const uint32_t plog = clog - a.hlog;  // log2 of the parts of a row
+    const uint32_t over = kQuant ? a.over : 0u;
     const uint32_t group = head >> a.hlog, hd = head & (a.nh - 1u);
     const uint32_t rlog = a.rlog, rmask = (1u << rlog) - 1u;
-    const uint32_t nt_sh = a.npt ? places_of(a, a.P) : 0, nt_own = len > a.P ? places_of(a, len - a.P) : 0;
+    const uint32_t nt_sh = a.npt ? places_of<kQuant>(a, a.P) : 0, nt_own = len > a.P ? places_of<kQuant>(a, len - a.P) : 0;
     const uint64_t total = own + (uint64_t)a.npt * a.ng * nt_sh, n_cta = shares(a, total);
     // places [t0, t0 + nt) of the list, an item's tiles, are spread over blocks c0..c1
     auto run = [](uint64_t t0, uint32_t nt, uint64_t n, uint64_t all, uint32_t &c0) {
@@ -773,25 +778,26 @@ __device__ __forceinline__ Runs runs_of(const Args &a, uint32_t r, uint32_t head
     }
     if (len && a.npt) {
         const uint32_t item = (xp >> rlog) * a.ng + group;
-        o.n_sh = run(own + (uint64_t)item * nt_sh + a.over, nt_sh - a.over, n_cta, total, c0) << plog;
-        o.sh = a.part0 + (((c0 + a.R * a.rt * a.ng + item) << a.clog) + hd) * a.piece_rows + (xp & rmask);
+        o.n_sh = run(own + (uint64_t)item * nt_sh + over, nt_sh - over, n_cta, total, c0) << plog;
+        o.sh = a.part0 + (((c0 + a.R * a.rt * a.ng + item) << clog) + hd) * a.piece_rows + (xp & rmask);
     }
     if (nt_own) {
         const uint32_t item = (x0 >> rlog) * a.ng + group;
-        o.n_own = run(first + (uint64_t)item * nt_own + a.over, nt_own - a.over, n_cta, total, c0) << plog;
-        o.own = a.part0 + (((c0 + r * a.rt * a.ng + item) << a.clog) + hd) * a.piece_rows + (x0 & rmask);
+        o.n_own = run(first + (uint64_t)item * nt_own + over, nt_own - over, n_cta, total, c0) << plog;
+        o.own = a.part0 + (((c0 + r * a.rt * a.ng + item) << clog) + hd) * a.piece_rows + (x0 & rmask);
     }
     o.n = o.n_tc + o.n_sh + o.n_own;
     return o;
 }
 
 // Row of piece e of the first row of `o`.
-__device__ __forceinline__ uint32_t place(const Args &a, const Runs &o, uint32_t e) {
+template <bool kQuant> __device__ __forceinline__ uint32_t place(const Args &a, const Runs &o, uint32_t e) {
     if (e < o.n_tc) return o.tc + (e >> a.one) * 256u + (e & a.one) * 128u;
-    const uint32_t plog = a.clog - a.hlog;
+    constexpr uint32_t clog = columns_log<kQuant>();
+    const uint32_t plog = clog - a.hlog;
     const bool sh = e - o.n_tc < o.n_sh;
     const uint32_t f = sh ? e - o.n_tc : e - o.n_tc - o.n_sh;
-    return (sh ? o.sh : o.own) + (((f >> plog) << a.clog) + ((f & ((1u << plog) - 1u)) << a.hlog)) * a.piece_rows;
+    return (sh ? o.sh : o.own) + (((f >> plog) << clog) + ((f & ((1u << plog) - 1u)) << a.hlog)) * a.piece_rows;
 }
 
 __device__ __forceinline__ uint16_t *out_row(const Args &a, uint32_t r, uint32_t head, uint32_t i, uint32_t j) {
@@ -807,7 +813,7 @@ __device__ __forceinline__ void write_lse(const Args &a, uint32_t r, uint32_t he
 // are there more): one trip to memory a row.  What counts is warps, since each
 // waits for its row: 32768 rows of three pieces took 37 us with 16 warps an SM,
 // 27 with 24, 23 with 32 and 21 where twice as many take half as many rows.
-template <class T, uint32_t D>
+template <class T, uint32_t D, bool kQuant>
 __global__ void __launch_bounds__(256, 4) k_merge_rows(const Args a) {
     wait_for_previous();
     constexpr uint32_t kLane = D / 32;
@@ -820,11 +826,11 @@ __global__ void __launch_bounds__(256, 4) k_merge_rows(const Args a) {
     const uint64_t own = a.cum[a.R], first = a.cum[r];
     uint32_t i = x_begin / a.g, j = x_begin - i * a.g;  // query token, query head of the KV head
     for (uint32_t x0 = x_begin; x0 < x_end;) {
-        const Runs o = runs_of(a, r, head, x0, x_end, len, own, first);
+        const Runs o = runs_of<kQuant>(a, r, head, x0, x_end, len, own, first);
         x0 += o.rows;
         uint32_t at[4];
 #pragma unroll
-        for (uint32_t e = 0; e < 4; e++) at[e] = e < o.n ? place(a, o, e) : 0;
+        for (uint32_t e = 0; e < 4; e++) at[e] = e < o.n ? place<kQuant>(a, o, e) : 0;
         const bool done = o.n_own == 1 && a.P == 0;  // k_rows has written the answer
 #pragma unroll 1
         for (uint32_t x = 0; x < o.rows; x++) {
@@ -834,7 +840,7 @@ __global__ void __launch_bounds__(256, 4) k_merge_rows(const Args a) {
                 for (uint32_t e0 = 0; e0 < o.n; e0 += 4) {
                     if (o.n > 4)
 #pragma unroll
-                        for (uint32_t e = 0; e < 4; e++) at[e] = e0 + e < o.n ? place(a, o, e0 + e) : 0;
+                        for (uint32_t e = 0; e < 4; e++) at[e] = e0 + e < o.n ? place<kQuant>(a, o, e0 + e) : 0;
                     float2 v[4];
                     float y[4][kLane];
 #pragma unroll
@@ -888,7 +894,7 @@ __global__ void __launch_bounds__(256, 4) k_merge_rows(const Args a) {
 // channels a lane, and the groups' sums meet in two halving exchanges.
 // kWide, for the fewest rows: a block to a row, its eight warps taking every
 // eighth 32 pieces; otherwise a warp takes a.merge_rows rows.
-template <class T, uint32_t D, bool kWide>
+template <class T, uint32_t D, bool kWide, bool kQuant>
 __global__ void __launch_bounds__(256, 3) k_merge(const Args a) {
     wait_for_previous();
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
@@ -902,7 +908,7 @@ __global__ void __launch_bounds__(256, 3) k_merge(const Args a) {
     constexpr uint32_t kPer = D / 8;
     const uint32_t grp = lane >> 3, gl = lane & 7u;
     for (uint32_t x0 = x_begin; x0 < x_end;) {
-        const Runs z = runs_of(a, r, head, x0, x_end, len, own, first);
+        const Runs z = runs_of<kQuant>(a, r, head, x0, x_end, len, own, first);
         const uint32_t n = z.n, x_first = x0;
         x0 += z.rows;
         if (z.n_own == 1 && a.P == 0) continue;  // k_rows has written the answer
@@ -917,7 +923,7 @@ __global__ void __launch_bounds__(256, 3) k_merge(const Args a) {
                 const float *s = nullptr;
                 float2 v = make_float2(-INFINITY, 0.f);
                 if (e0 + lane < n) {
-                    const uint32_t at = place(a, z, e0 + lane) + x;
+                    const uint32_t at = place<kQuant>(a, z, e0 + lane) + x;
                     v = a.part_ml[at];
                     s = a.part_o + (uint64_t)at * D;
                 }
@@ -1074,9 +1080,9 @@ cudaError_t launch_rows(const CUtensorMap &map, Args &a, int sms, cudaStream_t s
     return launch_next(k_rows<T, D, kR>, a.n_cta, S::kThreads, S::kBytes, s, a.pairs != 0, map, a);
 }
 
-template <class T, uint32_t D>
+template <class T, uint32_t D, bool kSplit>
 cudaError_t shared(const CUtensorMap &map, Args &a, int sms, cudaStream_t s) {
-    const cudaError_t e = cudaFuncSetAttribute(k_shared<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<D>::kBytes);
+    const cudaError_t e = cudaFuncSetAttribute(k_shared<T, D, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<D>::kBytes);
     if (e != cudaSuccess) return e;
     // An even deal of all tiles lets a block cross from one item to the
     // next, which costs about kCross tiles (the streams drain, new
@@ -1087,10 +1093,10 @@ cudaError_t shared(const CUtensorMap &map, Args &a, int sms, cudaStream_t s) {
     const uint64_t most = items * ((of + least - 1) / least), sm = (uint64_t)sms < kMaxTcCtas ? sms : kMaxTcCtas;
     const uint64_t n = sm < most ? sm : most, k = n / items;
     a.n_tc = (uint32_t)(k && (of + k - 1) / k <= items * of / n + kCross ? k * items : n);
-    return launch_next(k_shared<T, D>, a.n_tc, kTcThreads, TcSmem<D>::kBytes, s, a.after != 0, map, a);
+    return launch_next(k_shared<T, D, kSplit>, a.n_tc, kTcThreads, TcSmem<D>::kBytes, s, a.after != 0, map, a);
 }
 
-template <class T, uint32_t D>
+template <class T, uint32_t D, bool kQuant>
 cudaError_t joins(Args &a, int sms, cudaStream_t s) {
     // warps for the joins: as many as an SM holds (many rows: twice that), with a few rows each where there are rows enough
     const uint64_t per = (uint64_t)a.nq * a.g, rh = (uint64_t)a.R * a.Hkv;
@@ -1098,8 +1104,8 @@ cudaError_t joins(Args &a, int sms, cudaStream_t s) {
     const uint64_t fit = (uint64_t)sms * (many ? 64 : 24) / rh, chunks = fit < 1 ? 1 : fit < per ? fit : per;
     a.merge_rows = wide ? 1 : (uint32_t)((per + chunks - 1) / chunks);
     const uint64_t warps = rh * ((per + a.merge_rows - 1) / a.merge_rows);
-    if (wide) return launch_next(k_merge<T, D, true>, (unsigned)warps, 256, 0, s, true, a);
-    return launch_next(many ? k_merge_rows<T, D> : k_merge<T, D, false>, (unsigned)((warps + 7) / 8), 256, 0, s, true, a);
+    if (wide) return launch_next(k_merge<T, D, true, kQuant>, (unsigned)warps, 256, 0, s, true, a);
+    return launch_next(many ? k_merge_rows<T, D, kQuant> : k_merge<T, D, false, kQuant>, (unsigned)((warps + 7) / 8), 256, 0, s, true, a);
 }
 
 template <class T, uint32_t D>
@@ -1150,14 +1156,20 @@ bool make_token_map(const cg_pages *p, const uint16_t *base, uint32_t channels, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t launch_shared(uint32_t dtype, uint32_t head_dim, const CUtensorMap &map, Args &a, int sms, cudaStream_t s) {
-    if (head_dim == 128) return dtype == CG_FP16 ? shared<__half, 128>(map, a, sms, s) : shared<__nv_bfloat16, 128>(map, a, sms, s);
-    return dtype == CG_FP16 ? shared<__half, 64>(map, a, sms, s) : shared<__nv_bfloat16, 64>(map, a, sms, s);
+cudaError_t launch_shared(uint32_t dtype, uint32_t head_dim, bool split, const CUtensorMap &map, Args &a, int sms, cudaStream_t s) {
+    using B = __nv_bfloat16;
+    if (dtype == CG_FP16) return head_dim == 128 ? shared<__half, 128, false>(map, a, sms, s) : shared<__half, 64, false>(map, a, sms, s);
+    if (split) return head_dim == 128 ? shared<B, 128, true>(map, a, sms, s) : shared<B, 64, true>(map, a, sms, s);
+    return head_dim == 128 ? shared<B, 128, false>(map, a, sms, s) : shared<B, 64, false>(map, a, sms, s);
 }
 
-cudaError_t launch_joins(uint32_t dtype, uint32_t head_dim, Args &a, int sms, cudaStream_t s) {
-    if (head_dim == 128) return dtype == CG_FP16 ? joins<__half, 128>(a, sms, s) : joins<__nv_bfloat16, 128>(a, sms, s);
-    return dtype == CG_FP16 ? joins<__half, 64>(a, sms, s) : joins<__nv_bfloat16, 64>(a, sms, s);
+template <bool kQuant> cudaError_t launch_joins(uint32_t dtype, uint32_t head_dim, Args &a, int sms, cudaStream_t s) {
+    using B = __nv_bfloat16;
+    if (head_dim == 128) return dtype == CG_FP16 ? joins<__half, 128, kQuant>(a, sms, s) : joins<B, 128, kQuant>(a, sms, s);
+    return dtype == CG_FP16 ? joins<__half, 64, kQuant>(a, sms, s) : joins<B, 64, kQuant>(a, sms, s);
+}
+cudaError_t launch_joins(uint32_t dtype, uint32_t head_dim, bool quant, Args &a, int sms, cudaStream_t s) {
+    return quant ? launch_joins<true>(dtype, head_dim, a, sms, s) : launch_joins<false>(dtype, head_dim, a, sms, s);
 }
 
 }  // namespace cg
@@ -1207,7 +1219,6 @@ extern "C" cg_status cg_attend(const cg_pages *p, const cg_attention *at, void *
     a.nh = pl.nh;
     a.ng = pl.ng;
     a.hlog = (uint32_t)__builtin_ctz(pl.nh);
-    a.clog = 2;
     a.tlog = (uint32_t)__builtin_ctz(tt);
     a.rlog = (uint32_t)__builtin_ctz(pl.range_rows);
     a.rt = pl.rt;
@@ -1230,11 +1241,11 @@ extern "C" cg_status cg_attend(const cg_pages *p, const cg_attention *at, void *
     a.part0 = (uint32_t)pl.tc_rows;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool fp16 = at->dtype == CG_FP16;
-    if (a.pairs) CG_CUDA_TRY(launch_shared(at->dtype, at->head_dim, map, a, sms, s));
+    if (a.pairs) CG_CUDA_TRY(launch_shared(at->dtype, at->head_dim, false, map, a, sms, s));
     if (at->head_dim == 128)
         CG_CUDA_TRY((fp16 ? rows<__half, 128>(rows_map, pl.range_rows, a, sms, s) : rows<__nv_bfloat16, 128>(rows_map, pl.range_rows, a, sms, s)));
     else
         CG_CUDA_TRY((fp16 ? rows<__half, 64>(rows_map, pl.range_rows, a, sms, s) : rows<__nv_bfloat16, 64>(rows_map, pl.range_rows, a, sms, s)));
-    CG_CUDA_TRY(launch_joins(at->dtype, at->head_dim, a, sms, s));
+    CG_CUDA_TRY(launch_joins(at->dtype, at->head_dim, false, a, sms, s));
     return CG_OK;
 }

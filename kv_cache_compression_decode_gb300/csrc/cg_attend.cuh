@@ -23,7 +23,7 @@ struct Args {
     uint32_t R, nq, g, Hkv;  // requests, query tokens, query heads per KV head, KV heads
     uint32_t P, shared_slot; // shared tokens
     uint32_t nh, ng;         // row kernel: heads that one block takes together (a power of two), groups of them
-    uint32_t hlog, clog;     // log2 of nh, and of the warp columns of a block: a column has a head, or part of its tokens
+    uint32_t hlog;           // log2 of nh; a block's warp columns have a head each, or part of its tokens
     uint32_t tlog;           // log2 of the tokens of a tile
     uint32_t rlog;           // log2 of an item's rows
     uint32_t over;           // what a piece's beginning and end cost, in tiles: an item is dealt as that many tiles more
@@ -33,7 +33,6 @@ struct Args {
     uint32_t one;            // k_shared: the batch fits one 128-row tile
     uint32_t n_tc;           // blocks of k_shared
     uint32_t after;          // k_shared: its K and V are made by the kernel before it, which lets it start early
-    uint32_t split;          // k_shared: K is the sum of the map's matrices 0 and 2
     uint32_t merge_rows;     // rows of a warp of the joins
     uint32_t n_cta;          // blocks of the row kernel
     uint64_t qs[3], os[3];
@@ -71,9 +70,10 @@ __device__ __forceinline__ uint32_t tokens_of(const Args &a, uint32_t r, bool *b
 __device__ __forceinline__ uint32_t tiles_of(const Args &a, uint32_t tokens) {
     return (tokens + (1u << a.tlog) - 1u) >> a.tlog;
 }
-// Places on the work list that an item of `tokens` tokens takes.
-__device__ __forceinline__ uint32_t places_of(const Args &a, uint32_t tokens) {
-    return tokens ? tiles_of(a, tokens) + a.over : 0u;
+// Places on the work list that an item of `tokens` tokens takes.  (kQuant: k_quant_rows, whose items have a.over places
+// more and whose blocks have eight warp columns; k_rows has none more and four.)
+template <bool kQuant> __device__ __forceinline__ uint32_t places_of(const Args &a, uint32_t tokens) {
+    return tokens ? tiles_of(a, tokens) + (kQuant ? a.over : 0u) : 0u;
 }
 // Blocks that a list of `total` tiles is dealt to: two tiles each at least.
 __device__ __forceinline__ uint64_t shares(const Args &a, uint64_t total) {
@@ -107,14 +107,14 @@ __device__ __forceinline__ uint64_t quot(uint64_t x, uint64_t y) {
     return (x | y) >> 32 ? x / y : (uint32_t)x / (uint32_t)y;
 }
 
-__device__ __forceinline__ bool next_piece(const Args &a, Walk &w, Piece &p) {
+template <bool kQuant> __device__ __forceinline__ bool next_piece(const Args &a, Walk &w, Piece &p) {
     for (;;) {
         if (w.t >= w.end) return false;
         bool bad = false;
         uint32_t nt = 0, len = 0;  // places of an item of request r
         while (w.r < a.R) {
             len = w.lens ? w.lens[w.r] : tokens_of(a, w.r, &bad);
-            nt = len > a.P ? places_of(a, len - a.P) : 0;
+            nt = len > a.P ? places_of<kQuant>(a, len - a.P) : 0;
             const uint64_t all = (uint64_t)nt * a.rt * a.ng;
             if (w.t < w.base + all) break;
             w.base += all;
@@ -123,7 +123,7 @@ __device__ __forceinline__ bool next_piece(const Args &a, Walk &w, Piece &p) {
         p.r = w.r;
         if (w.r == a.R) {
             len = a.P;
-            nt = places_of(a, a.P);
+            nt = places_of<kQuant>(a, a.P);
         }
         if (nt == 0) return false;  // this and the next: lengths that changed under the call leave places over
         const uint64_t at = w.t - w.base;
@@ -135,10 +135,11 @@ __device__ __forceinline__ bool next_piece(const Args &a, Walk &w, Piece &p) {
         const uint32_t from = (uint32_t)(at - (uint64_t)local * nt);
         const uint32_t to = from + (uint32_t)min((uint64_t)(nt - from), w.end - w.t);
         w.t += to - from;
-        if (to <= a.over) continue;  // none of the item's tiles
-        p.tile0 = max(from, a.over) - a.over;
-        p.n = to - a.over - p.tile0;
-        p.of = nt - a.over;
+        const uint32_t over = kQuant ? a.over : 0u;
+        if (to <= over) continue;  // none of the item's tiles
+        p.tile0 = max(from, over) - over;
+        p.n = to - over - p.tile0;
+        p.of = nt - over;
         p.len = len;
         return true;
     }
@@ -148,7 +149,7 @@ __device__ __forceinline__ bool next_piece(const Args &a, Walk &w, Piece &p) {
 // every thread sums its own run of requests.  misc: a word for each warp and
 // two more; lens gets the tokens of up to max_lens requests.  Block 0 writes
 // a.cum and a.tokens.
-template <uint32_t kThreads>
+template <uint32_t kThreads, bool kQuant>
 __device__ __forceinline__ Walk take_share(const Args &a, uint64_t *misc, uint32_t *lens, uint32_t max_lens) {
     constexpr uint32_t kWarps = kThreads / 32;
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
@@ -161,7 +162,7 @@ __device__ __forceinline__ Walk take_share(const Args &a, uint64_t *misc, uint32
         const uint32_t n = tokens_of(a, r, &bad);
         if (keep) lens[r] = n;
         if (blockIdx.x == 0) a.tokens[r] = n;
-        mine += (uint64_t)(n > a.P ? places_of(a, n - a.P) : 0) * a.rt * a.ng;
+        mine += (uint64_t)(n > a.P ? places_of<kQuant>(a, n - a.P) : 0) * a.rt * a.ng;
     }
     if (bad && blockIdx.x == 0) flag(a.status, CG_ERR_RANGE);
     uint64_t inc = mine;
@@ -176,13 +177,13 @@ __device__ __forceinline__ Walk take_share(const Args &a, uint64_t *misc, uint32
         if (k < warp) before += misc[k];
         own += misc[k];
     }
-    const uint64_t total = own + (uint64_t)a.npt * a.ng * places_of(a, a.P);
+    const uint64_t total = own + (uint64_t)a.npt * a.ng * places_of<kQuant>(a, a.P);
     if (blockIdx.x == 0) {
         uint64_t at = before;
         for (uint32_t r = r0; r < r1; r++) {
             a.cum[r] = at;
             const uint32_t n = a.tokens[r];  // this thread's own write
-            at += (uint64_t)(n > a.P ? places_of(a, n - a.P) : 0) * a.rt * a.ng;
+            at += (uint64_t)(n > a.P ? places_of<kQuant>(a, n - a.P) : 0) * a.rt * a.ng;
         }
         if (tid == 0) a.cum[a.R] = own;
     }
@@ -223,13 +224,16 @@ __device__ __forceinline__ Row row_of(const Args &a, const Piece &p, uint32_t x,
     return o;
 }
 
+// log2 of the warp columns of a block of the row kernel
+template <bool kQuant> __host__ __device__ constexpr uint32_t columns_log() { return kQuant ? 3 : 2; }
+
 constexpr uint32_t kTcTok = 128, kTcSlots = 5;  // k_shared: tokens of a tile, tiles in flight
 constexpr uint32_t kMaxCtas = 304, kMaxTcCtas = 152;  // bounds of the grids that workspaces are sized for: 152 SMs
 
-// The launches of k_shared (a.n_tc is set; a.tables null: block i of the shared tokens is block i of the map) and
-// of the joins (cg_attend.cu).
-cudaError_t launch_shared(uint32_t dtype, uint32_t head_dim, const CUtensorMap &map, Args &a, int sms, cudaStream_t s);
-cudaError_t launch_joins(uint32_t dtype, uint32_t head_dim, Args &a, int sms, cudaStream_t s);
+// The launches of k_shared (a.n_tc is set; a.tables null: block i of the shared tokens is block i of the map; split, bf16
+// only: K is the sum of the map's matrices 0 and 2) and of the joins (cg_attend.cu).
+cudaError_t launch_shared(uint32_t dtype, uint32_t head_dim, bool split, const CUtensorMap &map, Args &a, int sms, cudaStream_t s);
+cudaError_t launch_joins(uint32_t dtype, uint32_t head_dim, bool quant, Args &a, int sms, cudaStream_t s);
 
 // A matrix (channel, row, block, K/V) of 16-bit words, in boxes of `box` channels x `rows` rows; `copies` of them, K and V
 // the first two, p->kv_stride apart.

@@ -206,6 +206,10 @@ __device__ __forceinline__ bool quantise(const uint4 &in, uint32_t lanes, uint2 
     return finite;
 }
 
+// Bound by the issue of instructions, 130 for a warp's 32 units, of which the
+// codes are 65 (75% of the cycles issue one): 9001 tokens x 32 layers x 1024
+// channels in 4 bits take 343 us, 4.55 TB/s.  Four blocks an SM (64 registers)
+// beat three and five: 588 / 606 / 602 us with the read after it.
 template <class T, uint32_t kBits>
 __global__ void __launch_bounds__(kThreads, 4) k_quant_write(const Job b) {
     const Run r(b);
@@ -241,6 +245,11 @@ __global__ void __launch_bounds__(kThreads, 4) k_quant_write(const Job b) {
     }
 }
 
+// Bound by DRAM: 15000 tokens x 32 layers in 8 bits take 441 us, 6.63 TB/s, 98%
+// of a plain copy's rate; in 4 bits instructions count, 9001 x 32 take 245 us,
+// 6.05 TB/s.  (A block that found its rows' places together, a thread at a time
+// going over their units, took 478 and 282 us: a warp to a row needs no barrier
+// and one address for all of it.)
 template <class T, uint32_t kBits>
 __global__ void __launch_bounds__(kThreads) k_quant_read(const Job b) {
     using Y = Type<T>;

@@ -14,8 +14,8 @@ bool misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t
 
 // Whether the shared blocks go through the workspace, by the row ranges that k_quant_rows would take over them (of 8 query
 // rows of a KV head, or of 16, which cost half as much again) and the tokens.  Microseconds a call, through the workspace /
-// in k_quant_rows, fp16, 8 KV heads: 2048 shared tokens, 64 rows 29 / 25, 128 rows 26 / 25; 8192 tokens, 64 rows 36 / 38,
-// 96 rows 33 / 43; 32768 tokens, 48 rows 87 / 70, 64 rows 90 / 93, 128 rows 86 / 160.  The workspace costs two launches
+// in k_quant_rows, fp16, 8 KV heads: 2048 shared tokens, 64 rows 29 / 27, 128 rows 25 / 26; 8192 tokens, 64 rows 40 / 41,
+// 96 rows 33 / 44; 32768 tokens, 48 rows 84 / 72, 64 rows 90 / 95, 128 rows 83 / 160.  The workspace costs two launches
 // and about the time of eight ranges.
 bool by_workspace(uint64_t ranges, uint32_t kN, uint64_t tokens, uint32_t heads) {
     const uint64_t half = ranges * (kN == 1 ? 2 : 3);
@@ -131,7 +131,6 @@ extern "C" cg_status cg_quant_attend(const cg_pages *p, const cg_quant *f, const
     a.nh = pl.nh;
     a.ng = pl.ng;
     a.hlog = pl.hlog;
-    a.clog = 3;
     a.tlog = (uint32_t)__builtin_ctz(pl.tt);
     a.rlog = pl.kN == 1 ? 3 : 4;
     a.over = 3;
@@ -179,9 +178,8 @@ extern "C" cg_status cg_quant_attend(const cg_pages *p, const cg_quant *f, const
         Args b = a;
         b.tables = nullptr;
         b.n_pool = at->shared_blocks;
-        b.split = pl.copies == 3;
         b.after = 1;
-        CG_CUDA_TRY(launch_shared(at->dtype, at->head_dim, map, b, sms, s));
+        CG_CUDA_TRY(launch_shared(at->dtype, at->head_dim, pl.copies == 3, map, b, sms, s));
         a.n_tc = b.n_tc;
     }
     const bool half = f->dtype == CG_FP16;
@@ -190,6 +188,6 @@ extern "C" cg_status cg_quant_attend(const cg_pages *p, const cg_quant *f, const
                                    : f->head_dim == 128 ? half ? launch_quant_rows_8_128_f : launch_quant_rows_8_128_b
                                                         : half ? launch_quant_rows_8_64_f : launch_quant_rows_8_64_b;
     CG_CUDA_TRY(rows(f->group, pl.kN, code_map, pair_map, a, q, sms, s));
-    CG_CUDA_TRY(launch_joins(at->dtype, at->head_dim, a, sms, s));
+    CG_CUDA_TRY(launch_joins(at->dtype, at->head_dim, true, a, sms, s));
     return CG_OK;
 }

@@ -16,7 +16,19 @@
 // rows' contraction for the scores, a channel's along tokens for the output),
 // query rows its 8 columns: the eight query heads of a KV head fill them, and a
 // single one wastes no codes.  A warp's tokens are permuted (pi) so that its
-// loads from the swizzled tiles meet no bank twice.
+// loads from the swizzled tiles meet no bank twice.  tcgen05 has no place here:
+// its operands would have to be written to shared memory as 16-bit numbers
+// first, which takes more instructions than the products do.
+//
+// A block takes eight neighbouring heads (or parts of fewer heads' tokens), a
+// warp to each: with 8 KV heads a token's whole row is one run of memory.  One
+// warp fetches by TMA, codes and pairs apart, five or six tiles of 32 tokens
+// ahead; a block has the SM, so that a warp may keep 232 registers.
+// Bound by how fast a warp's instructions follow one another: two warps a
+// scheduler issue in 47% of the cycles, about 340 instructions for 16 tokens of
+// a head (80 of them make the codes operands, 20 are products, which keep the
+// tensor cores 21% busy).  24 requests of 32 heads (210 MB of codes and pairs)
+// take 63 us, 3.4 TB/s; 100003 tokens in groups of 32 channels (128 MB) 46 us.
 #pragma once
 
 #include "cg_attend.cuh"
@@ -138,7 +150,7 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
         }
         fence_bar_init();
     }
-    Walk w = take_share<kQuantThreads>(a, reinterpret_cast<uint64_t *>(after + kQuantMisc),
+    Walk w = take_share<kQuantThreads, true>(a, reinterpret_cast<uint64_t *>(after + kQuantMisc),
                                        reinterpret_cast<uint32_t *>(after + kQuantLensAt), kQuantLens);
 
     const uint32_t tt = 1u << a.tlog;  // tokens of a tile
@@ -159,7 +171,7 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
         const uint32_t off = lane < subs ? lane << rlog : 0u;
         bool ok = true;
         uint32_t it = 0;
-        while (ok && next_piece(a, w, p)) {
+        while (ok && next_piece<true>(a, w, p)) {
             const bool shared = p.r == a.R;
             const uint32_t slot = shared ? a.shared_slot : a.slots ? a.slots[p.r] : p.r;
             const uint32_t *row = a.tables + (uint64_t)slot * a.n_blocks;
@@ -245,7 +257,7 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
             }
         }
     };
-    bool ok = true, more = next_piece(a, w, p);
+    bool ok = true, more = next_piece<true>(a, w, p);
     if (more) fetch_queries();
     while (more) {
         const bool shared = p.r == a.R, active = p.group * a.nh + hd < a.Hkv;
@@ -574,11 +586,11 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
         }
 
         const Piece done = p;
-        more = next_piece(a, w, p);
+        more = next_piece<true>(a, w, p);
         if (more) fetch_queries();
         if (active) {
-            const bool answer = a.P == 0 && a.hlog == a.clog && done.n == done.of;  // the whole sequence
-            const uint64_t slot = a.part0 + ((((uint64_t)blockIdx.x + done.item) << a.clog) + warp) * a.piece_rows;
+            const bool answer = a.P == 0 && a.hlog == columns_log<true>() && done.n == done.of;  // the whole sequence
+            const uint64_t slot = a.part0 + ((((uint64_t)blockIdx.x + done.item) << columns_log<true>()) + warp) * a.piece_rows;
             const uint32_t head = done.group * a.nh + hd, row0 = done.range << a.rlog;
 #pragma unroll
             for (uint32_t n = 0; n < kN; n++)
