@@ -317,7 +317,8 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                 q[n][e] = Half<__half>::pack(x[at] * f, x[at + kPer / 2] * f);
             }
             // what this lane's columns need, from the lanes that have the row
-            const float f = qa.scale2 * power2(24 - up);
+            // (neither 0 nor infinite: masked scores are -inf, and a score may be 0)
+            const float f = fminf(fmaxf(qa.scale2 * power2(24 - up), 0x1p-120f), 0x1p120f);
 #pragma unroll
             for (uint32_t j = 0; j < 2; j++) {
                 const uint32_t from = (2 * c + j) * 4;
@@ -445,8 +446,9 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                             for (uint32_t g = 0; g < NG; g++) pv[h][g] = 0;
                 }
                 // Weights are 2^{s fq - m}.  m and F stay while no operand can exceed 2^15, by a lane's largest weight, scale
-                // and F.  Otherwise m becomes the maximum of a column that did exceed it and F such that its largest
-                // operand lies in [2^4, 2^5), and O is scaled along: eleven octaves go by before the next time.
+                // and F, and no weight 2^60 (V may be zero, its scales too).  Otherwise m becomes the maximum of a column that
+                // did exceed it and F such that its largest operand lies in [2^4, 2^5), and O is scaled along: eleven octaves
+                // go by before the next time.
                 float widest = 0.f, x_most = -INFINITY;
 #pragma unroll
                 for (uint32_t g = 0; g < NG; g++) widest = fmaxf(widest, scale_of<T>(__vmaxu2(pv[0][g], pv[1][g])) * most[g]);
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                 for (uint32_t n = 0; n < kN; n++)
 #pragma unroll
                     for (uint32_t j = 0; j < 2; j++) x_most = fmaxf(x_most, fmaf(fmaxf(s[n][j], s[n][2 + j]), fq[n][j], -m[n][j]));
-                if (__builtin_expect(__any_sync(kFull, !(ex2(x_most) * widest <= 32768.f)), 0)) {
+                if (__builtin_expect(__any_sync(kFull, !(ex2(x_most) * widest <= 32768.f) || x_most > 60.f), 0)) {
 #pragma unroll
                     for (uint32_t g = 0; g < NG; g++) most[g] = 0.f;
 #pragma unroll
@@ -465,10 +467,11 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                             float mx = fmaxf(y[0], y[1]);
 #pragma unroll
                             for (uint32_t d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
-                            const bool first = m[n][j] == -INFINITY;
-                            const float z = !first ? m[n][j] : mx == -INFINITY ? 0.f : mx, wt[2] = {ex2(y[0] - z), ex2(y[1] - z)};
+                            // weights and their like against the maximum that m may become, fc of what they were
+                            const float top = fmaxf(m[n][j], mx), z = top == -INFINITY ? 0.f : top;
+                            const float fc = m[n][j] == top ? 1.f : ex2(m[n][j] - top), wt[2] = {ex2(y[0] - z), ex2(y[1] - z)};
                             float v[NG];  // the largest weights times scales
-                            bool move = first && mx != -INFINITY;
+                            bool move = m[n][j] == -INFINITY ? mx != -INFINITY : mx > m[n][j] + 60.f;
 #pragma unroll
                             for (uint32_t g = 0; g < NG; g++) {
                                 v[g] = 0.f;
@@ -477,18 +480,17 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                                     if (wt[h] != 0.f) v[g] = fmaxf(v[g], wt[h] * scale_of<T>(pv[h][g]));
 #pragma unroll
                                 for (uint32_t d = 4; d < 32; d <<= 1) v[g] = fmaxf(v[g], __shfl_xor_sync(kFull, v[g], d));
-                                move |= v[g] * F[n][g][j][0] > 32768.f;
+                                move |= v[g] * F[n][g][j][0] > 32768.f * fc;
                             }
                             // (a column moves for its own sake only: no query's rounding depends on the others)
-                            const float nm = move ? fmaxf(m[n][j], mx) : m[n][j], f = nm == m[n][j] ? 1.f : ex2(m[n][j] - nm);
-                            const float by_new = first ? 1.f : f;
-                            m[n][j] = nm;
+                            const float f = move ? fc : 1.f;
+                            if (move) m[n][j] = top;
                             l[n][j][0] *= f;
                             l[n][j][1] *= f;
 #pragma unroll
                             for (uint32_t g = 0; g < NG; g++) {
                                 float *F_ = F[n][g][j];
-                                const float old = f / F_[0], nf = move ? power2(4 - exponent(fmaxf(v[g] * by_new, 32.f * old))) : F_[0];
+                                const float old = f / F_[0], nf = move ? power2(4 - exponent(fmaxf(v[g], 32.f * old))) : F_[0];
                                 const float by = old * nf;
                                 F_[0] = F_[1] = nf;
                                 most[g] = fmaxf(most[g], nf);

@@ -215,6 +215,25 @@ def test_an_even_share_a_start_and_strided_inputs(R, n):
 
 
 @gpu
+@pytest.mark.parametrize("bt", [1, 4])
+@pytest.mark.parametrize("Hkv,D,group", [(1, 64, 32), (5, 64, 64), (40, 128, 128)])
+def test_small_blocks_and_long_rows(bt, Hkv, D, group):
+    """Rows of 8 to 640 eight-channel units, in blocks smaller than attention takes."""
+    cache, slots = empty([3, 11], bt, Hkv, D, 8, group, FP16, L=3)
+    k, v = rows_like((3, 10, Hkv * D), FP16), rows_like((3, 10, Hkv * D), FP16, 1)
+    cache.write(k, v, slots=slots, offsets=_ints([0, 2, 10]))
+    at = torch.tensor(places(cache, slots, [2, 8]), device="cuda")
+    n = Hkv * D // 2 + 2 * (Hkv * D // group)
+    for kv, x in enumerate((k, v)):
+        got = cache.pool[:, at[:, 1], kv, at[:, 2]].cpu().numpy().view(np.uint16)
+        assert np.array_equal(got[..., :n], want_rows(x, cache)[..., :n])
+    back, _ = cache.read(n_layers=3, rows=10, slots=slots, offsets=_ints([0, 2, 10]))
+    code, scale, low = parts(cache.pool[:, at[:, 1], 0, at[:, 2]], cache)
+    assert torch.equal(back, (code * scale + low).float().half())
+    cache.check()
+
+
+@gpu
 @pytest.mark.parametrize("dtype", [FP16, BF16])
 @pytest.mark.parametrize("bits", [4, 8])
 def test_values_on_borders_and_at_the_ends_of_the_type(dtype, bits):
@@ -581,6 +600,53 @@ def test_queries_of_any_size(dtype, size):
     q, out, lse = attend(cache, slots, q=q, scale=scale)
     cache.check()
     check(cache, q, out, lse, slots, 1, np.float32(scale).item())
+
+
+@gpu
+@pytest.mark.parametrize("R", [3, 40])
+@pytest.mark.parametrize("scale,size", [(0.0, 1.0), (0.0, 1e-30), (1e-20, 1.0), (3.0, 1.0), (-3.0, 1.0), (1e-30, 1e-30)])
+def test_scales(R, scale, size):
+    lens = [5 * 16 + 1 + 37 * r % 90 for r in range(R)]
+    cache, slots = make(lens, 5, 16, 2, 64, dtype=BF16)
+    q = (rows_like((R, 2, 8, 64), BF16).float() * size).to(BF16)
+    q, out, lse = attend(cache, slots, nq=2, q=q, scale=scale, shared_blocks=5)
+    cache.check()
+    check(cache, q, out, lse, slots, 1, np.float32(scale).item(), 5)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [FP16, BF16])
+def test_scores_that_rise_over_values_without_size(dtype):
+    """V is zero, or a constant, for most tokens while the scores climb by hundreds of octaves; then they fall again."""
+    n = 640
+    cache, slots = make([n, n], 0, 16, 1, 128, group=32, dtype=dtype)
+    t = torch.arange(n, device="cuda")
+    ramp = torch.cat([t, n - t]).float()[:, None] * 0.5
+    k = ramp.expand(-1, 128) + rows_like((2 * n, 128), dtype, 4).float() * 0.01
+    v = torch.zeros((2 * n, 128), device="cuda")
+    v[:, 32:64] = -2.5
+    v[::7] = rows_like((2 * n, 128), dtype, 5).float()[::7]
+    cache.write(*(x.to(dtype).expand(2, -1, -1) for x in (k, v)), slots=slots)
+    q = torch.ones((2, 1, 8, 128), dtype=dtype, device="cuda") * torch.tensor([1, 2, -1, 0, 0.25, 8, -8, 0.01], device="cuda").to(dtype)[:, None]
+    q, out, lse = attend(cache, slots, q=q, scale=0.125)
+    cache.check()
+    assert torch.isfinite(out).all()
+    check(cache, q, out, lse, slots, 1, 0.125)
+
+
+@gpu
+def test_a_query_that_is_not_finite_spoils_its_own_row_alone():
+    cache, slots = make([300], 0, 16, 2, 64)
+    q, out, lse = attend(cache, slots, nq=2)
+    bad = q.clone()
+    bad[0, 1, 3, 7] = float("nan")
+    bad[0, 0, 6, 0] = float("inf")
+    _, o, e = attend(cache, slots, nq=2, q=bad)
+    keep = torch.ones((2, 8), dtype=torch.bool, device="cuda")
+    keep[1, 3] = keep[0, 6] = False
+    assert torch.equal(o[0][keep], out[0][keep]) and torch.equal(e[0][keep], lse[0][keep])
+    assert torch.isnan(o[0, 1, 3]).all() and not torch.isfinite(o[0, 0, 6]).all()
+    cache.check()
 
 
 @gpu
