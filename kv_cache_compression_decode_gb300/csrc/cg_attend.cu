@@ -893,7 +893,12 @@ __global__ void __launch_bounds__(256, 4) k_merge_rows(const Args a) {
 // largest; then four groups of eight lanes add up every fourth piece, D / 8
 // channels a lane, and the groups' sums meet in two halving exchanges.
 // kWide, for the fewest rows: a block to a row, its eight warps taking every
-// eighth 32 pieces; otherwise a warp takes a.merge_rows rows.
+// eighth 32 pieces; otherwise a warp takes a.merge_rows rows.  With kQuant,
+// whose row kernel has no second block an SM and so at most 152 pieces a range
+// and part, few pieces are dealt evenly over the eight warps: 152 of them are
+// five rounds of loads a warp instead of eight (one request of 100003 tokens
+// 55.4 -> 53.3 us).  Loading two pieces of a group before either is added
+// spilled and was slower (24 ragged requests 66 -> 68 us).
 template <class T, uint32_t D, bool kWide, bool kQuant>
 __global__ void __launch_bounds__(256, 3) k_merge(const Args a) {
     wait_for_previous();
@@ -913,16 +918,18 @@ __global__ void __launch_bounds__(256, 3) k_merge(const Args a) {
         x0 += z.rows;
         if (z.n_own == 1 && a.P == 0) continue;  // k_rows has written the answer
         if (kWide && n <= 32 && warp) return;
+        // pieces that a warp looks at together; a block's eight warps share few evenly
+        const uint32_t step = kWide && kQuant && n > 32 ? min(32u, ((n + 31) / 32) * 4) : 32u;
 #pragma unroll 1
         for (uint32_t x = 0; x < z.rows; x++) {
             float m = -INFINITY, l = 0.f, o[kPer];
 #pragma unroll
             for (uint32_t k = 0; k < kPer; k++) o[k] = 0.f;
 #pragma unroll 1
-            for (uint32_t e0 = kWide ? 32 * warp : 0; e0 < n; e0 += kWide ? 256 : 32) {
+            for (uint32_t e0 = kWide ? step * warp : 0; e0 < n; e0 += kWide ? 8 * step : 32) {
                 const float *s = nullptr;
                 float2 v = make_float2(-INFINITY, 0.f);
-                if (e0 + lane < n) {
+                if (e0 + lane < n && lane < step) {
                     const uint32_t at = place<kQuant>(a, z, e0 + lane) + x;
                     v = a.part_ml[at];
                     s = a.part_o + (uint64_t)at * D;
@@ -944,7 +951,7 @@ __global__ void __launch_bounds__(256, 3) k_merge(const Args a) {
                 if (e0)
 #pragma unroll
                     for (uint32_t k = 0; k < kPer; k++) o[k] *= f;
-                const uint32_t cnt = min(n - e0, 32u);
+                const uint32_t cnt = min(n - e0, step);
 #pragma unroll 2
                 for (uint32_t b = 0; b < cnt; b += 4) {
                     const float wj = __shfl_sync(kFull, w, b + grp);

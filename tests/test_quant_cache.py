@@ -523,6 +523,19 @@ def test_query_rows_around_one_tile_over_thousands_of_shared_tokens(dtype, R, g,
 
 
 @gpu
+@pytest.mark.parametrize("Hkv,D,pieces", [(8, 64, n) for n in (1, 2, 8, 9, 12, 31, 32, 33, 36, 37, 64, 65, 151, 160)]
+                         + [(1, 64, n) for n in (1, 2, 5, 40)] + [(4, 128, n) for n in (17, 129)])
+def test_one_request_in_few_and_many_pieces(Hkv, D, pieces):
+    """The pieces that the join of one request's rows meets: fewer and more than its warps take in one and in several goes
+    (of eight heads a piece a block, of four two, of one eight)."""
+    tokens = max(1, 32 * (2 * pieces - 3) - 5)  # two places of 32 tokens a block, three of them for the beginning
+    cache, slots = make([tokens], bt=32, Hkv=Hkv, D=D, bits=4, group=64, seed=pieces)
+    q, out, lse = attend(cache, slots, Hq=2 * Hkv)
+    cache.check()
+    check(cache, q, out, lse, slots, 1, D ** -0.5)
+
+
+@gpu
 @pytest.mark.parametrize("Hkv,g,nq", [(4, 8, 1), (8, 8, 4), (12, 1, 1), (5, 5, 2), (6, 5, 2), (32, 1, 1), (9, 3, 7)])
 @pytest.mark.parametrize("D,shared", [(128, 0), (128, 9), (64, 0), (64, 9)])
 def test_groups_of_heads(Hkv, g, nq, D, shared):
