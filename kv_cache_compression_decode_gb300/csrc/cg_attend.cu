@@ -897,7 +897,8 @@ __global__ void __launch_bounds__(256, 4) k_merge_rows(const Args a) {
 // whose row kernel has no second block an SM and so at most 152 pieces a range
 // and part, few pieces are dealt evenly over the eight warps: 152 of them are
 // five rounds of loads a warp instead of eight (one request of 100003 tokens
-// 55.4 -> 53.3 us).  Loading two pieces of a group before either is added
+// 55.4 -> 53.3 us), and from nine pieces on the block's warps share a row
+// (with 33: 700 tokens 16.4 us; with nine 14.4).  Loading two pieces of a group before either is added
 // spilled and was slower (24 ragged requests 66 -> 68 us).
 template <class T, uint32_t D, bool kWide, bool kQuant>
 __global__ void __launch_bounds__(256, 3) k_merge(const Args a) {
@@ -910,16 +911,16 @@ __global__ void __launch_bounds__(256, 3) k_merge(const Args a) {
     const uint32_t x_end = min(x_begin + a.merge_rows, per);
     const uint32_t len = a.tokens[r];
     const uint64_t own = a.cum[a.R], first = a.cum[r];
-    constexpr uint32_t kPer = D / 8;
+    constexpr uint32_t kPer = D / 8, kFew = kQuant ? 8 : 32;  // pieces that one warp of a block takes alone
     const uint32_t grp = lane >> 3, gl = lane & 7u;
     for (uint32_t x0 = x_begin; x0 < x_end;) {
         const Runs z = runs_of<kQuant>(a, r, head, x0, x_end, len, own, first);
         const uint32_t n = z.n, x_first = x0;
         x0 += z.rows;
         if (z.n_own == 1 && a.P == 0) continue;  // k_rows has written the answer
-        if (kWide && n <= 32 && warp) return;
+        if (kWide && n <= kFew && warp) return;
         // pieces that a warp looks at together; a block's eight warps share few evenly
-        const uint32_t step = kWide && kQuant && n > 32 ? min(32u, ((n + 31) / 32) * 4) : 32u;
+        const uint32_t step = kWide && kQuant && n > kFew ? min(32u, ((n + 31) / 32) * 4) : 32u;
 #pragma unroll 1
         for (uint32_t x = 0; x < z.rows; x++) {
             float m = -INFINITY, l = 0.f, o[kPer];
@@ -979,7 +980,7 @@ __global__ void __launch_bounds__(256, 3) k_merge(const Args a) {
                 const float give = grp & 1u ? o[k] : o[k + kPer / 4], keep = grp & 1u ? o[k + kPer / 4] : o[k];
                 o[k] = keep + __shfl_xor_sync(kFull, give, 8);
             }
-            if (kWide && n > 32) {  // a row a block: the warps' sums meet in shared memory
+            if (kWide && n > kFew) {  // a row a block: the warps' sums meet in shared memory
                 __shared__ float2 sh_ml[8];
                 __shared__ float sh_o[8][D];
                 constexpr uint32_t kOwn = kPer / 4;
