@@ -14,9 +14,10 @@ bool misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t
 
 // Whether the shared blocks go through the workspace, by the row ranges that k_quant_rows would take over them (of 8 query
 // rows of a KV head, or of 16, which cost half as much again) and the tokens.  Microseconds a call, through the workspace /
-// in k_quant_rows, fp16, 8 KV heads: 2048 shared tokens, 64 rows 29 / 27, 128 rows 25 / 26; 8192 tokens, 64 rows 40 / 41,
-// 96 rows 33 / 44; 32768 tokens, 48 rows 84 / 72, 64 rows 90 / 95, 128 rows 83 / 160.  The workspace costs two launches
-// and about the time of eight ranges.
+// in k_quant_rows, fp16, 8 KV heads: 2048 shared tokens, 64 rows 28 / 21, 128 rows 25 / 25; 8192 tokens, 64 rows 33 / 35,
+// 96 rows 33 / 44; 32768 tokens, 48 rows 80 / 69, 64 rows 83 / 91, 128 rows 83 / 163.  bf16, whose K goes in two parts:
+// 8192 tokens, 64 rows 39 / 37, 96 rows 38 / 46; 32768 tokens, 64 rows 102 / 97, 96 rows 101 / 136.  The workspace costs
+// two launches and about the time of eight ranges.
 bool by_workspace(uint64_t ranges, uint32_t kN, uint64_t tokens, uint32_t heads) {
     const uint64_t half = ranges * (kN == 1 ? 2 : 3);
     return half > 16 && (half - 16) * tokens * heads > 160000;

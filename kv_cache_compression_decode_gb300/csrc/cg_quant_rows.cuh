@@ -25,10 +25,9 @@
 // warp fetches by TMA, codes and pairs apart, five or six tiles of 32 tokens
 // ahead; a block has the SM, so that a warp may keep 232 registers.
 // Bound by how fast a warp's instructions follow one another: two warps a
-// scheduler issue in 47% of the cycles, about 340 instructions for 16 tokens of
-// a head (80 of them make the codes operands, 20 are products, which keep the
-// tensor cores 21% busy).  24 requests of 32 heads (210 MB of codes and pairs)
-// take 63 us, 3.4 TB/s; 100003 tokens in groups of 32 channels (128 MB) 46 us.
+// scheduler issue in 47% of the cycles, with the tensor cores 21% busy.  24
+// requests of 32 heads (210 MB of codes and pairs) take 63 us, 3.4 TB/s; 100003
+// tokens in groups of 32 channels (128 MB) 47 us.
 #pragma once
 
 #include "cg_attend.cuh"
@@ -329,9 +328,12 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
 
         // Running maximum m and sum l of the weights, their products with the low values, and the power of two F that a
         // group's weights times scales are multiplied by before they become operands.
-        // Codes are taken about their middle: the operands' rounding then meets half the codes' size, and with one column
-        // tile the middle's part is a product of its own (mid), taken away again at the end.
-        constexpr bool kMid = kN == 1;
+        // Codes are taken about their middle: the operands' rounding then meets half the codes' size, and the middle's part
+        // is a product of its own (mid), taken away again at the end.  With two column tiles, whose registers spill, this is
+        // done for fp16 and up to two groups a head: 40 rows of eight heads, groups of 64, are off by 2.5e-4 instead of 4.0e-4
+        // (the output's own rounding: 2.1e-4), and with groups of 128 over 4000 tokens take 76 to 82 us instead of 75.  With
+        // four groups it would be 136 instead of 103 us; bf16's output rounding, 1.7e-3, hides it (53 instead of 50 us).
+        constexpr bool kMid = kN == 1 || (__is_same(T, __half) && NG <= 2);
         float o[kN][D / 16][4], m[kN][2], l[kN][2][2], lows[kN][NG][2][2], F[kN][NG][2][2], mid[kN][NG][4], most[NG];
 #pragma unroll
         for (uint32_t g = 0; g < NG; g++) most[g] = 1.f;  // the larger F of the columns
