@@ -1,0 +1,53 @@
+"""Caches in 4 or 8 bits at the ends of the types' ranges.  Tolerances are those of test_quant_cache.py."""
+import numpy as np
+import pytest
+import torch
+
+from kv_cache_compression_decode_gb300 import codec as C
+from tests.test_quant_cache import BF16, attend, check, empty, gpu, make, parts, places, rows_like
+
+
+@gpu
+@pytest.mark.parametrize("group", [32, 128])
+def test_the_top_code_past_the_largest_number_reads_back_as_that(group):
+    """bf16, 4 bits: the largest code's value may lie past 2^128 although every channel is finite."""
+    most, unit = float(torch.finfo(BF16).max), 2.0 ** 120
+    rng = np.random.default_rng(1)
+    x = rng.uniform(-4, 255, (64, 128)) * unit
+    low = np.linspace(-3, 4, 64)
+    x[:, 0::32], x[:, 1::32] = low[:, None] * unit, most
+    x[:, 2::32] = np.maximum(x[:, 2::32], low[:, None] * unit)
+    x = torch.tensor(np.maximum(x, low[:, None] * unit), device="cuda").to(BF16)
+    cache, slots = empty([64], 32, 1, 128, 4, group, BF16)
+    cache.write(x[None], -x[None], slots=slots)
+    at = torch.tensor(places(cache, slots, [64]), device="cuda")
+    y = x.double().view(64, -1, group)
+    odd = torch.isinf((y.amax(-1) - y.amin(-1)).float()).repeat_interleave(group, 1)  # such a span is stored as NaN, and flagged
+    assert odd.any()
+    for kv, y in enumerate(cache.read(rows=64, slots=slots)):
+        code, scale, first = parts(cache.pool[0, at[:, 1], kv, at[:, 2]], cache)
+        value = code * scale + first
+        assert torch.equal(torch.isnan(value), odd)
+        if kv == 0:
+            assert (value >= 2.0 ** 128).any()
+        assert torch.equal(torch.isnan(y[0]), odd) and torch.equal(y[0][~odd], value.clamp(max=most).float().to(BF16)[~odd])
+    with pytest.raises(C.CodecError) as e:
+        cache.check()
+    assert e.value.code == C.CG_ERR_NONFINITE
+
+
+@gpu
+@pytest.mark.parametrize("R", [8, 80])
+def test_keys_past_the_largest_number_reach_the_queries_that_use_them(R):
+    """bf16: groups whose top code lies past 2^128, and queries that are zero in their channels."""
+    shared, bt, Hkv = 160, 32, 8
+    cache, slots = make([shared * bt + 1 + r % 5 for r in range(R)], shared, bt, Hkv, 128, group=32, dtype=BF16)
+    k, v = rows_like((1, shared * bt, Hkv * 128), BF16, 1), rows_like((1, shared * bt, Hkv * 128), BF16, 2)
+    q = rows_like((R, 1, Hkv, 128), BF16, 3)
+    k.view(-1, Hkv, 128)[::7, :, 0:32] = 2.0 ** 120
+    k.view(-1, Hkv, 128)[::7, :, 3] = torch.finfo(BF16).max
+    q[..., 0:32] = 0.0
+    cache.write(k, v, layer=1, slots=slots.new_zeros(1))
+    q, out, lse = attend(cache, slots, q=q, shared_blocks=shared)
+    cache.check()
+    check(cache, q, out, lse, slots, 1, 128 ** -0.5, shared)
