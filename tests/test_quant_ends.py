@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+import tests.test_paged_attend as plain
 from kv_cache_compression_decode_gb300 import codec as C
 from tests.test_quant_cache import BF16, attend, check, empty, gpu, make, parts, places, rows_like
 
@@ -51,3 +52,30 @@ def test_keys_past_the_largest_number_reach_the_queries_that_use_them(R):
     q, out, lse = attend(cache, slots, q=q, shared_blocks=shared)
     cache.check()
     check(cache, q, out, lse, slots, 1, 128 ** -0.5, shared)
+
+
+@gpu
+@pytest.mark.parametrize("R", [2, 40])
+@pytest.mark.parametrize("bits", [16, 4])
+def test_scales_below_1e_35(bits, R):
+    """Products of 2^116 at a scale of 2^-118, which makes ordinary scores of them, and at a scale of zero."""
+    P, Hkv, D, size = 96, 2, 64, 2.0 ** 57
+    lens = [P + 2 + 7 * r % 50 for r in range(R)]
+    q = (rows_like((R, 2, 8, D), BF16, 7).double() * 2.0 ** 56).to(BF16)
+    if bits == 16:
+        cache, slots = plain.make(lens, P // 16, 16, Hkv, D, BF16)
+        cache.pool.mul_(size)
+    else:
+        cache, slots = make(lens, P // 16, 16, Hkv, D, dtype=BF16)
+        for s, n in [(0, P)] + [(s, n - P) for s, n in enumerate(lens, 1)]:
+            rows = [(rows_like((2, n, Hkv * D), BF16, 2 * s + i).double() * size).to(BF16) for i in range(2)]
+            cache.write(*rows, slots=torch.tensor([s], dtype=torch.int32, device="cuda"))
+    for scale in (2.0 ** -118, 0.0, -2.0 ** -118):
+        if bits == 16:
+            _, out, lse = plain.attend(cache, slots, nq=2, Hq=8, D=D, q=q, scale=scale, shared_blocks=P // 16)
+            cache.check()
+            plain.check(cache, q, out, lse, slots, 1, scale)
+        else:
+            _, out, lse = attend(cache, slots, nq=2, q=q, scale=scale, shared_blocks=P // 16)
+            cache.check()
+            check(cache, q, out, lse, slots, 1, scale, P // 16)
