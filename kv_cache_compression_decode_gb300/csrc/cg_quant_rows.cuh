@@ -286,10 +286,16 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
             }
             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-            const int up = mx == 0.f || mx == INFINITY ? 0 : max(-100, min(100, 14 - exponent(mx)));
-            const float high = a.flip ? -power2(up) : power2(up);  // a negative scale turns q
+            // (bf16's exponents go further than one factor: -113 .. 141)
+            const int up = mx == 0.f || mx == INFINITY ? 0 : 14 - exponent(mx), up0 = kHalf ? up : up / 2;
+            const float high = a.flip ? -power2(up0) : power2(up0);  // a negative scale turns q
 #pragma unroll
             for (uint32_t e = 0; e < D / 4; e++) x[e] *= high;
+            if constexpr (!kHalf) {
+                const float rest = power2(up - up0);
+#pragma unroll
+                for (uint32_t e = 0; e < D / 4; e++) x[e] *= rest;
+            }
             float sum = 0.f;
 #pragma unroll
             for (uint32_t g = 0; g < NG; g++) {
@@ -317,7 +323,8 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
             }
             // what this lane's columns need, from the lanes that have the row
             // (neither 0 nor infinite: masked scores are -inf, and a score may be 0)
-            const float f = fminf(fmaxf(qa.scale2 * power2(24 - up), 0x1p-120f), 0x1p120f);
+            const int down = 24 - up, down0 = down / 2;
+            const float f = fminf(fmaxf(qa.scale2 * power2(down0) * power2(down - down0), 0x1p-149f), 0x1p127f);
 #pragma unroll
             for (uint32_t j = 0; j < 2; j++) {
                 const uint32_t from = (2 * c + j) * 4;

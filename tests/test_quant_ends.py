@@ -79,3 +79,17 @@ def test_scales_below_1e_35(bits, R):
             _, out, lse = attend(cache, slots, nq=2, q=q, scale=scale, shared_blocks=P // 16)
             cache.check()
             check(cache, q, out, lse, slots, 1, scale, P // 16)
+
+
+@gpu
+@pytest.mark.parametrize("nq,Hq", [(1, 8), (3, 16)])
+@pytest.mark.parametrize("e", [-132, -126, -110, -100, 96, 111, 113, 116, 118, 126])
+def test_queries_over_the_whole_range_of_bf16(e, nq, Hq):
+    """Channels up to 2^e in size, and a scale that makes ordinary scores of them."""
+    cache, slots = make([100, 300], 0, 16, 2, 128, dtype=BF16)
+    q = rows_like((2, nq, Hq, 128), BF16).double()
+    q = (q / q.abs().max() * 1.9 * 2.0 ** e).to(BF16)
+    scale = float(np.float32(min(128 ** -0.5 * 2.0 ** -e, 2.0 ** 125)))
+    q, out, lse = attend(cache, slots, nq=nq, q=q, scale=scale)
+    cache.check()
+    check(cache, q, out, lse, slots, 1, scale)
