@@ -136,6 +136,9 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
     constexpr uint32_t kKWords = kQuarter / 4;             // words of a lane's quarter of a group
     constexpr bool kHalf = __is_same(T, __half);
     constexpr float kMiddle = kBits == 4 ? 8.f : 128.f;
+    // What the sums of q are multiplied by: at most 128 2^15 2^-8 lies within fp16; bf16 ones are at once in the units of the
+    // codes' part, so that a low value of 2^127 does not take the product past fp32.
+    constexpr float kSumUnit = kHalf ? 0x1p-8f : 0x1p-24f;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (s_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t sm = s_addr(smem);
@@ -304,7 +307,7 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                 for (uint32_t e = 0; e < G / 4; e++) y += x[g * (G / 4) + e];
                 y += __shfl_xor_sync(kFull, y, 1);
                 y += __shfl_xor_sync(kFull, y, 2);
-                if (g == (c & (NG - 1))) sum = y * 0x1p-8f;  // at most 128 2^15 2^-8: within fp16
+                if (g == (c & (NG - 1))) sum = y * kSumUnit;
             }
 #pragma unroll
             for (uint32_t k = 0; k < kLowMma; k++) qs[n][k][0] = qs[n][k][1] = 0u;
@@ -396,8 +399,9 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                         Half<T>::mma0(s[n], lw, qs[n][0][0], qs[n][0][1]);
 #pragma unroll
                         for (uint32_t e = 1; e < kLowMma; e++) Half<T>::mma(s[n], lw, qs[n][e][0], qs[n][e][1]);
+                        if constexpr (kHalf)  // to the units of the codes' part
 #pragma unroll
-                        for (uint32_t e = 0; e < 4; e++) s[n][e] *= 0x1p-16f;  // to the units of the codes' part
+                            for (uint32_t e = 0; e < 4; e++) s[n][e] *= 0x1p-24f / kSumUnit;
                     }
                     constexpr uint32_t kChains = G >= 64 ? 2 : 1;  // sums of a group side by side
 #pragma unroll

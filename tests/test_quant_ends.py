@@ -93,3 +93,17 @@ def test_queries_over_the_whole_range_of_bf16(e, nq, Hq):
     q, out, lse = attend(cache, slots, nq=nq, q=q, scale=scale)
     cache.check()
     check(cache, q, out, lse, slots, 1, scale)
+
+
+@gpu
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("e", [-100, -80, 80, 105, 114, 118])
+def test_keys_over_the_whole_range_of_bf16(e, group):
+    """Keys of about 2^e against queries of about 2^-e."""
+    cache, slots = make([100, 300], 0, 16, 2, 128, group=group, dtype=BF16)
+    k, v = rows_like((2, 400, 256), BF16, 1), rows_like((2, 400, 256), BF16, 2)
+    cache.write((k.double() * 2.0 ** e).to(BF16), v, slots=slots, offsets=torch.tensor([0, 100, 400], dtype=torch.int32, device="cuda"))
+    q = (rows_like((2, 1, 8, 128), BF16, 3).double() * 2.0 ** -e).to(BF16)
+    q, out, lse = attend(cache, slots, q=q)
+    cache.check()
+    check(cache, q, out, lse, slots, 1, 128 ** -0.5)
