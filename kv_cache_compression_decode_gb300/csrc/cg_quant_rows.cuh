@@ -629,12 +629,13 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                     constexpr uint32_t kPer = G / 8;  // channels of a group that this lane has
 #pragma unroll
                     for (uint32_t g = 0; g < NG; g++) {
-                        const float unit = 0x1p24f / F[n][g][j][0], centre = kMid ? mid[n][g][j] : 0.f;
+                        // (two factors: their product may lie past fp32 where V is large)
+                        const float unit = 1.f / F[n][g][j][0], centre = kMid ? mid[n][g][j] : 0.f;
                         float y[kPer];
 #pragma unroll
                         for (uint32_t d = 0; d < kPer / 2; d++) {
-                            y[2 * d] = fmaf(o[n][g * (G / 16) + d][j] - centre, unit, low[g]) * inv;
-                            y[2 * d + 1] = fmaf(o[n][g * (G / 16) + d][2 + j] * (kBits == 4 ? 0.0625f : 1.f) - centre, unit, low[g]) * inv;
+                            y[2 * d] = fmaf((o[n][g * (G / 16) + d][j] - centre) * 0x1p24f, unit, low[g]) * inv;
+                            y[2 * d + 1] = fmaf((o[n][g * (G / 16) + d][2 + j] * (kBits == 4 ? 0.0625f : 1.f) - centre) * 0x1p24f, unit, low[g]) * inv;
                         }
                         const uint32_t ch = g * G + r * kPer;
                         if (answer) {

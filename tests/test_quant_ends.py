@@ -107,3 +107,17 @@ def test_keys_over_the_whole_range_of_bf16(e, group):
     q, out, lse = attend(cache, slots, q=q)
     cache.check()
     check(cache, q, out, lse, slots, 1, 128 ** -0.5)
+
+
+@gpu
+@pytest.mark.parametrize("nq,Hq", [(1, 8), (3, 16)])
+@pytest.mark.parametrize("bits,group", [(4, 128), (8, 32)])
+def test_values_near_the_end_of_bf16(nq, Hq, bits, group):
+    """Values of V up to 2^117: forty tokens of nearly the same weight."""
+    cache, slots = make([40, 33], 0, 16, 2, 128, bits, group, BF16)
+    v = torch.randn((2, 73, 256), generator=torch.Generator("cuda").manual_seed(4), device="cuda").clamp(-2, 2)
+    k = torch.randn((2, 73, 256), generator=torch.Generator("cuda").manual_seed(5), device="cuda") * 0.1
+    cache.write(k.to(BF16), (v.double() * 2.0 ** 116).to(BF16), slots=slots, offsets=torch.tensor([0, 40, 73], dtype=torch.int32, device="cuda"))
+    q, out, lse = attend(cache, slots, nq=nq, Hq=Hq)
+    cache.check()
+    check(cache, q, out, lse, slots, 1, 128 ** -0.5)
