@@ -139,6 +139,9 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
     // What the sums of q are multiplied by: at most 128 2^15 2^-8 lies within fp16; bf16 ones are at once in the units of the
     // codes' part, so that a low value of 2^127 does not take the product past fp32.
     constexpr float kSumUnit = kHalf ? 0x1p-8f : 0x1p-24f;
+    // Octaves that a weight may rise above the maximum that the sums go by.  Times low values they have to stay within fp32:
+    // fp16's are below 2^16, bf16's may have any size.
+    constexpr float kClimb = kHalf ? 60.f : 16.f;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (s_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t sm = s_addr(smem);
@@ -459,7 +462,7 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                             for (uint32_t g = 0; g < NG; g++) pv[h][g] = 0;
                 }
                 // Weights are 2^{s fq - m}.  m and F stay while no operand can exceed 2^15, by a lane's largest weight, scale
-                // and F, and no weight 2^60 (V may be zero, its scales too).  Otherwise m becomes the maximum of a column that
+                // and F, and no weight 2^kClimb (V may be zero, its scales too).  Otherwise m becomes the maximum of a column that
                 // did exceed it and F such that its largest operand lies in [2^4, 2^5), and O is scaled along: eleven octaves
                 // go by before the next time.
                 float widest = 0.f, x_most = -INFINITY;
@@ -469,7 +472,7 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                 for (uint32_t n = 0; n < kN; n++)
 #pragma unroll
                     for (uint32_t j = 0; j < 2; j++) x_most = fmaxf(x_most, fmaf(fmaxf(s[n][j], s[n][2 + j]), fq[n][j], -m[n][j]));
-                if (__builtin_expect(__any_sync(kFull, !(ex2(x_most) * widest <= 32768.f) || x_most > 60.f), 0)) {
+                if (__builtin_expect(__any_sync(kFull, !(ex2(x_most) * widest <= 32768.f) || x_most > kClimb), 0)) {
 #pragma unroll
                     for (uint32_t g = 0; g < NG; g++) most[g] = 0.f;
 #pragma unroll
@@ -484,7 +487,7 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
                             const float top = fmaxf(m[n][j], mx), z = top == -INFINITY ? 0.f : top;
                             const float fc = m[n][j] == top ? 1.f : ex2(m[n][j] - top), wt[2] = {ex2(y[0] - z), ex2(y[1] - z)};
                             float v[NG];  // the largest weights times scales
-                            bool move = m[n][j] == -INFINITY ? mx != -INFINITY : mx > m[n][j] + 60.f;
+                            bool move = m[n][j] == -INFINITY ? mx != -INFINITY : mx > m[n][j] + kClimb;
 #pragma unroll
                             for (uint32_t g = 0; g < NG; g++) {
                                 v[g] = 0.f;

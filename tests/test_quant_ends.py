@@ -121,3 +121,21 @@ def test_values_near_the_end_of_bf16(nq, Hq, bits, group):
     q, out, lse = attend(cache, slots, nq=nq, Hq=Hq)
     cache.check()
     check(cache, q, out, lse, slots, 1, 128 ** -0.5)
+
+
+@gpu
+@pytest.mark.parametrize("nq", [1, 3])
+def test_scores_that_rise_over_large_constant_values(nq):
+    """bf16: groups whose channels are all 2^90 (scale 0) while the scores climb by hundreds of octaves."""
+    n = 640
+    cache, slots = make([n, n], 0, 16, 1, 128, group=32, dtype=BF16)
+    t = torch.arange(n, device="cuda")
+    k = torch.cat([t, n - t]).float()[:, None].expand(-1, 128) * 0.5
+    v = torch.full((2 * n, 128), 2.0 ** 90, device="cuda")
+    v[:, 32:64] = 1.5
+    cache.write(*(x.to(BF16).expand(2, -1, -1) for x in (k, v)), slots=slots)
+    by = torch.tensor([1, 2, -1, 0, 0.25, 0.125, -0.5, 0.01], device="cuda").to(BF16)
+    q = by[:, None].expand(2, nq, 8, 128).contiguous()
+    q, out, lse = attend(cache, slots, nq=nq, q=q, scale=0.03125)
+    cache.check()
+    check(cache, q, out, lse, slots, 1, 0.03125)
