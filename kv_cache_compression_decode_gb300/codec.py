@@ -134,6 +134,19 @@ EXPORTS = ("cg_status_string", "cg_status_from_flags", "cg_encode_bounds", "cg_e
 _lib = None
 
 
+def _packed(struct) -> type:
+    """The type of an argument that is a reference to `struct`, or its bytes
+    (packing a call's arguments is quicker than building the structure)."""
+    size, pointer = ct.sizeof(struct), ct.POINTER(struct).from_param
+
+    class Packed:
+        @staticmethod
+        def from_param(x):
+            return x if type(x) is bytes and len(x) == size else pointer(x)
+
+    return Packed
+
+
 def lib() -> ct.CDLL:
     """Load libcg.so (building it first if its sources are newer)."""
     global _lib
@@ -168,14 +181,13 @@ def lib() -> ct.CDLL:
         L.cg_pages_fork.argtypes = [PG, P, P, P, U32, P, ct.c_size_t, P, P]
         L.cg_pages_free.argtypes = [PG, P, U32, P, P]
         L.cg_pages_compact.argtypes = [PG, P, P, ct.c_size_t, P, P]
-        L.cg_attend_ws_bytes.argtypes = [PG, P, SZ]  # a cg_attention, or its bytes
-        L.cg_attend.argtypes = [PG, P, P, ct.c_size_t, P, P]
-        QF = ct.POINTER(cg_quant)
+        AT, QF, QR = _packed(cg_attention), ct.POINTER(cg_quant), _packed(cg_token_rows)
+        L.cg_attend_ws_bytes.argtypes = [PG, AT, SZ]
+        L.cg_attend.argtypes = [PG, AT, P, ct.c_size_t, P, P]
         L.cg_quant_row.argtypes = [QF, ct.POINTER(U32)]
-        # cg_pages, cg_quant, then cg_token_rows or cg_attention: references, addresses or bytes
-        L.cg_quant_write.argtypes = L.cg_quant_read.argtypes = [P, P, P, P, P]
-        L.cg_quant_attend_ws_bytes.argtypes = [P, P, P, SZ]
-        L.cg_quant_attend.argtypes = [P, P, P, P, ct.c_size_t, P, P]
+        L.cg_quant_write.argtypes = L.cg_quant_read.argtypes = [PG, QF, QR, P, P]
+        L.cg_quant_attend_ws_bytes.argtypes = [PG, QF, AT, SZ]
+        L.cg_quant_attend.argtypes = [PG, QF, AT, P, ct.c_size_t, P, P]
         L.cg_cache_source.argtypes = [P, ct.POINTER(ct.c_int), ct.POINTER(ct.c_void_p)]
         for name in EXPORTS:
             if name not in ("cg_status_string",):
