@@ -255,10 +255,13 @@ class PagedCache:
             raise ValueError("layer, shared_slot and shared_blocks are not negative")
         if R == 0:
             return out
-        a = _pack_attention(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else 0,
-                            _ids(slots, d, "slots") if slots is not None else 0, self._dtype, R, nq, hq,
-                            self._kv_heads(hd), hd, layer, shared_slot, shared_blocks, *qs[:3], *os_[:3],
-                            scale if scale is not None else 1.0 / math.sqrt(hd) if hd else 0.0)
+        try:
+            a = _pack_attention(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else 0,
+                                _ids(slots, d, "slots") if slots is not None else 0, self._dtype, R, nq, hq,
+                                self._kv_heads(hd), hd, layer, shared_slot, shared_blocks, *qs[:3], *os_[:3],
+                                scale if scale is not None else 1.0 / math.sqrt(hd) if hd else 0.0)
+        except struct.error:  # a number that its field cannot hold: refused as those that the library refuses
+            _check(codec.CG_ERR_INVALID_ARG, "attend")
         key = (R, nq, hq, hd, self._shared_key(shared_blocks))
         ws_bytes = self._attn.get(key)
         if ws_bytes is None:
@@ -365,7 +368,10 @@ class QuantCache(PagedCache):
             n = m
         if layer < 0 or (slots is None and n > self._n_slots):
             raise ValueError("layer is negative, or there are more sequences than slots")
-        return _pack_rows(k.data_ptr(), v.data_ptr(), s, o, b, n, n_rows, layer, n_layers, k0, k1, v0, v1)
+        try:
+            return _pack_rows(k.data_ptr(), v.data_ptr(), s, o, b, n, n_rows, layer, n_layers, k0, k1, v0, v1)
+        except struct.error:  # as in attend
+            _check(codec.CG_ERR_INVALID_ARG, "write, read")
 
     def write(self, k: torch.Tensor, v: torch.Tensor, layer: int = 0, slots: Optional[torch.Tensor] = None,
               offsets: Optional[torch.Tensor] = None, start: Optional[torch.Tensor] = None, stream=None) -> None:

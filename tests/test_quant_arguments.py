@@ -1,9 +1,12 @@
 """What the calls on paged caches make of wrong arguments, on the host."""
 import ctypes as ct
+import math
 
 import pytest
+import torch
 
 from kv_cache_compression_decode_gb300 import codec as C
+from kv_cache_compression_decode_gb300 import paged
 from tests.test_quant_cache import fake_attention, fake_format, fake_pages, fake_rows, quant_pages
 
 
@@ -31,3 +34,27 @@ def test_an_object_of_another_type_is_refused_before_the_call():
                      (ct.addressof(p), ref(f), ref(r)), (ref(p), ct.addressof(f), ref(r)), (ref(p), ref(f), ct.addressof(r))):
             with pytest.raises(ct.ArgumentError):
                 call(*args, 0, None)
+
+
+def host_caches():
+    i32 = dict(dtype=torch.int32)
+    state = lambda: (torch.zeros((3, 4), **i32), torch.zeros(3, **i32), torch.zeros(5, **i32), torch.zeros(1, **i32))  # noqa: E731
+    return (paged.PagedCache(torch.zeros((2, 5, 2, 16, 64), dtype=torch.float16), *state()),
+            paged.QuantCache(torch.zeros((2, 5, 2, 16, 24), dtype=torch.int16), *state(), n_kv_heads=1, head_dim=64))
+
+
+@pytest.mark.parametrize("kw", [dict(scale=1e39), dict(scale=-1e300), dict(scale=math.inf), dict(scale=math.nan), dict(layer=1 << 32),
+                                dict(layer=2), dict(shared_blocks=1 << 32), dict(shared_blocks=5), dict(shared_blocks=1, shared_slot=1 << 40)])
+def test_numbers_that_their_type_cannot_hold_are_invalid_arguments(kw):
+    """As those that the library refuses: neither wrapped into range nor an exception of another kind."""
+    q = torch.zeros((2, 1, 4, 64), dtype=torch.float16)
+    for cache in host_caches():
+        with pytest.raises(C.CodecError) as e:
+            cache.attend(kw.get("layer", 0), q, **{k: v for k, v in kw.items() if k != "layer"})
+        assert e.value.code == C.CG_ERR_INVALID_ARG
+    if "layer" in kw and kw["layer"] > 2:
+        x = torch.zeros((1, 3, 64), dtype=torch.float16)
+        for call in (lambda: cache.write(x, x, **kw), lambda: cache.read(out=(x, x), **kw)):
+            with pytest.raises(C.CodecError) as e:
+                call()
+            assert e.value.code == C.CG_ERR_INVALID_ARG
