@@ -267,6 +267,8 @@ class PagedCache:
         if ws_bytes is None:
             n = ct.c_size_t()
             _check(self._attend_ws_bytes(a, n), "attend (workspace)")
+            if len(self._attn) >= 1024:  # shapes come and go: those still in use are soon there again
+                self._attn.clear()
             ws_bytes = self._attn[key] = n.value
         handle = self._stream(stream)
         ws = self._workspace(ws_bytes, stream, handle)

@@ -58,3 +58,20 @@ def test_numbers_that_their_type_cannot_hold_are_invalid_arguments(kw):
             with pytest.raises(C.CodecError) as e:
                 call()
             assert e.value.code == C.CG_ERR_INVALID_ARG
+
+
+def test_a_server_of_many_contexts_keeps_few_sizes(monkeypatch):
+    """A quantised cache asks for its workspace by the number of shared blocks; what it remembers of that is bounded."""
+    i32 = dict(dtype=torch.int32)
+    cache = paged.QuantCache(torch.zeros((1, 5, 2, 16, 24), dtype=torch.int16), torch.zeros((3, 9000), **i32), torch.zeros(3, **i32),
+                             torch.zeros(5, **i32), torch.zeros(1, **i32), n_kv_heads=1, head_dim=64)
+    given = []
+    monkeypatch.setattr(cache, "_stream", lambda stream: 0)
+    monkeypatch.setattr(cache, "_workspace", lambda n, stream, handle: given.append(n))
+    monkeypatch.setattr(cache, "_attend", lambda a, ws, handle: C.CG_OK)
+    q = torch.zeros((300, 1, 4, 64), dtype=torch.float16)[:3]
+    for _ in range(2):
+        for shared in range(1, 9000, 2):
+            cache.attend(0, q, shared_blocks=shared)
+        assert len(cache._attn) <= 1024
+    assert given[:4500] == given[4500:] and len(given) == 9000
