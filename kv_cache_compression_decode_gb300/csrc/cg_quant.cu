@@ -307,10 +307,11 @@ __global__ void __launch_bounds__(kThreads) k_quant_read(const Job b) {
                         fma2(x[k], x[k + 1], x[k], x[k + 1], s, low);
                     }
                 }
-                // some may lie past the type's range (bf16's past fp32's, too: 15 scales can be 2^128)
-                if (fmaf(kTop, s, low) > Y::kMost && s < INFINITY && low < INFINITY)
+                if (fmaf(kTop, s, low) > Y::kMost) {  // some may lie past the type's range (bf16's past fp32's, too)
+                    const float most = s < INFINITY && low < INFINITY ? Y::kMost : INFINITY;
 #pragma unroll
-                    for (uint32_t k = 0; k < 8; k++) x[k] = fminf(x[k], Y::kMost);
+                    for (uint32_t k = 0; k < 8; k++) x[k] = x[k] > Y::kMost ? most : x[k];
+                }
                 uint4 o;
                 typename Y::T2 *h = reinterpret_cast<typename Y::T2 *>(&o);
 #pragma unroll
