@@ -595,8 +595,10 @@ cg_status cg_attend(const cg_pages *p, const cg_attention *a, void *ws, size_t w
  *           is the low half of its byte
  *   pairs   16-bit scale, 16-bit low value for each of the C / group groups
  *   padding up to a multiple of 16 bytes, never used
- * A code q stands for low + q * scale.  The row's width in 16-bit words
- * (cg_quant_row) is the C of the cg_pages that describes the pool.
+ * A code q stands for low + q * scale.  A scale is not negative, and a pair is
+ * finite or holds a NaN: so cg_quant_write stores them, and a pool that is
+ * filled otherwise keeps to it.  The row's width in 16-bit words (cg_quant_row)
+ * is the C of the cg_pages that describes the pool.
  */
 typedef struct {
     uint32_t dtype;                /* CG_FP16 or CG_BF16: scales and low values, and every tensor of the calls */
@@ -657,13 +659,24 @@ cg_status cg_quant_read(const cg_pages *p, const cg_quant *f, const cg_token_row
  * are those of cg_attend, with K and V the values that the codes stand for and
  * a->dtype, n_kv_heads and head_dim those of the format.
  * Codes go into the products as they are, exactly; q is exact but for parts
- * below 2^-25 of a query's largest channel, and scales, low values, softmax
- * sums and outputs are applied and accumulated in fp32.  The product of a
- * weight and a scale is rounded to 11 bits for the product with V's codes (one
- * above 2^-28 of the largest is not lost).  The shared blocks of many query
- * rows (more than 64 to a KV head, and a few thousand tokens) are first read
- * into the workspace, as cg_quant_read would read them, with bf16 in two parts
- * for K, and attended to as by cg_attend.
+ * below 2^-25 of a query's largest channel (its sums over a group, which meet
+ * the low values, have 22 bits with fp16 and 24 with bf16), and scales, low
+ * values, softmax sums and outputs are applied and accumulated in fp32.  The
+ * product of a weight and a scale is rounded to 11 bits for the product with
+ * V's codes (one above 2^-28 of the largest is not lost).  Weights stand up to
+ * 2^16 above the largest's 1 (2^60 with fp16, whose values are small), so that
+ * a sequence's tokens times its largest |V| stay below 2^111; |scale| times a
+ * query's largest channel stays below 2^116.
+ * The shared blocks of many query rows are first read into the workspace, as
+ * cg_quant_read would read them, with bf16 in two parts for K, and attended to
+ * as by cg_attend.  With g = n_queries * n_q_heads / n_kv_heads query rows of a
+ * request and w twice the number of ranges of 8 rows that all requests' make
+ * (where g > 8, three times that of ranges of 16), this is so where w > 16 and
+ * (w - 16) * shared_blocks * block_tokens * n_kv_heads > 160000: from 65 rows
+ * on, of many tokens.  Values are then rounded to 16 bits (bf16's K to 16 bits
+ * of mantissa) and weights as by cg_attend: over 16384 shared tokens an fp16
+ * sequence's lse of 15 is off by 9e-5 at most, and by 9e-6 against the codes.  So
+ * what a sequence's answer is off by depends on the batch around it.
  * ws: device, 256-byte aligned, cg_quant_attend_ws_bytes bytes, which depend
  * on shared_blocks too.
  */
