@@ -1235,7 +1235,7 @@ extern "C" cg_status cg_attend(const cg_pages *p, const cg_attention *at, void *
         a.qs[k] = at->q_stride[k];
         a.os[k] = at->out_stride[k];
     }
-    a.scale2 = fmaxf(fabsf(at->scale) * kLog2e, 0x1p-149f);  // not 0: masked scores are -inf before the product
+    a.scale2 = fminf(fmaxf(fabsf(at->scale) * kLog2e, 0x1p-149f), 0x1p127f);  // not 0: masked scores are -inf before the product; nor infinite
     a.flip = at->scale < 0.f ? 0x80008000u : 0u;
     a.status = dev_status;
     uint8_t *w = static_cast<uint8_t *>(ws);

@@ -105,7 +105,7 @@ extern "C" cg_status cg_quant_attend(const cg_pages *p, const cg_quant *f, const
     q.stage = (uint32_t)round_up(2 * (q.tile + q.ptile), 1024);
     const uint32_t room = kStageBytes / q.stage;
     q.n_stages = room < kQuantMaxStages ? room : kQuantMaxStages;
-    q.scale2 = fmaxf(fabsf(at->scale) * 1.4426950408889634f, 0x1p-149f);  // not 0: masked scores are -inf before the product
+    q.scale2 = fminf(fmaxf(fabsf(at->scale) * 1.4426950408889634f, 0x1p-149f), 0x1p127f);  // not 0: masked scores are -inf before the product; nor infinite
 
     const uint16_t *layer = p->pool + at->layer * p->layer_stride;
     const uint32_t box = bt < pl.tt ? bt : pl.tt, codes = quant_codes(f);

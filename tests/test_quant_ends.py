@@ -139,3 +139,23 @@ def test_scores_that_rise_over_large_constant_values(nq):
     q, out, lse = attend(cache, slots, nq=nq, q=q, scale=0.03125)
     cache.check()
     check(cache, q, out, lse, slots, 1, 0.03125)
+
+
+@gpu
+@pytest.mark.parametrize("R", [2, 40])
+@pytest.mark.parametrize("bits", [16, 4])
+def test_queries_of_zero_at_the_largest_scale(bits, R):
+    """A scale of 3e38 times log2 e lies past fp32: a score of zero is zero all the same, and the answer the mean."""
+    P, Hkv, D, scale = 96, 2, 64, 3e38
+    lens = [P + 1 + 7 * r % 50 for r in range(R)]
+    q = torch.zeros((R, 1, 8, D), dtype=BF16, device="cuda")
+    if bits == 16:
+        cache, slots = plain.make(lens, P // 16, 16, Hkv, D, BF16)
+        _, out, lse = plain.attend(cache, slots, Hq=8, D=D, q=q, scale=scale, shared_blocks=P // 16)
+        cache.check()
+        plain.check(cache, q, out, lse, slots, 1, scale)
+    else:
+        cache, slots = make(lens, P // 16, 16, Hkv, D, dtype=BF16)
+        _, out, lse = attend(cache, slots, q=q, scale=scale, shared_blocks=P // 16)
+        cache.check()
+        check(cache, q, out, lse, slots, 1, scale, P // 16)
