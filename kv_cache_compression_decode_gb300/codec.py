@@ -196,6 +196,15 @@ def lib() -> ct.CDLL:
     return _lib
 
 
+def packed_call(name: str, n_args: int):
+    """A libcg function that takes addresses and packed bytes for its pointers
+    as they are: for a caller that has made them from checked arguments, whom
+    looking at their types again would cost 0.3 us a call."""
+    f = lib()[name]  # a function object of its own: lib().<name> goes on checking
+    f.argtypes, f.restype = [ct.c_void_p] * n_args, ct.c_int
+    return f
+
+
 class CodecError(RuntimeError):
     def __init__(self, code: int, what: str):
         super().__init__(f"{what}: {cg_status_string(code)} ({code})")

@@ -312,9 +312,11 @@ class QuantCache(PagedCache):
                              f"not {pool.shape[4]}")
         super().__init__(pool, tables, lens, refs, status)
         self._format = self._format_of(n_kv_heads, head_dim, bits, group, dtype)
-        self._format_ref = ct.byref(self._format)
+        self._at, self._format_at = ct.addressof(self._c), ct.addressof(self._format)
+        self._cg_write, self._cg_read = codec.packed_call("cg_quant_write", 5), codec.packed_call("cg_quant_read", 5)
+        self._cg_attend = codec.packed_call("cg_quant_attend", 7)
         self._type, self._dtype, self._heads, self._hd = dtype, _DTYPES[dtype], n_kv_heads, head_dim
-        self._channels, self._n_slots, self._lib = n_kv_heads * head_dim, tables.shape[0], lib()
+        self._channels, self._n_slots = n_kv_heads * head_dim, tables.shape[0]
 
     @staticmethod
     def _format_of(n_kv_heads, head_dim, bits, group, dtype) -> cg_quant:
@@ -383,7 +385,7 @@ class QuantCache(PagedCache):
         (default: an even share); they are its last tokens (advance `lens` first)
         or those from start[r] on."""
         rows = self._rows(k, v, layer, slots, offsets, start)
-        _check(self._lib.cg_quant_write(self._ref, self._format_ref, rows, self._status_ptr, self._stream(stream)),
+        _check(self._cg_write(self._at, self._format_at, rows, self._status_ptr, self._stream(stream)),
                "cg_quant_write")
 
     def read(self, layer: int = 0, n_layers: Optional[int] = None, rows: Optional[int] = None,
@@ -403,7 +405,7 @@ class QuantCache(PagedCache):
         if (n_layers is not None and k.shape[0] != n_layers) or (rows is not None and k.shape[1] != rows):
             raise ValueError("read: n_layers and rows are those of out")
         r = self._rows(k, v, layer, slots, offsets, start)
-        _check(self._lib.cg_quant_read(self._ref, self._format_ref, r, self._status_ptr, self._stream(stream)),
+        _check(self._cg_read(self._at, self._format_at, r, self._status_ptr, self._stream(stream)),
                "cg_quant_read")
         return k, v
 
@@ -438,8 +440,7 @@ class QuantCache(PagedCache):
         return shared_blocks
 
     def _attend_ws_bytes(self, a, n) -> int:
-        return lib().cg_quant_attend_ws_bytes(self._ref, self._format_ref, a, ct.byref(n))
+        return lib().cg_quant_attend_ws_bytes(self._ref, ct.byref(self._format), a, ct.byref(n))
 
     def _attend(self, a, ws, handle) -> int:
-        return lib().cg_quant_attend(self._ref, self._format_ref, a, ws.data_ptr(), ws.numel(), self._status_ptr,
-                                     handle)
+        return self._cg_attend(self._at, self._format_at, a, ws.data_ptr(), ws.numel(), self._status_ptr, handle)
